@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool nx = kl >= nk2;
     k_ld = (nx ? kl - nk2 : kl) * BK;
     TileRows t = tile_at(nx);
-    if (!nx && kl >= nk) t.rows_a = t.rows_w = 0;
+    if ((nx ? kl - nk2 : kl) >= nk) t.rows_a = t.rows_w = 0;
     return t;
   };
   // LDS layout: A scales of buffers 0, 1 | W scales 0, 1 | A tiles 0, 1 | W tiles 0, 1
@@ -1121,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     __syncthreads();   // it is in buffer nb; nobody reads buffer cb any more
     const int kl = kt + 2;
     const bool nx = kl >= nk2;                   // stage kl - nk2 of the next tile
-    const bool live = nx || kl < nk;
+    const bool live = (nx ? kl - nk2 : kl) < nk;
     const int k_ld = (nx ? kl - nk2 : kl) * BK;
     TileRows lt = nx ? nxt : cur;
     if (!live) lt.rows_a = lt.rows_w = 0;        // a padding stage: empty ranges
