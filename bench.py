@@ -406,7 +406,7 @@ def main():
     Dg = torch.empty((Mg, Ng), dtype=torch.bfloat16, device=dev)
     L.Dg = Dg
     flops = 2 * Mg * Ng * Kg
-    msrc = _src_hash("gemm.hip", "fp4_device.h")
+    msrc = _src_hash("gemm.hip", "gemm_kernels.h", "fp4_device.h")
 
     def gemm_nv(i):
         st = lib.fp4_scaled_gemm(fp4.FP4_NVFP4, P(aq_nv), P(as_nv), P(ga_nv), P(wq_nv), P(wsc_nv),

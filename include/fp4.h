@@ -50,7 +50,8 @@ typedef enum {
   FP4_ERR_ALIAS = 8      /* an output aliases an input the call reads         */
 } fp4_status;
 
-/* FP4_E4M3 (one FP8 E4M3 byte per value) is valid only as fp4_scaled_gemm's output. */
+/* FP4_E4M3 (one FP8 E4M3 byte per value) is valid only as an output of
+ * fp4_scaled_gemm and fp4_grouped_gemm. */
 typedef enum { FP4_F32 = 0, FP4_BF16 = 1, FP4_E4M3 = 2 } fp4_dtype;
 typedef enum { FP4_NVFP4 = 0, FP4_MXFP4 = 1 } fp4_format;
 typedef enum { FP4_RNE = 0, FP4_SR = 1 } fp4_rounding;
@@ -346,6 +347,187 @@ fp4_status hadamard_quantize_mx(const void* x, fp4_dtype xt, int64_t rows, int64
  */
 fp4_status hadamard_rotate(const void* x, fp4_dtype xt, int64_t rows, int64_t cols, int group,
                            void* y, fp4_dtype yt, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Expert layers: routing, rows to the experts and back, and the FP4 products
+ * with bias, activation and residual in their epilogue.
+ * ------------------------------------------------------------------------ */
+
+/* act(x): x, max(x, 0), x sigmoid(x), x Phi(x) (the normal distribution's Phi),
+ * 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))). */
+typedef enum {
+  FP4_ACT_NONE = 0,
+  FP4_ACT_RELU = 1,
+  FP4_ACT_SILU = 2,
+  FP4_ACT_GELU = 3,
+  FP4_ACT_GELU_TANH = 4
+} fp4_activation;
+
+/* How logits become scores. */
+typedef enum { FP4_SCORE_SOFTMAX = 0, FP4_SCORE_SIGMOID = 1 } fp4_score;
+
+#define FP4_MOE_MAX_EXPERTS 1024
+#define FP4_MOE_MAX_TOPK 16
+#define FP4_MOE_MAX_GROUPS 64
+#define FP4_MOE_MAX_TOKENS (1LL << 26)   /* T; T * top_k <= 2^30 */
+
+/*
+ * fp4_scaled_gemm_fused -- fp4_scaled_gemm with an epilogue:
+ *   z = g_d * ((g_a s_a . A) @ (g_b s_b . W)^T) + bias           [M, N], float32
+ *   D = act(z) + residual                                        [M, N]
+ *   gated: D[:, j] = act(z[:, 2j]) * z[:, 2j + 1] + residual     [M, N / 2]
+ * (W's rows hold gate and up projections alternately, laid out once).
+ * Everything is float32 until the one rounding to D's type.
+ *   activation      fp4_activation;  gated 0 or 1 (N even)
+ *   bias            [N] FP4_F32 / FP4_BF16 (bias_type), or NULL
+ *   residual        [M, No], No = N or N / 2, FP4_F32 / FP4_BF16, or NULL; may be
+ *                   D itself when the types are equal (in place), and must not
+ *                   overlap D otherwise
+ *   preact          out [M, N] FP4_F32 / FP4_BF16: z, for fp4_epilogue_backward,
+ *                   or NULL
+ *   D               out [M, No], FP4_F32 or FP4_BF16
+ * Formats, K, size limits and alignment as fp4_scaled_gemm; bias, residual,
+ * preact and D aligned to their element.  M == 0 or N == 0 is a no-op; K == 0
+ * takes z = bias (operands are not read).  Type arguments of NULL pointers are
+ * not looked at.
+ */
+fp4_status fp4_scaled_gemm_fused(fp4_format fmt, const uint8_t* A, const uint8_t* a_scales,
+                                 const float* g_a, const uint8_t* W, const uint8_t* w_scales,
+                                 const float* g_b, float g_d, int64_t M, int64_t N, int64_t K,
+                                 fp4_activation activation, int gated, const void* bias,
+                                 fp4_dtype bias_type, const void* residual, fp4_dtype residual_type,
+                                 void* preact, fp4_dtype preact_type, void* D, fp4_dtype dt,
+                                 hipStream_t stream);
+
+/*
+ * fp4_grouped_gemm_fused -- fp4_grouped_gemm with the epilogue of
+ * fp4_scaled_gemm_fused; bias is [num_groups, N] (each group its own).
+ * Rows from offsets[num_groups] on (slots that moe_dispatch dropped) are written
+ * as zeros in D and preact, so that a quantizer of the whole tensor sees no
+ * stale values.
+ */
+fp4_status fp4_grouped_gemm_fused(fp4_format fmt, const uint8_t* A, const uint8_t* a_scales,
+                                  const float* g_a, const uint8_t* W, const uint8_t* w_scales,
+                                  const float* g_b, float g_d, int64_t num_groups,
+                                  const int32_t* offsets, int64_t M_total, int64_t N, int64_t K,
+                                  fp4_activation activation, int gated, const void* bias,
+                                  fp4_dtype bias_type, const void* residual,
+                                  fp4_dtype residual_type, void* preact, fp4_dtype preact_type,
+                                  void* D, fp4_dtype dt, hipStream_t stream);
+
+/*
+ * fp4_epilogue_backward -- gradients of the epilogue above:
+ *   dz = dD * act'(z);  gated: dz[:, 2j] = dD[:, j] z[:, 2j + 1] act'(z[:, 2j]),
+ *   dz[:, 2j + 1] = dD[:, j] act(z[:, 2j]);  dbias[n] = sum over rows of dz[:, n].
+ * (The residual's gradient is dD; relu'(0) = 0.)  Sums are float32 in a fixed
+ * order, of dz before its rounding.
+ *   dD [M, No], z [M, N] (the forward's preact), dz out [M, N]: FP4_F32 / FP4_BF16
+ *   offsets    device int32 [num_groups + 1] as fp4_grouped_gemm: dbias is
+ *              [num_groups, N], a group's rows summed (none: zeros), and rows
+ *              outside every group get no dz; or NULL with num_groups == 1
+ *   dbias      out float32, or NULL (then the workspace may be NULL)
+ *   workspace  >= fp4_epilogue_backward_workspace_bytes bytes, 4-byte aligned
+ * M, N <= FP4_GEMM_MAX_MN, num_groups <= FP4_GROUPED_MAX_GROUPS.  N == 0 is a
+ * no-op; M == 0 writes dbias = 0.
+ */
+size_t fp4_epilogue_backward_workspace_bytes(int64_t num_groups, int64_t M, int64_t N);
+fp4_status fp4_epilogue_backward(const void* dD, fp4_dtype dD_type, const void* z, fp4_dtype z_type,
+                                 int64_t num_groups, const int32_t* offsets, int64_t M, int64_t N,
+                                 fp4_activation activation, int gated, void* dz, fp4_dtype dz_type,
+                                 float* dbias, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/*
+ * moe_route -- the experts of each token and their weights.
+ * Per token, over its E logits l (NaN and -inf mask the expert, +inf counts as
+ * the largest finite float32):
+ *   score      s = softmax(l) over the unmasked experts, or sigmoid(l)
+ *   selection  v = s + bias[e] where a bias is given (it only selects); else s
+ *              where group_top is 2 and num_groups > 1; else l itself (the same
+ *              order as s, without its rounding).  v = -inf or NaN masks too.
+ *   groups     the E experts in num_groups groups of E / num_groups in a row; a
+ *              group's score is its largest v (group_top 1) or the sum of its two
+ *              largest (2; one where only one is unmasked); the experts of all but
+ *              the top_groups best groups are masked
+ *   ids        the top_k largest v, largest first; -1 once no expert is left
+ *   weights    scale * s, renormalized: scale * s / (sum of the selected s), 0
+ *              when that sum is 0 in float32; 0 where the id is -1
+ * Equal v and equal group scores go to the lower index.
+ *   logits   [T, E] FP4_F32 / FP4_BF16;  bias device float32 [E] or NULL
+ *   ids      out int32 [T, top_k];  weights out float32 [T, top_k]
+ * 1 <= E <= FP4_MOE_MAX_EXPERTS, 1 <= top_k <= min(E, FP4_MOE_MAX_TOPK), E a
+ * multiple of num_groups <= FP4_MOE_MAX_GROUPS, 1 <= top_groups <= num_groups,
+ * group_top 1 or 2, T <= FP4_MOE_MAX_TOKENS, T * top_k <= 2^30.  Pointers aligned
+ * to their element.  T == 0 is a no-op.
+ */
+fp4_status moe_route(const void* logits, fp4_dtype lt, int64_t T, int64_t E, int top_k,
+                     fp4_score score, const float* bias, int num_groups, int top_groups,
+                     int group_top, int renormalize, float scale, int32_t* ids, float* weights,
+                     hipStream_t stream);
+
+/*
+ * moe_route_backward -- d_logits [T, E] of the weights' gradient d_weights
+ * [T, top_k] for moe_route's ids (the selection itself has no gradient, nor has
+ * the bias).  Ids outside [0, E) contribute nothing; masked experts get 0.
+ * Every entry of d_logits (FP4_F32 / FP4_BF16) is written.
+ */
+fp4_status moe_route_backward(const float* d_weights, const void* logits, fp4_dtype lt,
+                              const int32_t* ids, int64_t T, int64_t E, int top_k, fp4_score score,
+                              int renormalize, float scale, void* d_logits, fp4_dtype dt,
+                              hipStream_t stream);
+
+/*
+ * moe_dispatch -- tokens sorted by expert and quantized, as fp4_grouped_gemm
+ * reads them.  Slot s = t * top_k + j is token t's j-th expert ids[t][j].
+ *   offsets    out int32 [E + 1]: expert e has the rows offsets[e] .. offsets[e+1];
+ *              inside an expert rows keep the order of their slots
+ *   slot_rows  out int32 [T, top_k]: the row of each slot, -1 for an id outside
+ *              [0, E) (a dropped slot: it has no row)
+ *   row_slots  out int32 [T * top_k]: the slot of each row, -1 from offsets[E] on
+ *   q, scales  out [T * top_k, H / 2] codes and [T * top_k, H / bs] scale bytes:
+ *              row r holds token row_slots[r] / top_k of x quantized exactly as
+ *              nvfp4_quantize (one tensor scale over all of x [T, H]) or
+ *              mxfp4_quantize does; rows from offsets[E] on are zeros
+ *   global_amax, amax_given, global_scale   as nvfp4_quantize (NVFP4); NULL, 0 and
+ *              NULL for MXFP4
+ *   workspace  >= moe_dispatch_workspace_bytes bytes, 4-byte aligned
+ * x [T, H] FP4_F32 / FP4_BF16, H % 32 == 0; q 16-byte aligned, the others to their
+ * element; global_amax and global_scale distinct.  E, top_k, T limits as
+ * moe_route (top_k may exceed E).  T == 0 writes offsets = 0 (and amax 0,
+ * tensor scale 1).
+ */
+size_t moe_dispatch_workspace_bytes(int64_t T, int64_t top_k, int64_t E);
+fp4_status moe_dispatch(fp4_format fmt, const void* x, fp4_dtype xt, int64_t T, int64_t H,
+                        const int32_t* ids, int top_k, int64_t E, uint8_t* q, uint8_t* scales,
+                        float* global_amax, int amax_given, float* global_scale, int32_t* offsets,
+                        int32_t* slot_rows, int32_t* row_slots, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_combine -- y[t] = sum over j of weights[t][j] * rows[slot_rows[t][j]]
+ * (+ residual[t]), summed in float32 in the order of j and rounded once.
+ * Slots whose row is outside [0, M) add nothing.
+ *   rows [M, H], residual [T, H] or NULL, y out [T, H]: FP4_F32 / FP4_BF16
+ *   weights [T, top_k] float32;  slot_rows [T, top_k]
+ * 1 <= top_k <= FP4_MOE_MAX_TOPK; T limits as moe_route; H <= FP4_GEMM_MAX_MN;
+ * T * ceil(H / 256) < 2^31.  residual may be y itself (equal types).  Pointers
+ * aligned to their element.  T == 0 or H == 0 is a no-op.
+ */
+fp4_status moe_combine(const void* rows, fp4_dtype rt, int64_t M, int64_t H, const float* weights,
+                       const int32_t* slot_rows, int64_t T, int top_k, const void* residual,
+                       fp4_dtype residual_type, void* y, fp4_dtype yt, hipStream_t stream);
+
+/*
+ * moe_combine_backward -- gradients of moe_combine for moe_dispatch's rows
+ * (M = T * top_k):  d_rows[slot_rows[t][j]] = weights[t][j] * dy[t], zeros for rows
+ * of no slot (row_slots[r] < 0);  d_weights[t][j] = <dy[t], rows[slot_rows[t][j]]>
+ * in float32, 0 for a dropped slot.  (The residual's gradient is dy.)
+ * A row belongs to at most one slot.
+ */
+fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows, fp4_dtype rt,
+                                const float* weights, const int32_t* slot_rows,
+                                const int32_t* row_slots, int64_t T, int top_k, int64_t H,
+                                void* d_rows, fp4_dtype drt, float* d_weights, hipStream_t stream);
 
 /* Human-readable text of a status (static storage). */
 const char* fp4_status_string(fp4_status s);

@@ -422,3 +422,253 @@ fp4_status hadamard_rotate(const void* x, fp4_dtype xt, int64_t rows, int64_t co
 }
 
 }  // extern "C"
+
+namespace {
+
+bool valid_act(fp4_activation a) { return a >= FP4_ACT_NONE && a <= FP4_ACT_GELU_TANH; }
+// a pointer aligned to its FP4_F32 / FP4_BF16 element
+bool elem_aligned(const void* p, fp4_dtype t) { return aligned(p, t == FP4_BF16 ? 2 : 4); }
+
+// Shared front half of the fused GEMMs (ngroups 0: dense).
+fp4_status fused_gemm(fp4_format fmt, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
+                      const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
+                      int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                      fp4_activation activation, int gated, const void* bias, fp4_dtype bias_type,
+                      const void* residual, fp4_dtype residual_type, void* preact,
+                      fp4_dtype preact_type, void* D, fp4_dtype dt, hipStream_t stream,
+                      const char* name) {
+  if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return FP4_ERR_DTYPE;
+  if (!valid_dtype(dt) || !valid_act(activation)) return FP4_ERR_DTYPE;
+  if (bias != nullptr && !valid_dtype(bias_type)) return FP4_ERR_DTYPE;
+  if (residual != nullptr && !valid_dtype(residual_type)) return FP4_ERR_DTYPE;
+  if (preact != nullptr && !valid_dtype(preact_type)) return FP4_ERR_DTYPE;
+  if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return FP4_ERR_SHAPE;
+  if (M > FP4_GEMM_MAX_MN || N > FP4_GEMM_MAX_MN || K > FP4_GEMM_MAX_K) return FP4_ERR_SHAPE;
+  if (gated != 0 && (gated != 1 || N % 2 != 0)) return FP4_ERR_SHAPE;
+  if (((M + 255) / 256 + ngroups) * ((N + 255) / 256) >= (int64_t)1 << 31) return FP4_ERR_SHAPE;
+  if (fmt == FP4_MXFP4 && (g_a != nullptr || g_b != nullptr)) return FP4_ERR_DTYPE;
+  if (M == 0 || N == 0) return FP4_OK;
+  if (D == nullptr || (ngroups > 0 && offsets == nullptr)) return FP4_ERR_NULL;
+  if (K > 0 && (A == nullptr || a_scales == nullptr || W == nullptr || w_scales == nullptr))
+    return FP4_ERR_NULL;
+  if (K > 0 && fmt == FP4_NVFP4 && (g_a == nullptr || g_b == nullptr)) return FP4_ERR_NULL;
+  if (!aligned(A, 16) || !aligned(W, 16) || !elem_aligned(D, dt) || !aligned(offsets, 4) ||
+      !aligned(g_a, 4) || !aligned(g_b, 4))
+    return FP4_ERR_ALIGN;
+  if ((bias && !elem_aligned(bias, bias_type)) || (residual && !elem_aligned(residual, residual_type)) ||
+      (preact && !elem_aligned(preact, preact_type)))
+    return FP4_ERR_ALIGN;
+  // in place only element for element
+  if (residual == D && residual_type != dt) return FP4_ERR_ALIAS;
+  if (preact == D || (preact != nullptr && preact == residual)) return FP4_ERR_ALIAS;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  const fp4impl::Epilogue ep{activation, gated, bias, bias_type == FP4_BF16, residual,
+                             residual_type == FP4_BF16, preact, preact_type == FP4_BF16};
+  FP4_TRY_LAUNCH(fp4impl::launch_fused_gemm(fmt == FP4_MXFP4, A, a_scales, g_a, W, w_scales, g_b, g_d,
+                                            ngroups, offsets, M, N, K, ep, D, dt == FP4_BF16, stream),
+                 name);
+  return FP4_OK;
+}
+
+// Sizes shared by the routing and dispatch calls.
+bool bad_slots(int64_t T, int64_t E, int top_k) {
+  return T < 0 || T > FP4_MOE_MAX_TOKENS || E < 1 || E > FP4_MOE_MAX_EXPERTS || top_k < 1 ||
+         top_k > FP4_MOE_MAX_TOPK || T * top_k > (int64_t)1 << 30;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4_status fp4_scaled_gemm_fused(fp4_format fmt, const uint8_t* A, const uint8_t* a_scales,
+                                 const float* g_a, const uint8_t* W, const uint8_t* w_scales,
+                                 const float* g_b, float g_d, int64_t M, int64_t N, int64_t K,
+                                 fp4_activation activation, int gated, const void* bias,
+                                 fp4_dtype bias_type, const void* residual, fp4_dtype residual_type,
+                                 void* preact, fp4_dtype preact_type, void* D, fp4_dtype dt,
+                                 hipStream_t stream) {
+  return fused_gemm(fmt, A, a_scales, g_a, W, w_scales, g_b, g_d, 0, nullptr, M, N, K, activation, gated,
+                    bias, bias_type, residual, residual_type, preact, preact_type, D, dt, stream,
+                    "fp4_scaled_gemm_fused");
+}
+
+fp4_status fp4_grouped_gemm_fused(fp4_format fmt, const uint8_t* A, const uint8_t* a_scales,
+                                  const float* g_a, const uint8_t* W, const uint8_t* w_scales,
+                                  const float* g_b, float g_d, int64_t num_groups,
+                                  const int32_t* offsets, int64_t M_total, int64_t N, int64_t K,
+                                  fp4_activation activation, int gated, const void* bias,
+                                  fp4_dtype bias_type, const void* residual,
+                                  fp4_dtype residual_type, void* preact, fp4_dtype preact_type,
+                                  void* D, fp4_dtype dt, hipStream_t stream) {
+  if (num_groups < 1 || num_groups > FP4_GROUPED_MAX_GROUPS) return FP4_ERR_SHAPE;
+  return fused_gemm(fmt, A, a_scales, g_a, W, w_scales, g_b, g_d, num_groups, offsets, M_total, N, K,
+                    activation, gated, bias, bias_type, residual, residual_type, preact, preact_type, D,
+                    dt, stream, "fp4_grouped_gemm_fused");
+}
+
+size_t fp4_epilogue_backward_workspace_bytes(int64_t num_groups, int64_t M, int64_t N) {
+  if (num_groups < 1 || M < 0 || N < 1) return 0;
+  return fp4impl::epilogue_grad_workspace_bytes(num_groups, M, N);
+}
+
+fp4_status fp4_epilogue_backward(const void* dD, fp4_dtype dD_type, const void* z, fp4_dtype z_type,
+                                 int64_t num_groups, const int32_t* offsets, int64_t M, int64_t N,
+                                 fp4_activation activation, int gated, void* dz, fp4_dtype dz_type,
+                                 float* dbias, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+  if (!valid_dtype(dD_type) || !valid_dtype(z_type) || !valid_dtype(dz_type) || !valid_act(activation))
+    return FP4_ERR_DTYPE;
+  if (M < 0 || N < 0 || M > FP4_GEMM_MAX_MN || N > FP4_GEMM_MAX_MN) return FP4_ERR_SHAPE;
+  if (gated != 0 && (gated != 1 || N % 2 != 0)) return FP4_ERR_SHAPE;
+  if (num_groups < 1 || num_groups > FP4_GROUPED_MAX_GROUPS || (offsets == nullptr && num_groups != 1))
+    return FP4_ERR_SHAPE;
+  if (N == 0 || (M == 0 && dbias == nullptr)) return FP4_OK;
+  if (M > 0 && (dD == nullptr || z == nullptr || dz == nullptr)) return FP4_ERR_NULL;
+  if (dbias != nullptr &&
+      (workspace == nullptr || workspace_bytes < fp4_epilogue_backward_workspace_bytes(num_groups, M, N)))
+    return FP4_ERR_WORKSPACE;
+  if (!elem_aligned(dD, dD_type) || !elem_aligned(z, z_type) || !elem_aligned(dz, dz_type) ||
+      !aligned(dbias, 4) || !aligned(offsets, 4) || (dbias != nullptr && !aligned(workspace, 4)))
+    return FP4_ERR_ALIGN;
+  if (M > 0 && (dz == dD || (dz == z && dz_type != z_type))) return FP4_ERR_ALIAS;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  FP4_TRY_LAUNCH(fp4impl::launch_epilogue_grad(dD, dD_type == FP4_BF16, z, z_type == FP4_BF16, num_groups,
+                                               offsets, M, N, activation, gated != 0, dz,
+                                               dz_type == FP4_BF16, dbias, workspace, stream),
+                 "fp4_epilogue_backward");
+  return FP4_OK;
+}
+
+fp4_status moe_route(const void* logits, fp4_dtype lt, int64_t T, int64_t E, int top_k,
+                     fp4_score score, const float* bias, int num_groups, int top_groups,
+                     int group_top, int renormalize, float scale, int32_t* ids, float* weights,
+                     hipStream_t stream) {
+  if (!valid_dtype(lt) || (score != FP4_SCORE_SOFTMAX && score != FP4_SCORE_SIGMOID)) return FP4_ERR_DTYPE;
+  if (bad_slots(T, E, top_k) || top_k > E) return FP4_ERR_SHAPE;
+  if (num_groups < 1 || num_groups > FP4_MOE_MAX_GROUPS || E % num_groups != 0 || top_groups < 1 ||
+      top_groups > num_groups || group_top < 1 || group_top > 2)
+    return FP4_ERR_SHAPE;
+  if (T == 0) return FP4_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return FP4_ERR_NULL;
+  if (!elem_aligned(logits, lt) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return FP4_ERR_ALIGN;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  const fp4impl::RouteProblem p{logits, lt == FP4_BF16, T, E, top_k, score == FP4_SCORE_SIGMOID,
+                                renormalize != 0, scale};
+  FP4_TRY_LAUNCH(fp4impl::launch_route(p, bias, num_groups, top_groups, group_top, ids, weights, stream),
+                 "moe_route");
+  return FP4_OK;
+}
+
+fp4_status moe_route_backward(const float* d_weights, const void* logits, fp4_dtype lt,
+                              const int32_t* ids, int64_t T, int64_t E, int top_k, fp4_score score,
+                              int renormalize, float scale, void* d_logits, fp4_dtype dt,
+                              hipStream_t stream) {
+  if (!valid_dtype(lt) || !valid_dtype(dt) || (score != FP4_SCORE_SOFTMAX && score != FP4_SCORE_SIGMOID))
+    return FP4_ERR_DTYPE;
+  if (bad_slots(T, E, top_k) || top_k > E) return FP4_ERR_SHAPE;
+  if (T == 0) return FP4_OK;
+  if (d_weights == nullptr || logits == nullptr || ids == nullptr || d_logits == nullptr)
+    return FP4_ERR_NULL;
+  if (!aligned(d_weights, 4) || !elem_aligned(logits, lt) || !aligned(ids, 4) || !elem_aligned(d_logits, dt))
+    return FP4_ERR_ALIGN;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  const fp4impl::RouteProblem p{logits, lt == FP4_BF16, T, E, top_k, score == FP4_SCORE_SIGMOID,
+                                renormalize != 0, scale};
+  FP4_TRY_LAUNCH(fp4impl::launch_route_grad(p, d_weights, ids, d_logits, dt == FP4_BF16, stream),
+                 "moe_route_backward");
+  return FP4_OK;
+}
+
+size_t moe_dispatch_workspace_bytes(int64_t T, int64_t top_k, int64_t E) {
+  if (T < 0 || T > FP4_MOE_MAX_TOKENS || top_k < 1 || top_k > FP4_MOE_MAX_TOPK || E < 1 ||
+      E > FP4_MOE_MAX_EXPERTS)
+    return 0;
+  return fp4impl::dispatch_workspace_bytes(T * top_k, E);
+}
+
+fp4_status moe_dispatch(fp4_format fmt, const void* x, fp4_dtype xt, int64_t T, int64_t H,
+                        const int32_t* ids, int top_k, int64_t E, uint8_t* q, uint8_t* scales,
+                        float* global_amax, int amax_given, float* global_scale, int32_t* offsets,
+                        int32_t* slot_rows, int32_t* row_slots, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  if (fmt != FP4_NVFP4 && fmt != FP4_MXFP4) return FP4_ERR_DTYPE;
+  if (!valid_dtype(xt)) return FP4_ERR_DTYPE;
+  if (bad_slots(T, E, top_k) || H < 0 || H > FP4_GEMM_MAX_K || H % 32 != 0) return FP4_ERR_SHAPE;
+  const bool mx = fmt == FP4_MXFP4;
+  if (mx && (global_amax != nullptr || global_scale != nullptr || amax_given)) return FP4_ERR_DTYPE;
+  if (offsets == nullptr) return FP4_ERR_NULL;
+  if (!mx && (global_scale == nullptr || (amax_given && global_amax == nullptr))) return FP4_ERR_NULL;
+  if (T > 0) {
+    if (ids == nullptr || slot_rows == nullptr || row_slots == nullptr) return FP4_ERR_NULL;
+    if (H > 0 && (x == nullptr || q == nullptr || scales == nullptr)) return FP4_ERR_NULL;
+    if (workspace == nullptr || workspace_bytes < moe_dispatch_workspace_bytes(T, top_k, E))
+      return FP4_ERR_WORKSPACE;
+  }
+  if (!elem_aligned(x, xt) || !aligned(q, 16) || !aligned(ids, 4) || !aligned(offsets, 4) ||
+      !aligned(slot_rows, 4) || !aligned(row_slots, 4) || !aligned(workspace, 4) ||
+      !aligned(global_amax, 4) || !aligned(global_scale, 4))
+    return FP4_ERR_ALIGN;
+  // one workgroup writes *global_scale while the others still read *global_amax
+  if (global_amax != nullptr && global_amax == global_scale) return FP4_ERR_ALIAS;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  const fp4impl::DispatchProblem p{mx, x, xt == FP4_BF16, T, H, ids, top_k, E, q, scales,
+                                   amax_given ? global_amax : nullptr,
+                                   amax_given ? nullptr : global_amax, global_scale, offsets, slot_rows,
+                                   row_slots, workspace};
+  FP4_TRY_LAUNCH(fp4impl::launch_dispatch(p, stream), "moe_dispatch");
+  return FP4_OK;
+}
+
+fp4_status moe_combine(const void* rows, fp4_dtype rt, int64_t M, int64_t H, const float* weights,
+                       const int32_t* slot_rows, int64_t T, int top_k, const void* residual,
+                       fp4_dtype residual_type, void* y, fp4_dtype yt, hipStream_t stream) {
+  if (!valid_dtype(rt) || !valid_dtype(yt) || (residual != nullptr && !valid_dtype(residual_type)))
+    return FP4_ERR_DTYPE;
+  if (bad_slots(T, 1, top_k) || M < 0 || M > FP4_GEMM_MAX_MN || H < 0 || H > FP4_GEMM_MAX_MN)
+    return FP4_ERR_SHAPE;
+  if (T * ((H + 255) / 256) >= (int64_t)1 << 31) return FP4_ERR_SHAPE;
+  if (T == 0 || H == 0) return FP4_OK;
+  if ((M > 0 && rows == nullptr) || weights == nullptr || slot_rows == nullptr || y == nullptr)
+    return FP4_ERR_NULL;
+  if (!elem_aligned(rows, rt) || !aligned(weights, 4) || !aligned(slot_rows, 4) || !elem_aligned(y, yt) ||
+      (residual != nullptr && !elem_aligned(residual, residual_type)))
+    return FP4_ERR_ALIGN;
+  if (rows == y || (residual == y && residual_type != yt)) return FP4_ERR_ALIAS;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  FP4_TRY_LAUNCH(fp4impl::launch_combine(rows, rt == FP4_BF16, M, H, weights, slot_rows, T, top_k,
+                                         residual, residual_type == FP4_BF16, y, yt == FP4_BF16, stream),
+                 "moe_combine");
+  return FP4_OK;
+}
+
+fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows, fp4_dtype rt,
+                                const float* weights, const int32_t* slot_rows,
+                                const int32_t* row_slots, int64_t T, int top_k, int64_t H,
+                                void* d_rows, fp4_dtype drt, float* d_weights, hipStream_t stream) {
+  if (!valid_dtype(dyt) || !valid_dtype(rt) || !valid_dtype(drt)) return FP4_ERR_DTYPE;
+  if (bad_slots(T, 1, top_k) || H < 0 || H > FP4_GEMM_MAX_MN) return FP4_ERR_SHAPE;
+  if (T == 0) return FP4_OK;
+  if (weights == nullptr || slot_rows == nullptr || row_slots == nullptr || d_weights == nullptr)
+    return FP4_ERR_NULL;
+  if (H > 0 && (dy == nullptr || rows == nullptr || d_rows == nullptr)) return FP4_ERR_NULL;
+  if (!elem_aligned(dy, dyt) || !elem_aligned(rows, rt) || !elem_aligned(d_rows, drt) ||
+      !aligned(weights, 4) || !aligned(slot_rows, 4) || !aligned(row_slots, 4) || !aligned(d_weights, 4))
+    return FP4_ERR_ALIGN;
+  if (H > 0 && (d_rows == dy || d_rows == rows)) return FP4_ERR_ALIAS;
+  fp4_status st = check_arch();
+  if (st != FP4_OK) return st;
+  FP4_TRY_LAUNCH(fp4impl::launch_combine_grad(dy, dyt == FP4_BF16, rows, rt == FP4_BF16, T * top_k, H,
+                                              weights, slot_rows, row_slots, T, top_k, d_rows,
+                                              drt == FP4_BF16, d_weights, stream),
+                 "moe_combine_backward");
+  return FP4_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,175 @@
+// Backward pass of the fused epilogues: dz from dD and the pre-activations, and
+// the bias gradient (column sums of dz, per group in the grouped form).
+//
+//   D = act(z) + residual          dz = dD act'(z)
+//   D = act(g) u + residual        dg = dD u act'(g),  du = dD act(g)   (z: g, u alternate)
+//
+// The residual's gradient is dD itself.
+#include "epilogue.h"
+#include "fp4_internal.h"
+
+using namespace fp4dev;
+
+namespace {
+
+struct GradArgs {
+  const void* dD;
+  const void* z;
+  void* dz;
+  float* partials;            // [groups * splits][N], or NULL: no bias gradient
+  const int32_t* offsets;     // grouped, else NULL
+  int dD_bf16, z_bf16, dz_bf16;
+  int64_t M;
+  int N, groups, splits, gated, activation, col_wgs;
+};
+
+constexpr int kGradThreads = 256;
+constexpr int kGradWaves = kGradThreads / 64;
+
+// Values [c, c + V) of row `row` (zeros past N in the scalar form, V 2)
+template <int V>
+__device__ __forceinline__ void load_cols(const void* p, int64_t row, int c, int N, bool bf16, float (&v)[V]) {
+  const int64_t i = row * N + c;
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      const f32x4 x = load4(p, i + 4 * k, bf16);
+      v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = c + k < N ? load1(p, i + k, bf16) : 0.0f;
+  }
+}
+
+// A workgroup takes 64 V columns and one split of a group's rows, its waves
+// every kGradWaves-th row of it, so a lane keeps its columns' sums in registers.
+// Bias partials: the waves' sums added in wave order, one row per split.
+// V 8: 16-byte accesses (N a multiple of 16, aligned pointers); V 2: any size.
+template <int V>
+__global__ void __launch_bounds__(kGradThreads) k_epilogue_grad(GradArgs a) {
+  __shared__ float red[kGradWaves][64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int part = blockIdx.x / a.col_wgs;
+  const int c = ((blockIdx.x - part * a.col_wgs) * 64 + lane) * V;
+  const int e = part / a.splits, s = part - e * a.splits;
+  int64_t lo = 0, hi = a.M;
+  if (a.offsets != nullptr) {
+    lo = min(max((int64_t)a.offsets[e], (int64_t)0), a.M);
+    hi = min(max((int64_t)a.offsets[e + 1], lo), a.M);
+  }
+  const int64_t per = (hi - lo + a.splits - 1) / a.splits;
+  const int64_t r0 = min(lo + s * per, hi), r1 = min(r0 + per, hi);
+  float sum[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum[k] = 0.0f;
+  const int No = a.gated ? a.N / 2 : a.N;
+  if (c < a.N) {
+    with_act(a.activation, [&](auto act) {
+      constexpr int ACT = decltype(act)::value;
+      for (int64_t r = r0 + wave; r < r1; r += kGradWaves) {
+        float z[V], dz[V];
+        load_cols<V>(a.z, r, c, a.N, a.z_bf16, z);
+        if (a.gated) {
+          float d[V / 2];
+          if constexpr (V == 8)
+            load_cols<V / 2>(a.dD, r, c / 2, No, a.dD_bf16, d);
+          else
+            d[0] = load1(a.dD, r * No + c / 2, a.dD_bf16);
+#pragma unroll
+          for (int k = 0; k < V / 2; ++k) {
+            float v, g;
+            act_both<ACT>(z[2 * k], v, g);
+            dz[2 * k] = d[k] * z[2 * k + 1] * g;
+            dz[2 * k + 1] = d[k] * v;
+          }
+        } else {
+          float d[V];
+          load_cols<V>(a.dD, r, c, a.N, a.dD_bf16, d);
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            float v, g;
+            act_both<ACT>(z[k], v, g);
+            dz[k] = d[k] * g;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum[k] += dz[k];
+        if constexpr (V == 8) {
+          store_vec<8>(a.dz, r * a.N + c, a.dz_bf16, dz);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (c + k < a.N) store1(a.dz, r * a.N + c + k, a.dz_bf16, dz[k]);
+        }
+      }
+    });
+  }
+  if (a.partials == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < V; ++k) red[wave][lane * V + k] = sum[k];
+  __syncthreads();
+  const int c0 = (blockIdx.x - part * a.col_wgs) * 64 * V;
+  for (int i = threadIdx.x; i < 64 * V && c0 + i < a.N; i += kGradThreads) {
+    float t = red[0][i];
+#pragma unroll
+    for (int w = 1; w < kGradWaves; ++w) t += red[w][i];
+    a.partials[(int64_t)part * a.N + c0 + i] = t;
+  }
+}
+
+// dbias[e][c] = sum of the splits' partials, in order
+__global__ void __launch_bounds__(kGradThreads)
+    k_bias_grad(const float* __restrict__ partials, int splits, int64_t cols, int N, float* __restrict__ dbias) {
+  const int64_t i = (int64_t)blockIdx.x * kGradThreads + threadIdx.x;
+  if (i >= cols) return;
+  const int64_t e = i / N, c = i - e * N;
+  const float* p = partials + e * splits * N + c;
+  float s = 0.0f;
+  for (int k = 0; k < splits; ++k) s += p[(int64_t)k * N];
+  dbias[i] = s;
+}
+
+// Row splits: enough workgroups to fill the device several times over at the
+// vector form's 512 columns each, at least 64 rows a split.
+int64_t grad_splits(int64_t groups, int64_t M, int64_t N) {
+  const int64_t cols = (N + 511) / 512, want = 4096;
+  const int64_t by_wgs = (want + cols * groups - 1) / (cols * groups);
+  const int64_t by_rows = M / groups / 64;
+  const int64_t s = by_wgs < by_rows ? by_wgs : by_rows;
+  return s < 1 ? 1 : s;
+}
+
+}  // namespace
+
+namespace fp4impl {
+
+size_t epilogue_grad_workspace_bytes(int64_t groups, int64_t M, int64_t N) {
+  return (size_t)(groups * grad_splits(groups, M, N) * N) * 4;
+}
+
+hipError_t launch_epilogue_grad(const void* dD, bool dD_bf16, const void* z, bool z_bf16, int64_t groups,
+                                const int32_t* offsets, int64_t M, int64_t N, int activation, bool gated,
+                                void* dz, bool dz_bf16, float* dbias, void* workspace, hipStream_t stream) {
+  auto ok16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool vec = N % 16 == 0 && ok16(dD) && ok16(z) && ok16(dz);
+  const int64_t splits = grad_splits(groups, M, N);
+  const int64_t per = 64 * (vec ? 8 : 2), col_wgs = (N + per - 1) / per;
+  if (groups * splits * col_wgs >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  float* partials = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
+  const GradArgs a{dD, z, dz, partials, offsets, dD_bf16, z_bf16, dz_bf16, M, (int)N, (int)groups,
+                   (int)splits, gated, activation, (int)col_wgs};
+  const dim3 grid((unsigned)(groups * splits * col_wgs));
+  if (vec)
+    hipLaunchKernelGGL((k_epilogue_grad<8>), grid, dim3(kGradThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_epilogue_grad<2>), grid, dim3(kGradThreads), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || dbias == nullptr) return e;
+  const int64_t cols = groups * N;
+  hipLaunchKernelGGL(k_bias_grad, dim3((unsigned)((cols + kGradThreads - 1) / kGradThreads)),
+                     dim3(kGradThreads), 0, stream, partials, (int)splits, cols, (int)N, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace fp4impl

@@ -124,6 +124,76 @@ hipError_t launch_grouped_gemm(bool mx, const uint8_t* A, const uint8_t* a_scale
                                const float* g_b, float g_d, int64_t ngroups,
                                const int32_t* offsets, int64_t M, int64_t N, int64_t K, void* D,
                                int d_bytes, hipStream_t stream);
+// ---- gemm_fused.hip -------------------------------------------------------
+// Optional parts of a fused epilogue (NULL: absent); *_bf16: 1 bf16, 0 float32.
+struct Epilogue {
+  int activation, gated;
+  const void* bias;
+  int bias_bf16;
+  const void* residual;
+  int residual_bf16;
+  void* preact;
+  int preact_bf16;
+};
+// D = act(alpha A W^T + bias) + residual (gated: act of the even columns times
+// the odd ones).  ngroups > 0: grouped as launch_grouped_gemm, bias [ngroups, N],
+// and the rows from offsets[ngroups] on are zeroed.
+hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
+                             const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
+                             int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                             const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream);
+
+// ---- epilogue_grad.hip ----------------------------------------------------
+size_t epilogue_grad_workspace_bytes(int64_t groups, int64_t M, int64_t N);
+// dz and (dbias != NULL, through the workspace) the bias gradient [groups, N].
+// offsets NULL: one group of all M rows.
+hipError_t launch_epilogue_grad(const void* dD, bool dD_bf16, const void* z, bool z_bf16, int64_t groups,
+                                const int32_t* offsets, int64_t M, int64_t N, int activation, bool gated,
+                                void* dz, bool dz_bf16, float* dbias, void* workspace, hipStream_t stream);
+
+// ---- moe.hip --------------------------------------------------------------
+struct RouteProblem {
+  const void* logits;
+  bool bf16;
+  int64_t T, E;
+  int top_k;
+  bool sigmoid, renorm;
+  float scale;
+};
+hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, int top_groups,
+                        int group_top, int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_route_grad(const RouteProblem& p, const float* dw, const int32_t* ids, void* dl,
+                             bool dl_bf16, hipStream_t stream);
+
+struct DispatchProblem {
+  bool mx;
+  const void* x;
+  bool bf16;
+  int64_t T, H;
+  const int32_t* ids;
+  int top_k;
+  int64_t E;
+  uint8_t* q;
+  uint8_t* scales;
+  const float* amax_in;   // NVFP4: given amax, or NULL (computed, written to amax_out)
+  float* amax_out;
+  float* scale_out;
+  int32_t* offsets;
+  int32_t* slot_rows;
+  int32_t* row_slots;
+  void* workspace;
+};
+size_t dispatch_workspace_bytes(int64_t n, int64_t E);
+hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream);
+
+hipError_t launch_combine(const void* rows, bool rows_bf16, int64_t M, int64_t H, const float* weights,
+                          const int32_t* slot_rows, int64_t T, int top_k, const void* residual,
+                          bool res_bf16, void* y, bool y_bf16, hipStream_t stream);
+hipError_t launch_combine_grad(const void* dy, bool dy_bf16, const void* rows, bool rows_bf16, int64_t M,
+                               int64_t H, const float* weights, const int32_t* slot_rows,
+                               const int32_t* row_slots, int64_t T, int top_k, void* d_rows, bool dr_bf16,
+                               float* d_weights, hipStream_t stream);
+
 // *out = s_global of the tensor amax *amax (one thread).
 hipError_t launch_nv_global_scale(const float* amax, float* out, hipStream_t stream);
 
