@@ -1,0 +1,491 @@
+// Block-scaled FP4 products of few rows (decode), dense and grouped, through the
+// fused epilogue: D = act(alpha A W^T + bias) + residual with at most a few tens
+// of rows per group, where W is read once and everything else is small.
+//
+// Work.  A unit is 16 RT rows of one group against kSlots * S strips of 16 W
+// rows; the units of all groups are numbered in a row (group, row chunk, strips)
+// and each workgroup (one per CU) takes an equal, contiguous part of them, so
+// empty groups cost nothing and full ones spread over the device.  Of the 8
+// waves, KS split K and 8 / KS take different strips; a wave adds its K range
+// for S strips, and the KS partial tiles meet in LDS once per unit (one barrier,
+// buffers alternating by unit), in wave order.
+//
+// A wave's K range goes by pairs of 128-value steps.  W is loaded 8 rows x 128
+// bytes per instruction (full lines) and turned to the MFMA's operand layout
+// through a wave-private XOR-swizzled LDS tile; the loads of the next two pairs
+// are in flight in registers, across units.  A's codes are read from L2 per
+// pair, in the operand layout, and dequantized once for the S strips.
+// NVFP4: both operands to fp16 exactly (E2M1 x E4M3 has 6 significant bits),
+// v_mfma_f32_16x16x32_f16.  MXFP4: codes and E8M0 bytes straight into
+// v_mfma_scale_f32_16x16x128_f8f6f4.  W is the MFMA's first operand, so a lane
+// ends with 4 consecutive columns of one row.
+#include <atomic>
+
+#include "epilogue.h"
+#include "fp4_device.h"
+#include "fp4_internal.h"
+
+using namespace fp4dev;
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kRing = 2;                        // pairs in flight per wave
+constexpr int kGroup = 4;                       // pairs per group of W scale bytes
+constexpr int kBufferWord3 = 0x00020000;        // raw buffer descriptor word 3 (gfx9 family)
+constexpr int kFar = 0x7ffffff0;                // a buffer offset past every range: reads 0
+constexpr int kLoadNT = 2;                      // buffer load cache policy: nontemporal
+
+struct FewArgs {
+  const uint8_t* A;
+  const uint8_t* as;
+  const uint8_t* W;
+  const uint8_t* ws;
+  const float* g_a;
+  const float* g_b;
+  float g_d;
+  int M, N, K, ks;                              // ks: waves that split K (1, 2, 4, 8)
+  const int32_t* offsets;                       // grouped, else NULL
+  int groups;
+  void* D;
+  FusedArgs f;
+};
+
+// SVEC: W's scale rows are 16-byte aligned and K is a multiple of 256; else
+// scale bytes are read two at a time, with those past K as zeros.
+template <bool MX, int RT, int S, bool SVEC, bool OUT_BF16>
+__global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
+  constexpr int kSB = MX ? 8 : 16;              // scale bytes of a row per pair
+  constexpr int kSG = kSB * kGroup;             // of a row per group of pairs
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int r8 = lane >> 3, c8 = lane & 7;
+  const int KS = a.ks, slots = kWaves / KS;
+  const int part = wave % KS, slot = wave / KS;
+  const int N = a.N, K = a.K;
+  const int wrow = K / 2, srow = K / (MX ? 32 : 16);
+  const int strip_rows = 16 * S * slots;        // W rows per unit
+  const int sb_n = (N + strip_rows - 1) / strip_rows;
+  // LDS: transpose tiles [8 waves][2] x 2 KB | W scale groups [8 waves][S][16 rows] x kSG |
+  // partial tiles [2][8 waves][S][RT] x 1 KB
+  uint8_t* tile = lds + wave * 4096;
+  uint8_t* sgl = lds + kWaves * 4096 + wave * (S * 16 * kSG);
+  v4f* red = reinterpret_cast<v4f*>(lds + kWaves * 4096 + kWaves * S * 16 * kSG);
+
+  // ---- this workgroup's units
+  const bool grouped = a.offsets != nullptr;
+  // rows and row chunks of groups c .. c + 63, one per lane
+  auto chunk_of = [&](int c, int& lo, int& n, int& inc) {
+    const int e = c + lane;
+    lo = n = 0;
+    if (e < a.groups) {
+      lo = min(max(a.offsets[e], 0), a.M);
+      n = min(max(a.offsets[e + 1], lo), a.M) - lo;
+    }
+    inc = (n + 16 * RT - 1) / (16 * RT);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(inc, d, 64);
+      if (lane >= d) inc += v;
+    }
+  };
+  int items = (a.M + 16 * RT - 1) / (16 * RT);
+  if (grouped) {
+    items = 0;
+    for (int c = 0; c < a.groups; c += 64) {
+      int lo, n, inc;
+      chunk_of(c, lo, n, inc);
+      items += __shfl(inc, 63, 64);
+    }
+  }
+  const int64_t U = (int64_t)items * sb_n;
+  const int64_t u0 = U * blockIdx.x / gridDim.x, u1 = U * (blockIdx.x + 1) / gridDim.x;
+  const int nu = (int)(u1 - u0);
+  if (nu == 0) return;                          // (the whole workgroup)
+
+  // An item: 16 RT rows of a group.  row0: its first row, rows: how many, e: the
+  // group.  Unit u is item u / sb_n, strips from (u % sb_n) strip_rows on.
+  struct Item {
+    int row0, rows, e;
+  };
+  auto item_of = [&](int it) {
+    Item r{it * 16 * RT, 0, 0};
+    if (!grouped) {
+      r.rows = min(16 * RT, a.M - r.row0);
+      return r;
+    }
+    int base = 0;
+    for (int c = 0; c < a.groups; c += 64) {
+      int lo, n, inc;
+      chunk_of(c, lo, n, inc);
+      const int mine = (n + 16 * RT - 1) / (16 * RT), start = base + inc - mine;
+      const uint64_t hit = __ballot(it >= start && it < start + mine);
+      if (hit) {
+        const int src = __ffsll((unsigned long long)hit) - 1;
+        const int in = (it - __shfl(start, src, 64)) * 16 * RT;
+        r.e = c + src;
+        r.row0 = __shfl(lo, src, 64) + in;
+        r.rows = min(16 * RT, __shfl(n, src, 64) - in);
+        break;
+      }
+      base += __shfl(inc, 63, 64);
+    }
+    r.e = __builtin_amdgcn_readfirstlane(r.e);
+    r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
+    r.rows = __builtin_amdgcn_readfirstlane(r.rows);
+    return r;
+  };
+
+  // ---- this wave's pairs [pbeg, pbeg + E): dealt evenly, the longer parts first
+  const int P = (K + 255) / 256;
+  const int pbase = P / KS, prem = P % KS;
+  const int pbeg = part * pbase + min(part, prem), E = pbase + (part < prem ? 1 : 0);
+
+  // ---- loads.  Through descriptors whose range is the rows that exist: rows
+  // past N or past the item read zeros.  K past the end: only without SVEC,
+  // where W reads run into the next row (finite, against A = 0) or off the range.
+  struct Elem {
+    u32x4 w[S][2];
+    u32x4 x[RT][2];
+    uint32_t xs[RT];
+    uint32_t ws[SVEC ? 1 : S];
+    u32x4 sg[SVEC ? S : 1];                     // W scale bytes of the group that starts here
+  };
+  Elem ring[kRing];
+  const int w_lane = r8 * wrow + 16 * c8;
+
+  int lu = 0, le = 0;                           // next element to load: unit u0 + lu, pair pbeg + le
+  int l_it = -1, l_n0 = 0;
+  Item l_item{0, 0, 0};
+  auto load_unit = [&]() {                      // the unit's item and first W row of this slot
+    const int64_t u = u0 + lu;
+    const int it = (int)(u / sb_n);
+    if (it != l_it) {
+      l_item = item_of(it);
+      l_it = it;
+    }
+    l_n0 = (int)(u - (int64_t)it * sb_n) * strip_rows + slot * 16 * S;
+  };
+  auto load_elem = [&](Elem& el) {
+    // past the last unit: empty ranges (no branch around the loads)
+    const bool live = lu < nu;
+    if (live && le == 0) load_unit();
+    const int p = pbeg + le;
+    const int rows_w = live ? max(0, min(16 * S, N - l_n0)) : 0;
+    const int rows_a = live ? l_item.rows : 0;
+    const int64_t wr0 = (int64_t)l_item.e * N + l_n0;
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.W) + wr0 * wrow, 0, rows_w * wrow, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.ws) + wr0 * srow, 0, rows_w * srow, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.A) + (int64_t)l_item.row0 * wrow, 0, rows_a * wrow, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.as) + (int64_t)l_item.row0 * srow, 0, rows_a * srow, kBufferWord3);
+    if constexpr (SVEC) {
+      if (le % kGroup == 0) {
+        // lane (r16, g): kSG / 4 bytes of row r16 of each strip
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const int off = (16 * s + r16) * srow + (kSG / 4) * g;
+          // (bytes past this wave's last pair are never used)
+          if constexpr (MX) {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, kSB * p, 0);
+            el.sg[s] = u32x4{v.x, v.y, 0, 0};
+          } else {
+            el.sg[s] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, kSB * p, 0);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const int b0 = kSB * p + (kSB / 4) * g;  // first scale byte of this lane's 64 values
+        const int off = (16 * s + r16) * srow + b0;
+        if constexpr (MX) {
+          const uint32_t x0 = __builtin_amdgcn_raw_buffer_load_b8(rs, b0 < srow ? off : kFar, 0, 0);
+          const uint32_t x1 = __builtin_amdgcn_raw_buffer_load_b8(rs, b0 + 1 < srow ? off + 1 : kFar, 0, 0);
+          el.ws[s] = x0 | (x1 << 8);
+        } else {
+          uint32_t v = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, b0 + i < srow ? off + i : kFar, 0, 0) << (8 * i);
+          el.ws[s] = v;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int row = 16 * t + r16;
+      const int k0 = 256 * p + 64 * g;          // this lane's 64 values of the pair
+      el.x[t][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, SVEC || k0 < K ? row * wrow + k0 / 2 : kFar, 0, 0);
+      el.x[t][1] = __builtin_amdgcn_raw_buffer_load_b128(
+          ra, SVEC || k0 + 32 < K ? row * wrow + k0 / 2 + 16 : kFar, 0, 0);
+      const int b0 = kSB * p + (kSB / 4) * g;
+      if constexpr (SVEC) {
+        el.xs[t] = MX ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rsa, row * srow + b0, 0, 0)
+                      : __builtin_amdgcn_raw_buffer_load_b32(rsa, row * srow + b0, 0, 0);
+      } else {
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < kSB / 4; ++i)
+          v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rsa, b0 + i < srow ? row * srow + b0 + i : kFar, 0, 0)
+               << (8 * i);
+        el.xs[t] = v;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      el.w[s][0] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_lane + 16 * s * wrow, 128 * p, kLoadNT);
+      el.w[s][1] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_lane + (16 * s + 8) * wrow, 128 * p, kLoadNT);
+    }
+    if (++le == E) {
+      le = 0;
+      ++lu;
+    }
+  };
+
+  v4f acc[S][RT];
+  auto clear = [&]() {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[s][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+
+  // ---- end of unit u0 + cu: partial tiles to LDS, then outputs by all threads,
+  // two columns each
+  int c_it = -1;
+  Item c_item{0, 0, 0};
+  auto finish = [&](int cu) {
+    v4f* buf = red + (cu & 1) * kWaves * S * RT * 64;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) buf[((wave * S + s) * RT + t) * 64 + lane] = acc[s][t];
+    const int64_t u = u0 + cu;
+    const int it = (int)(u / sb_n);
+    if (it != c_it) {
+      c_item = item_of(it);
+      c_it = it;
+    }
+    const int n0 = (int)(u - (int64_t)it * sb_n) * strip_rows;
+    float alpha = a.g_d;
+    if (!MX) alpha = K > 0 ? ((*a.g_a) * a.g_b[c_item.e]) * a.g_d : 0.0f;
+    __syncthreads();
+    const int pairs = strip_rows / 2;
+    const float* fb = reinterpret_cast<const float*>(buf);
+    for (int i = threadIdx.x; i < c_item.rows * pairs; i += kThreads) {
+      const int m = i / pairs, c = 2 * (i - m * pairs);          // row and first column inside the unit
+      const int n = n0 + c;
+      if (n >= N) continue;
+      const int sl = c / (16 * S), s = (c / 16) % S, q = c & 3, gg = (c & 15) >> 2;
+      // lane (m % 16, gg) element q of tile (s, m / 16) of the slot's waves
+      const int at = (((sl * KS * S + s) * RT + m / 16) * 64 + gg * 16 + (m & 15)) * 4 + q;
+      float z0 = fb[at], z1 = fb[at + 1];
+      for (int k = 1; k < KS; ++k) {
+        z0 += fb[at + k * S * RT * 256];
+        z1 += fb[at + k * S * RT * 256 + 1];
+      }
+      const int64_t row = c_item.row0 + m;
+      const int64_t b0 = (int64_t)c_item.e * N + n;
+      const bool both = n + 1 < N;
+      z0 = fmaf(z0, alpha, a.f.bias != nullptr ? load1(a.f.bias, b0, a.f.bias_bf16) : 0.0f);
+      z1 = fmaf(z1, alpha, a.f.bias != nullptr && both ? load1(a.f.bias, b0 + 1, a.f.bias_bf16) : 0.0f);
+      if (a.f.preact != nullptr) {
+        store1(a.f.preact, row * N + n, a.f.preact_bf16, z0);
+        if (both) store1(a.f.preact, row * N + n + 1, a.f.preact_bf16, z1);
+      }
+      with_act(a.f.activation, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (a.f.gated) {
+          const int64_t o = row * (N / 2) + n / 2;
+          float d = act_value<ACT>(z0) * z1;
+          if (a.f.residual != nullptr) d += load1(a.f.residual, o, a.f.residual_bf16);
+          store1(a.D, o, OUT_BF16, d);
+        } else {
+          const int64_t o = row * N + n;
+          float d0 = act_value<ACT>(z0), d1 = act_value<ACT>(z1);
+          if (a.f.residual != nullptr) d0 += load1(a.f.residual, o, a.f.residual_bf16);
+          if (a.f.residual != nullptr && both) d1 += load1(a.f.residual, o + 1, a.f.residual_bf16);
+          store1(a.D, o, OUT_BF16, d0);
+          if (both) store1(a.D, o + 1, OUT_BF16, d1);
+        }
+      });
+    }
+  };
+
+  // ---- one element: the group's scale bytes to LDS, strip by strip through the
+  // tile, the ring slot refilled once its registers are in LDS
+  const int wsw = (r8 ^ c8) << 4;
+  const int rd = r16 * 128;
+  int cu = 0, ce = 0;                           // element being computed
+  auto elem = [&](Elem& el) {
+    if constexpr (SVEC) {
+      if (ce % kGroup == 0) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if constexpr (MX)
+            *reinterpret_cast<u32x2*>(sgl + (16 * s + r16) * kSG + (kSG / 4) * g) =
+                u32x2{el.sg[s].x, el.sg[s].y};
+          else
+            *reinterpret_cast<u32x4*>(sgl + (16 * s + r16) * kSG + (kSG / 4) * g) = el.sg[s];
+        }
+      }
+    }
+    // A's operand, dequantized once for the S strips
+    u32x4 xc[RT][2];
+    uint32_t xs[RT];
+    v8h xq[MX ? 1 : RT][2][4];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      xc[t][0] = el.x[t][0];
+      xc[t][1] = el.x[t][1];
+      xs[t] = el.xs[t];
+      if constexpr (!MX) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const v2h hp = st ? e4m3_pair_h<true>(xs[t]) : e4m3_pair_h<false>(xs[t]);
+          const v2h h0 = v2h{hp.x, hp.x}, h1 = v2h{hp.y, hp.y};
+          xq[t][st][0] = dq8(xc[t][st].x, h0);
+          xq[t][st][1] = dq8(xc[t][st].y, h0);
+          xq[t][st][2] = dq8(xc[t][st].z, h1);
+          xq[t][st][3] = dq8(xc[t][st].w, h1);
+        }
+      }
+    }
+    uint32_t wsb[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if constexpr (SVEC) {
+        const uint8_t* src = sgl + (16 * s + r16) * kSG + kSB * (ce % kGroup) + (kSB / 4) * g;
+        wsb[s] = MX ? (uint32_t)*reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
+      } else {
+        wsb[s] = el.ws[s];
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      uint8_t* tb = tile + (s & 1) * 2048;
+      *reinterpret_cast<u32x4*>(tb + r8 * 128 + wsw) = el.w[s][0];
+      *reinterpret_cast<u32x4*>(tb + (8 + r8) * 128 + (wsw ^ 64)) = el.w[s][1];
+      if (s == S - 1) load_elem(el);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int c = 2 * g + st;
+        const u32x4 codes = *reinterpret_cast<const u32x4*>(
+            tb + rd + ((c ^ (r16 & 7) ^ ((r16 >> 3) << 2)) << 4));
+        if constexpr (MX) {
+          const v8i wo = {(int)codes.x, (int)codes.y, (int)codes.z, (int)codes.w, 0, 0, 0, 0};
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            const v8i xo = {(int)xc[t][st].x, (int)xc[t][st].y, (int)xc[t][st].z, (int)xc[t][st].w, 0, 0, 0, 0};
+            acc[s][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                wo, xo, acc[s][t], 4, 4, 0, st ? wsb[s] >> 8 : wsb[s], 0, st ? xs[t] >> 8 : xs[t]);
+          }
+        } else {
+          const v2h wp = st ? e4m3_pair_h<true>(wsb[s]) : e4m3_pair_h<false>(wsb[s]);
+          const v2h w0 = v2h{wp.x, wp.x}, w1 = v2h{wp.y, wp.y};
+          const v8h q0 = dq8(codes.x, w0), q1 = dq8(codes.y, w0), q2 = dq8(codes.z, w1), q3 = dq8(codes.w, w1);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q0, xq[t][st][0], acc[s][t], 0, 0, 0);
+            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q1, xq[t][st][1], acc[s][t], 0, 0, 0);
+            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q2, xq[t][st][2], acc[s][t], 0, 0, 0);
+            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q3, xq[t][st][3], acc[s][t], 0, 0, 0);
+          }
+        }
+      }
+    }
+    if (++ce == E) {
+      ce = 0;
+      finish(cu);
+      ++cu;
+      clear();
+    }
+  };
+
+  clear();
+  if (E == 0) {                                 // no pair for this wave: zeros in every unit
+    for (cu = 0; cu < nu; ++cu) finish(cu);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) load_elem(ring[i]);
+  // element j of the wave lives in ring slot j % kRing
+  const int64_t J = (int64_t)nu * E;
+  for (int64_t j = 0; j < J; j += kRing) {
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+      if (j + i < J) elem(ring[i]);
+  }
+}
+
+template <bool MX, int RT, int S, bool SVEC, bool OUT_BF16>
+hipError_t launch_t(const FewArgs& a, hipStream_t stream) {
+  constexpr int kSG = (MX ? 8 : 16) * kGroup;
+  constexpr int lds = kWaves * 4096 + kWaves * S * 16 * kSG + 2 * kWaves * S * RT * 1024;
+  static_assert(lds <= 160 * 1024, "LDS");
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t e = fp4impl::set_lds_limit_once(
+      lds_set, reinterpret_cast<const void*>(&k_few_rows<MX, RT, S, SVEC, OUT_BF16>), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_few_rows<MX, RT, S, SVEC, OUT_BF16>), dim3(fp4impl::num_cus()), dim3(kThreads),
+                     lds, stream, a);
+  return hipGetLastError();
+}
+
+template <bool MX, int RT, int S>
+hipError_t launch_s(const FewArgs& a, bool svec, bool out_bf16, hipStream_t stream) {
+  if (svec) return out_bf16 ? launch_t<MX, RT, S, true, true>(a, stream) : launch_t<MX, RT, S, true, false>(a, stream);
+  return out_bf16 ? launch_t<MX, RT, S, false, true>(a, stream) : launch_t<MX, RT, S, false, false>(a, stream);
+}
+
+template <bool MX>
+hipError_t launch_m(const FewArgs& a, int64_t rows, bool svec, bool out_bf16, hipStream_t stream) {
+  if (rows <= 16) return launch_s<MX, 1, 4>(a, svec, out_bf16, stream);
+  return launch_s<MX, 2, 2>(a, svec, out_bf16, stream);
+}
+
+}  // namespace
+
+namespace fp4impl {
+
+// Average rows of a group up to which W's bytes, read once per 16 or 32 rows,
+// cost less than the 256-row tiles of the tile kernels.
+constexpr int64_t kFewRows = 32;
+
+bool few_rows(int64_t ngroups, int64_t M, int64_t N, int64_t K) {
+  (void)N;
+  return K > 0 && M <= kFewRows * (ngroups > 0 ? ngroups : 1);
+}
+
+hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
+                           const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
+                           int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                           const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream) {
+  const FusedArgs f{ep.bias, ep.residual, ep.preact, ep.bias_bf16, ep.residual_bf16, ep.preact_bf16,
+                    ep.activation, ep.gated, 0};
+  // waves that split K: at least two pairs each, so that the partial tiles'
+  // exchange is small beside the stream
+  const int64_t P = (K + 255) / 256;
+  const int ks = P >= 16 ? 8 : P >= 8 ? 4 : P >= 4 ? 2 : 1;
+  const FewArgs a{A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, ks, offsets,
+                  (int)ngroups, D, f};
+  const bool svec = K % 256 == 0 && (reinterpret_cast<uintptr_t>(a_scales) & 15) == 0 &&
+                    (reinterpret_cast<uintptr_t>(w_scales) & 15) == 0;
+  const int64_t rows = ngroups > 0 ? M / ngroups : M;
+  return mx ? launch_m<true>(a, rows, svec, out_bf16, stream)
+            : launch_m<false>(a, rows, svec, out_bf16, stream);
+}
+
+}  // namespace fp4impl

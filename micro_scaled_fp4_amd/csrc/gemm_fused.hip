@@ -43,32 +43,34 @@ hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales,
                              int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
                              const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream) {
   // buffer ranges cover one 256-row tile of an operand: 256 * K / 2 < 2^31
-  if (M > (1 << 30) || N > (1 << 30) || K >= (1 << 23) || ngroups > (1 << 20))
+  if (M > (1 << 30) || N > (1 << 30) || K >= (1 << 23) || ngroups > (1 << 20) ||
+      ((M + BM - 1) / BM + ngroups) * ((N + BN - 1) / BN) >= (int64_t)1 << 31)
     return hipErrorInvalidValue;
-  FusedArgs f{ep.bias, ep.residual, ep.preact, ep.bias_bf16, ep.residual_bf16, ep.preact_bf16,
-              ep.activation, ep.gated, 0};
-  auto ok16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  f.vec = N % 16 == 0 && ok16(ep.bias) && ok16(ep.residual) && ok16(ep.preact) && ok16(D);
-  if (ngroups > 0) {
-    if (((M + BM - 1) / BM + ngroups) * ((N + BN - 1) / BN) >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  hipError_t e;
+  if (few_rows(ngroups, M, N, K)) {
+    e = launch_few_rows(mx, A, a_scales, g_a, W, w_scales, g_b, g_d, ngroups, offsets, M, N, K, ep, D,
+                        out_bf16, stream);
+  } else {
+    FusedArgs f{ep.bias, ep.residual, ep.preact, ep.bias_bf16, ep.residual_bf16, ep.preact_bf16,
+                ep.activation, ep.gated, 0};
+    auto ok16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    f.vec = N % 16 == 0 && ok16(ep.bias) && ok16(ep.residual) && ok16(ep.preact) && ok16(D);
     const Groups gr{offsets, (int)ngroups};
-    const hipError_t e =
-        mx ? launch_fused_t<true, true>(A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K,
-                                        D, out_bf16, gr, f, stream)
-           : launch_fused_t<false, true>(A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N,
-                                         (int)K, D, out_bf16, gr, f, stream);
-    if (e != hipSuccess) return e;
-    const int64_t No = ep.gated ? N / 2 : N;
-    hipLaunchKernelGGL(k_zero_tail, dim3(64), dim3(256), 0, stream, offsets, (int)ngroups, (int)M,
-                       No * (out_bf16 ? 2 : 4), static_cast<uint8_t*>(D), N * (ep.preact_bf16 ? 2 : 4),
-                       static_cast<uint8_t*>(ep.preact));
-    return hipGetLastError();
+#define FP4_LAUNCH(MXV, GV)                                                                            \
+  launch_fused_t<MXV, GV>(A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, D, out_bf16, \
+                          gr, f, stream)
+    if (ngroups > 0)
+      e = mx ? FP4_LAUNCH(true, true) : FP4_LAUNCH(false, true);
+    else
+      e = mx ? FP4_LAUNCH(true, false) : FP4_LAUNCH(false, false);
+#undef FP4_LAUNCH
   }
-  const Groups gr{nullptr, 0};
-  return mx ? launch_fused_t<true, false>(A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N,
-                                          (int)K, D, out_bf16, gr, f, stream)
-            : launch_fused_t<false, false>(A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N,
-                                           (int)K, D, out_bf16, gr, f, stream);
+  if (e != hipSuccess || ngroups == 0) return e;
+  const int64_t No = ep.gated ? N / 2 : N;
+  hipLaunchKernelGGL(k_zero_tail, dim3(64), dim3(256), 0, stream, offsets, (int)ngroups, (int)M,
+                     No * (out_bf16 ? 2 : 4), static_cast<uint8_t*>(D), N * (ep.preact_bf16 ? 2 : 4),
+                     static_cast<uint8_t*>(ep.preact));
+  return hipGetLastError();
 }
 
 }  // namespace fp4impl
