@@ -186,10 +186,10 @@ __device__ __forceinline__ void add_residual(float (&d)[NV], const ResidualRaw& 
 
 // One lane's 16 columns n .. n + 15 of row `row` (D's row; z = the accumulators
 // times alpha plus bias), whole (vec launches): preact, activation, residual
-// and store.  n is a multiple of 16.
-template <bool OUT_BF16>
+// and store.  n is a multiple of 16.  `used` is called once r has been read.
+template <bool OUT_BF16, typename F>
 __device__ __forceinline__ void finish_piece(float (&z)[16], const FusedArgs& f, const ResidualRaw& r,
-                                             int64_t row, int n, int N, void* D) {
+                                             int64_t row, int n, int N, void* D, F&& used) {
   if (f.preact != nullptr) store_vec<16>(f.preact, row * N + n, f.preact_bf16, z);
   if (f.gated) {
     float d[8];
@@ -197,14 +197,20 @@ __device__ __forceinline__ void finish_piece(float (&z)[16], const FusedArgs& f,
 #pragma unroll
       for (int q = 0; q < 8; ++q) d[q] = act_value<decltype(a)::value>(z[2 * q]) * z[2 * q + 1];
     });
-    if (f.residual != nullptr) add_residual<8>(d, r, f.residual_bf16);
+    if (f.residual != nullptr) {
+      add_residual<8>(d, r, f.residual_bf16);
+      used();
+    }
     store_vec<8>(D, row * (N / 2) + n / 2, OUT_BF16, d);
   } else {
     with_act(f.activation, [&](auto a) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) z[q] = act_value<decltype(a)::value>(z[q]);
     });
-    if (f.residual != nullptr) add_residual<16>(z, r, f.residual_bf16);
+    if (f.residual != nullptr) {
+      add_residual<16>(z, r, f.residual_bf16);
+      used();
+    }
     store_vec<16>(D, row * N + n, OUT_BF16, z);
   }
 }

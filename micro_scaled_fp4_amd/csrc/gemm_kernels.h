@@ -472,7 +472,7 @@ __device__ __forceinline__ void transpose_groups(v4f (&x)[4]) {
 // 64 columns by its 4 lanes: 128 contiguous bytes in bf16) and gate / up pairs
 // meet in a lane.  Rows go one MFMA row tile (16 rows) at a time in a rolled
 // loop (the activation's code exists once, not once per tile), the residual of
-// the next 16 rows loading meanwhile.
+// the next 16 rows loading from where this one's is used up.
 //   row0  D's row of the group's row 0;  m0, n0  the wave's first row (inside
 //   its group, which has m_rows) and column;  bias0  the group's first bias element
 template <bool OUT_BF16, int TN, int TM>
@@ -487,13 +487,11 @@ __device__ __forceinline__ void store_fused(v4f (&acc)[TN][TM], float alpha, con
     float bias[16];
     load_bias(bias, f, bias0, n, N);
     const bool fetch = f.residual != nullptr && f.vec && n < N;
-    ResidualRaw res, nxt;
-    if (fetch && m0 + r16 < m_rows) load_residual(nxt, f, row0 + m0 + r16, n, No);
+    ResidualRaw res;
+    if (fetch && m0 + r16 < m_rows) load_residual(res, f, row0 + m0 + r16, n, No);
 #pragma unroll 1
     for (int j = 0; j < TM; ++j) {
       const int m = m0 + 16 * j + r16;
-      res = nxt;
-      if (fetch && j + 1 < TM && m + 16 < m_rows) load_residual(nxt, f, row0 + m + 16, n, No);
       v4f x[4];
       // (compile-time accumulator indices keep the accumulators in their AGPRs)
       static_for<TM>([&](auto j_c) {
@@ -512,7 +510,9 @@ __device__ __forceinline__ void store_fused(v4f (&acc)[TN][TM], float alpha, con
 #pragma unroll
         for (int q = 0; q < 16; ++q) z[q] = fmaf(x[q >> 2][q & 3], alpha, bias[q]);
         if (f.vec)
-          finish_piece<OUT_BF16>(z, f, res, row0 + m, n, N, D);
+          finish_piece<OUT_BF16>(z, f, res, row0 + m, n, N, D, [&] {
+            if (j + 1 < TM && m + 16 < m_rows) load_residual(res, f, row0 + m + 16, n, No);
+          });
         else
           finish_piece_scalar<OUT_BF16>(z, f, row0 + m, n, N, D);
       }
@@ -884,24 +884,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ra[2][kTM], rw[2][kTN];   // codes of sub-steps u (parity u & 1)
     v8h da[2][kTM], dw[2][kTN];        // fp16 operands of sub-steps u (parity u & 1)
     uint32_t pa[2][kTM], pw[2][kTN];   // scale pairs of k-steps 0 and 1 of a stage
-    read_scales(0, sa0, sw0);
+    // a tile's first operands, from stage 0 in buffer 0
+    auto first_operands = [&]() {
+      read_scales(0, sa0, sw0);
 #pragma unroll
-    for (int i = 0; i < kTM; ++i) {
-      ra[0][i] = raw_dw(tile_a(0), ra0 + 16 * i, 0);
-      ra[1][i] = raw_dw(tile_a(0), ra0 + 16 * i, 1);
-      rw[0][i] = raw_dw(tile_w(0), rw0 + 16 * i, 0);
-      rw[1][i] = raw_dw(tile_w(0), rw0 + 16 * i, 1);
-    }
-    wait_lgkm();
-    static_for<kTM>([&](auto i_c) {
-      constexpr int i = decltype(i_c)::value;
-      pa[0][i] = scale_pair(sa0[i], 0);
-      pw[0][i] = scale_pair(sw0[i], 0);
-      static_for<4>([&](auto k_c) {
-        dq_part(da[0][i], ra[0][i], pa[0][i], k_c, 0);
-        dq_part(dw[0][i], rw[0][i], pw[0][i], k_c, 0);
+      for (int i = 0; i < kTM; ++i) {
+        ra[0][i] = raw_dw(tile_a(0), ra0 + 16 * i, 0);
+        ra[1][i] = raw_dw(tile_a(0), ra0 + 16 * i, 1);
+        rw[0][i] = raw_dw(tile_w(0), rw0 + 16 * i, 0);
+        rw[1][i] = raw_dw(tile_w(0), rw0 + 16 * i, 1);
+      }
+      wait_lgkm();
+      static_for<kTM>([&](auto i_c) {
+        constexpr int i = decltype(i_c)::value;
+        pa[0][i] = scale_pair(sa0[i], 0);
+        pw[0][i] = scale_pair(sw0[i], 0);
+        static_for<4>([&](auto k_c) {
+          dq_part(da[0][i], ra[0][i], pa[0][i], k_c, 0);
+          dq_part(dw[0][i], rw[0][i], pw[0][i], k_c, 0);
+        });
       });
-    });
+    };
+    first_operands();
     // Each MFMA is issued with its share of the other work in a slot of its
     // own (no instruction crosses a slot), so the vector ALU work runs while
     // the MFMA pipe is busy: per MFMA row i, slot j dequantizes dword j % 4 of
@@ -976,7 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         nv_stage(std::integral_constant<int, 1>{}, kt + 1, sa1, sw1, sa0, sw0);
       }
       epilogue(tile_at(false));
-    } while (next_tile());
+      if (!next_tile()) break;
+      // (fused: read again, so that the epilogue has their registers)
+      if constexpr (FUSED) first_operands();
+    } while (true);
   }
 }
 
@@ -1186,12 +1193,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
   __syncthreads();
   uint32_t sa0[4], sw0[2], sa1[4], sw1[2];
   u32x4 fa0[kTM], fw0[kT8N], fa1[kTM], fw1[kT8N];
-  read_scales(0, sa0, sw0);
+  // a tile's first operands, from stage 0 in buffer 0
+  auto first_operands = [&]() {
+    read_scales(0, sa0, sw0);
 #pragma unroll
-  for (int i = 0; i < kTM; ++i) fa0[i] = frag(tile_a(0), ra0 + 16 * i, 2 * g);
+    for (int i = 0; i < kTM; ++i) fa0[i] = frag(tile_a(0), ra0 + 16 * i, 2 * g);
 #pragma unroll
-  for (int i = 0; i < kT8N; ++i) fw0[i] = frag(tile_w(0), rw0 + 16 * i, 2 * g);
-  wait_lgkm();
+    for (int i = 0; i < kT8N; ++i) fw0[i] = frag(tile_w(0), rw0 + 16 * i, 2 * g);
+    wait_lgkm();
+  };
+  first_operands();
   // One stage: buffer CB holds stage kt (scales sa / sw); row i of a k-step
   // also reads A fragments 2i, 2i + 1 and W fragment i of the next k-step (the
   // order the next k-step's first row needs them in).  The loads of stage
@@ -1260,6 +1271,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
         acc[decltype(i_c)::value][decltype(j_c)::value] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
       });
     });
+    // (fused: read again, so that the epilogue has their registers; buffer 0 is not
+    // refilled before the next barrier)
+    if constexpr (FUSED) first_operands();
   }
 }
 
@@ -1290,8 +1304,9 @@ hipError_t launch_t(const uint8_t* A, const uint8_t* as, const uint8_t* W, const
   // MXFP4: the 8-wave kernel (grouped launches: k_gemm, whose group lookup
   // would not fit the 8-wave kernel's 256 registers without spills); NVFP4: k_gemm
   constexpr bool kMx8 = MX && !GROUPED;
-  const void* fn = kMx8 ? reinterpret_cast<const void*>(&k_gemm_mx8<OUT, SCALE_VEC, FUSED>)
-                        : reinterpret_cast<const void*>(&k_gemm<MX, OUT, SCALE_VEC, GROUPED, FUSED>);
+  const void* fn;
+  if constexpr (kMx8) fn = reinterpret_cast<const void*>(&k_gemm_mx8<OUT, SCALE_VEC, FUSED>);
+  else fn = reinterpret_cast<const void*>(&k_gemm<MX, OUT, SCALE_VEC, GROUPED, FUSED>);
   static std::atomic<uint64_t> lds_set{0};   // devices on which this kernel's LDS limit is set
   const hipError_t e = fp4impl::set_lds_limit_once(lds_set, fn, lds);
   if (e != hipSuccess) return e;
