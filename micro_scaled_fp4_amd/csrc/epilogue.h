@@ -14,6 +14,13 @@
 
 namespace fp4dev {
 
+// LDS traffic between the lanes of one wave: LDS operations of a wave complete
+// in order, so only the compiler has to keep them in order.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // values of fp4_activation
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
 
@@ -215,56 +222,68 @@ __device__ __forceinline__ void finish_piece(float (&z)[16], const FusedArgs& f,
   }
 }
 
-// The same one column (gated: one pair of columns) at a time, for sizes and
-// alignments that take no whole pieces: columns [n, n + 16) below N.
+// The same for sizes and alignments that take no whole pieces: a wave's 8 rows
+// of 64 columns, the accumulators in LDS rows of kStripRow floats; a lane takes
+// one column (gated: one pair of columns) of each row, so every access of a row
+// is contiguous across the lanes.  Rows row0 .. row0 + 7 below m_rows (given as
+// their count), columns n0 .. n0 + 63 below N; bias: of the lane's column(s).
+constexpr int kStripRow = 68;                  // 64 columns, rows 4 banks apart
 template <bool OUT_BF16>
-__device__ __forceinline__ void finish_piece_scalar(const float (&z)[16], const FusedArgs& f,
-                                                    int64_t row, int n, int N, void* D) {
+__device__ __forceinline__ void finish_strip(const float* strip, float alpha, const FusedArgs& f, float b0, float b1,
+                                             int64_t row0, int rows, int n0, int N, void* D) {
+  const int lane = threadIdx.x & 63;
+  if (f.gated) {   // 32 pairs, 2 rows at a time
+    const int n = n0 + 2 * (lane & 31);
+    if (n >= N) return;
+    const int64_t No = N / 2;
+    float r[4];
 #pragma unroll
-  for (int q = 0; q < 16; ++q)
-    if (f.preact != nullptr && n + q < N) store1(f.preact, row * N + n + q, f.preact_bf16, z[q]);
-  const int64_t No = f.gated ? N / 2 : N;
-  if (f.gated) {   // N is even: a pair is inside or past it
+    for (int i = 0; i < 4; ++i) {
+      const int m = 2 * i + (lane >> 5);
+      r[i] = f.residual != nullptr && m < rows
+                 ? load1(f.residual, (row0 + m) * No + n / 2, f.residual_bf16) : 0.0f;
+    }
     with_act(f.activation, [&](auto a) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (n + 2 * q < N) {
-          const int64_t o = row * No + n / 2 + q;
-          float d = act_value<decltype(a)::value>(z[2 * q]) * z[2 * q + 1];
-          if (f.residual != nullptr) d += load1(f.residual, o, f.residual_bf16);
-          store1(D, o, OUT_BF16, d);
+      for (int i = 0; i < 4; ++i) {
+        const int m = 2 * i + (lane >> 5);
+        if (m >= rows) continue;
+        const float z0 = fmaf(strip[m * kStripRow + (n - n0)], alpha, b0);
+        const float z1 = fmaf(strip[m * kStripRow + (n - n0) + 1], alpha, b1);
+        if (f.preact != nullptr) {
+          store1(f.preact, (row0 + m) * N + n, f.preact_bf16, z0);
+          store1(f.preact, (row0 + m) * N + n + 1, f.preact_bf16, z1);
         }
+        store1(D, (row0 + m) * No + n / 2, OUT_BF16, act_value<decltype(a)::value>(z0) * z1 + r[i]);
+      }
     });
   } else {
+    const int n = n0 + lane;
+    if (n >= N) return;
+    float r[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+      r[m] = f.residual != nullptr && m < rows
+                 ? load1(f.residual, (row0 + m) * N + n, f.residual_bf16) : 0.0f;
     with_act(f.activation, [&](auto a) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (n + q < N) {
-          const int64_t o = row * No + n + q;
-          float d = act_value<decltype(a)::value>(z[q]);
-          if (f.residual != nullptr) d += load1(f.residual, o, f.residual_bf16);
-          store1(D, o, OUT_BF16, d);
-        }
+      for (int m = 0; m < 8; ++m) {
+        if (m >= rows) continue;
+        const float z = fmaf(strip[m * kStripRow + lane], alpha, b0);
+        if (f.preact != nullptr) store1(f.preact, (row0 + m) * N + n, f.preact_bf16, z);
+        store1(D, (row0 + m) * N + n, OUT_BF16, act_value<decltype(a)::value>(z) + r[m]);
+      }
     });
   }
 }
 
-// Bias of 16 columns (zero past N, or all zero without one).  base: the group's
-// first element.
-__device__ __forceinline__ void load_bias(float (&b)[16], const FusedArgs& f, int64_t base, int n, int N) {
+// Bias of 16 columns from n < N on (vec launches; zero without one).  base: the
+// group's first element.
+__device__ __forceinline__ void load_bias(float (&b)[16], const FusedArgs& f, int64_t base, int n) {
 #pragma unroll
-  for (int q = 0; q < 16; ++q) b[q] = 0.0f;
-  if (f.bias == nullptr || n >= N) return;
-  if (f.vec) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const f32x4 v = load4(f.bias, base + n + 4 * k, f.bias_bf16);
-      b[4 * k] = v.x; b[4 * k + 1] = v.y; b[4 * k + 2] = v.z; b[4 * k + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 16; ++q)
-      if (n + q < N) b[q] = load1(f.bias, base + n + q, f.bias_bf16);
+  for (int k = 0; k < 4; ++k) {
+    const f32x4 v = f.bias != nullptr ? load4(f.bias, base + n + 4 * k, f.bias_bf16) : f32x4{0, 0, 0, 0};
+    b[4 * k] = v.x; b[4 * k + 1] = v.y; b[4 * k + 2] = v.z; b[4 * k + 3] = v.w;
   }
 }
 

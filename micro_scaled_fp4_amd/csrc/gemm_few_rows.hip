@@ -24,6 +24,7 @@
 #include "epilogue.h"
 #include "fp4_device.h"
 #include "fp4_internal.h"
+#include "scale_bytes.h"
 
 using namespace fp4dev;
 
@@ -38,8 +39,6 @@ constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRing = 2;                        // pairs in flight per wave
 constexpr int kGroup = 4;                       // pairs per group of W scale bytes
-constexpr int kBufferWord3 = 0x00020000;        // raw buffer descriptor word 3 (gfx9 family)
-constexpr int kFar = 0x7ffffff0;                // a buffer offset past every range: reads 0
 constexpr int kLoadNT = 2;                      // buffer load cache policy: nontemporal
 
 struct FewArgs {
@@ -57,12 +56,14 @@ struct FewArgs {
   FusedArgs f;
 };
 
-// SVEC: W's scale rows are 16-byte aligned and K is a multiple of 256; else
-// scale bytes are read two at a time, with those past K as zeros.
+// SVEC: scale rows are 16-byte aligned and K is a multiple of 256; else scale
+// bytes are read as the aligned dwords that hold them and shifted into place,
+// with those past K as zeros.
 template <bool MX, int RT, int S, bool SVEC, bool OUT_BF16>
 __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   constexpr int kSB = MX ? 8 : 16;              // scale bytes of a row per pair
   constexpr int kSG = kSB * kGroup;             // of a row per group of pairs
+  constexpr int kGD = kSG / 16;                 // dwords per lane of a group (MXFP4 2, NVFP4 4)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -155,9 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   struct Elem {
     u32x4 w[S][2];
     u32x4 x[RT][2];
-    uint32_t xs[RT];
-    uint32_t ws[SVEC ? 1 : S];
-    u32x4 sg[SVEC ? S : 1];                     // W scale bytes of the group that starts here
+    uint32_t xs[RT][SVEC ? 1 : 2];
+    uint32_t sg[S][kGD + (SVEC ? 0 : 1)];       // W scale bytes of the group that starts here
+    int xs_first, sg_first;                     // !SVEC: row 0's first byte in the ranges
   };
   Elem ring[kRing];
   const int w_lane = r8 * wrow + 16 * c8;
@@ -184,42 +185,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     const int64_t wr0 = (int64_t)l_item.e * N + l_n0;
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(a.W) + wr0 * wrow, 0, rows_w * wrow, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.ws) + wr0 * srow, 0, rows_w * srow, kBufferWord3);
+    const ScaleRange rs = scale_range<SVEC>(a.ws + wr0 * srow, rows_w * srow);
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(a.A) + (int64_t)l_item.row0 * wrow, 0, rows_a * wrow, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.as) + (int64_t)l_item.row0 * srow, 0, rows_a * srow, kBufferWord3);
-    if constexpr (SVEC) {
-      if (le % kGroup == 0) {
-        // lane (r16, g): kSG / 4 bytes of row r16 of each strip
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          const int off = (16 * s + r16) * srow + (kSG / 4) * g;
-          // (bytes past this wave's last pair are never used)
-          if constexpr (MX) {
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, kSB * p, 0);
-            el.sg[s] = u32x4{v.x, v.y, 0, 0};
-          } else {
-            el.sg[s] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, kSB * p, 0);
-          }
-        }
-      }
-    } else {
+    const ScaleRange rsa = scale_range<SVEC>(a.as + (int64_t)l_item.row0 * srow, rows_a * srow);
+    if (le % kGroup == 0) {
+      // lane (r16, g): the scale bytes of pair p + g of row r16 of each strip
+      // (those past this wave's last pair are never used)
+      el.sg_first = rs.lead + kSB * p;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const int b0 = kSB * p + (kSB / 4) * g;  // first scale byte of this lane's 64 values
-        const int off = (16 * s + r16) * srow + b0;
-        if constexpr (MX) {
-          const uint32_t x0 = __builtin_amdgcn_raw_buffer_load_b8(rs, b0 < srow ? off : kFar, 0, 0);
-          const uint32_t x1 = __builtin_amdgcn_raw_buffer_load_b8(rs, b0 + 1 < srow ? off + 1 : kFar, 0, 0);
-          el.ws[s] = x0 | (x1 << 8);
-        } else {
-          uint32_t v = 0;
+        const int off = (16 * s + r16) * srow + kSB * g;
+        if constexpr (!SVEC) {
+          const int at = (off + el.sg_first) & ~3;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, b0 + i < srow ? off + i : kFar, 0, 0) << (8 * i);
-          el.ws[s] = v;
+          for (int i = 0; i <= kGD; ++i) el.sg[s][i] = __builtin_amdgcn_raw_buffer_load_b32(rs.rsrc, at + 4 * i, 0, 0);
+        } else if constexpr (MX) {
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs.rsrc, off, kSB * p, 0);
+          el.sg[s][0] = v.x;
+          el.sg[s][1] = v.y;
+        } else {
+          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs.rsrc, off, kSB * p, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) el.sg[s][i] = v[i];
         }
       }
     }
@@ -227,20 +215,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     for (int t = 0; t < RT; ++t) {
       const int row = 16 * t + r16;
       const int k0 = 256 * p + 64 * g;          // this lane's 64 values of the pair
-      el.x[t][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, SVEC || k0 < K ? row * wrow + k0 / 2 : kFar, 0, 0);
+      el.x[t][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, SVEC || k0 < K ? row * wrow + k0 / 2 : kOutOfRange, 0, 0);
       el.x[t][1] = __builtin_amdgcn_raw_buffer_load_b128(
-          ra, SVEC || k0 + 32 < K ? row * wrow + k0 / 2 + 16 : kFar, 0, 0);
-      const int b0 = kSB * p + (kSB / 4) * g;
-      if constexpr (SVEC) {
-        el.xs[t] = MX ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rsa, row * srow + b0, 0, 0)
-                      : __builtin_amdgcn_raw_buffer_load_b32(rsa, row * srow + b0, 0, 0);
+          ra, SVEC || k0 + 32 < K ? row * wrow + k0 / 2 + 16 : kOutOfRange, 0, 0);
+      const int b0 = row * srow + (kSB / 4) * g;
+      if constexpr (!SVEC) {
+        el.xs_first = rsa.lead + kSB * p;
+        const int at = (b0 + el.xs_first) & ~3;
+        el.xs[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rsa.rsrc, at, 0, 0);
+        el.xs[t][1] = __builtin_amdgcn_raw_buffer_load_b32(rsa.rsrc, at + 4, 0, 0);
+      } else if constexpr (MX) {
+        el.xs[t][0] = __builtin_amdgcn_raw_buffer_load_b16(rsa.rsrc, b0, kSB * p, 0);
       } else {
-        uint32_t v = 0;
-#pragma unroll
-        for (int i = 0; i < kSB / 4; ++i)
-          v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rsa, b0 + i < srow ? row * srow + b0 + i : kFar, 0, 0)
-               << (8 * i);
-        el.xs[t] = v;
+        el.xs[t][0] = __builtin_amdgcn_raw_buffer_load_b32(rsa.rsrc, b0, kSB * p, 0);
       }
     }
 #pragma unroll
@@ -330,16 +317,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   const int rd = r16 * 128;
   int cu = 0, ce = 0;                           // element being computed
   auto elem = [&](Elem& el) {
-    if constexpr (SVEC) {
-      if (ce % kGroup == 0) {
+    if (ce % kGroup == 0) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          if constexpr (MX)
-            *reinterpret_cast<u32x2*>(sgl + (16 * s + r16) * kSG + (kSG / 4) * g) =
-                u32x2{el.sg[s].x, el.sg[s].y};
-          else
-            *reinterpret_cast<u32x4*>(sgl + (16 * s + r16) * kSG + (kSG / 4) * g) = el.sg[s];
+      for (int s = 0; s < S; ++s) {
+        uint32_t v[kGD];
+        if constexpr (SVEC) {
+#pragma unroll
+          for (int i = 0; i < kGD; ++i) v[i] = el.sg[s][i];
+        } else {
+          place_bytes<kGD>(v, el.sg[s], ((16 * s + r16) * srow + kSB * g + el.sg_first) & 3,
+                           srow - kSB * (pbeg + ce + g));
         }
+        uint8_t* dst = sgl + (16 * s + r16) * kSG + kSB * g;
+        if constexpr (MX)
+          *reinterpret_cast<u32x2*>(dst) = u32x2{v[0], v[1]};
+        else
+          *reinterpret_cast<u32x4*>(dst) = u32x4{v[0], v[1], v[2], v[3]};
       }
     }
     // A's operand, dequantized once for the S strips
@@ -350,7 +343,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     for (int t = 0; t < RT; ++t) {
       xc[t][0] = el.x[t][0];
       xc[t][1] = el.x[t][1];
-      xs[t] = el.xs[t];
+      if constexpr (SVEC) {
+        xs[t] = el.xs[t][0];
+      } else {
+        uint32_t v[1];
+        place_bytes<1>(v, el.xs[t], ((16 * t + r16) * srow + (kSB / 4) * g + el.xs_first) & 3,
+                       srow - kSB * (pbeg + ce) - (kSB / 4) * g);
+        xs[t] = v[0];
+      }
       if constexpr (!MX) {
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
@@ -366,12 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     uint32_t wsb[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      if constexpr (SVEC) {
-        const uint8_t* src = sgl + (16 * s + r16) * kSG + kSB * (ce % kGroup) + (kSB / 4) * g;
-        wsb[s] = MX ? (uint32_t)*reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
-      } else {
-        wsb[s] = el.ws[s];
-      }
+      const uint8_t* src = sgl + (16 * s + r16) * kSG + kSB * (ce % kGroup) + (kSB / 4) * g;
+      wsb[s] = MX ? (uint32_t)*reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {

@@ -54,6 +54,7 @@
 #include "epilogue.h"
 #include "fp4_device.h"
 #include "fp4_internal.h"
+#include "scale_bytes.h"
 
 using namespace fp4dev;
 
@@ -79,8 +80,6 @@ constexpr int kTileW = BN * kRowBytes;        // 32 KB
 static_assert(BM == 256 && BN == 256 && kThreads == 256, "stage loads assume 256-row tiles");
 constexpr int kGroupM = 8;
 constexpr int kXcds = 8;
-constexpr int kBufferWord3 = 0x00020000;      // raw buffer descriptor word 3 (gfx9 family)
-constexpr int kOutOfRange = 0x7ffffff0;       // a buffer offset past every range: reads 0
 
 template <bool MX>
 struct Cfg {
@@ -276,42 +275,51 @@ __device__ __forceinline__ void dma_tile(__amdgpu_buffer_rsrc_t src, uint8_t* ti
 
 // One operand's scale bytes of a stage, in registers between their global load
 // and their LDS store: thread t holds row t's 8 (MXFP4) or 16 (NVFP4) bytes.
-template <bool MX>
+// Rows of any length and alignment (!SCALE_VEC) are loaded as the aligned dwords
+// that hold the bytes, one more than the bytes take, and put in place at the
+// store, bytes past the row's end (other rows' or none) as zeros.
+template <bool MX, bool SCALE_VEC>
 struct StageScales {
-  uint32_t s[MX ? 2 : 4];
+  static constexpr int kDw = MX ? 2 : 4;
+  uint32_t s[SCALE_VEC ? kDw : kDw + 1];
+  int first, valid;     // !SCALE_VEC: row 0's first byte in the range, bytes left of a row
 };
 
+// Row `row` of the range, from stage value k0 on.
 template <bool MX, bool SCALE_VEC>
-__device__ __forceinline__ void load_scales(StageScales<MX>& r, __amdgpu_buffer_rsrc_t scales, int nsc,
-                                            int k0) {
-  constexpr int bs = MX ? 32 : 16;
-  constexpr int spr = Cfg<MX>::kScaleRow;
-  const int kb = k0 / bs;
-  const int sr = threadIdx.x;
-  if (SCALE_VEC) {   // K % 256 == 0 and 16-byte aligned scale rows
+__device__ __forceinline__ void load_scales(StageScales<MX, SCALE_VEC>& r, const ScaleRange& scales,
+                                            int row, int nsc, int k0) {
+  const int kb = k0 / (MX ? 32 : 16);
+  if constexpr (SCALE_VEC) {   // K % 256 == 0 and 16-byte aligned scale rows
     if constexpr (MX) {
-      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales, sr * nsc + kb, 0, 0);
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales.rsrc, row * nsc + kb, 0, 0);
       r.s[0] = v.x;
       r.s[1] = v.y;
     } else {
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(scales, sr * nsc + kb, 0, 0);
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(scales.rsrc, row * nsc + kb, 0, 0);
       r.s[0] = v.x;
       r.s[1] = v.y;
       r.s[2] = v.z;
       r.s[3] = v.w;
     }
   } else {
+    r.first = scales.lead + kb;
+    r.valid = nsc - kb;
+    const int at = (row * nsc + r.first) & ~3;
 #pragma unroll
-    for (int q = 0; q < spr / 4; ++q) {
-      uint32_t v = 0;
+    for (int q = 0; q <= StageScales<MX, SCALE_VEC>::kDw; ++q)
+      r.s[q] = __builtin_amdgcn_raw_buffer_load_b32(scales.rsrc, at + 4 * q, 0, 0);
+  }
+}
+// The loaded bytes of row `row` in place.
+template <bool MX, bool SCALE_VEC>
+__device__ __forceinline__ void placed_scales(uint32_t (&out)[MX ? 2 : 4], const StageScales<MX, SCALE_VEC>& r,
+                                              int row, int nsc) {
+  if constexpr (SCALE_VEC) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = kb + 4 * q + i;
-        v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(scales, b < nsc ? sr * nsc + b : kOutOfRange,
-                                                             0, 0) << (8 * i);
-      }
-      r.s[q] = v;
-    }
+    for (int q = 0; q < (MX ? 2 : 4); ++q) out[q] = r.s[q];
+  } else {
+    place_bytes<(MX ? 2 : 4)>(out, r.s, (row * nsc + r.first) & 3, r.valid);
   }
 }
 
@@ -321,16 +329,19 @@ __device__ __forceinline__ void load_scales(StageScales<MX>& r, __amdgpu_buffer_
 // (h, g, r16) are contiguous, so a lane fetches its whole stage's scales with
 // one (MXFP4) or two (NVFP4) 16-byte reads.  Thread t holds scale row t, which
 // is row r16 = t % 16 of tile t / 16 = 8 h + i of the 256-row operand tile.
-template <bool MX>
-__device__ __forceinline__ void store_scales(const StageScales<MX>& r, uint8_t* __restrict__ sc) {
+template <bool MX, bool SCALE_VEC>
+__device__ __forceinline__ void store_scales(const StageScales<MX, SCALE_VEC>& r, int nsc,
+                                             uint8_t* __restrict__ sc) {
   const int t = threadIdx.x, h = t >> 7, i = (t >> 4) & 7, r16 = t & 15;
+  uint32_t s[MX ? 2 : 4];
+  placed_scales<MX, SCALE_VEC>(s, r, t, nsc);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const int e = ((h * 4 + g) * 16 + r16) * 8 + i;
     if (MX)
-      reinterpret_cast<uint16_t*>(sc)[e] = (uint16_t)(r.s[g >> 1] >> (16 * (g & 1)));
+      reinterpret_cast<uint16_t*>(sc)[e] = (uint16_t)(s[g >> 1] >> (16 * (g & 1)));
     else
-      reinterpret_cast<uint32_t*>(sc)[e] = r.s[g];
+      reinterpret_cast<uint32_t*>(sc)[e] = s[g];
   }
 }
 
@@ -475,46 +486,72 @@ __device__ __forceinline__ void transpose_groups(v4f (&x)[4]) {
 // the next 16 rows loading from where this one's is used up.
 //   row0  D's row of the group's row 0;  m0, n0  the wave's first row (inside
 //   its group, which has m_rows) and column;  bias0  the group's first bias element
+//   strip  this wave's LDS (kStripBytes) for sizes that take no 16-byte accesses
+constexpr int kStripBytes = 8 * kStripRow * 4;
 template <bool OUT_BF16, int TN, int TM>
 __device__ __forceinline__ void store_fused(v4f (&acc)[TN][TM], float alpha, const FusedArgs& f,
                                             int64_t row0, int m0, int m_rows, int n0, int N,
-                                            int64_t bias0, void* D, int r16, int g) {
+                                            int64_t bias0, void* D, uint8_t* strip_bytes, int r16, int g) {
   static_assert(TN % 4 == 0 && TM == 8, "4 W tiles per transposition, 8 row tiles in the switch");
   const int No = f.gated ? N / 2 : N;
+  float* strip = reinterpret_cast<float*>(strip_bytes);
   static_for<TN / 4>([&](auto i4_c) {
     constexpr int i4 = 4 * decltype(i4_c)::value;
-    const int n = n0 + 16 * (i4 + g);
-    float bias[16];
-    load_bias(bias, f, bias0, n, N);
-    const bool fetch = f.residual != nullptr && f.vec && n < N;
-    ResidualRaw res;
-    if (fetch && m0 + r16 < m_rows) load_residual(res, f, row0 + m0 + r16, n, No);
-#pragma unroll 1
-    for (int j = 0; j < TM; ++j) {
-      const int m = m0 + 16 * j + r16;
-      v4f x[4];
-      // (compile-time accumulator indices keep the accumulators in their AGPRs)
+    const int nw = n0 + 16 * i4, n = nw + 16 * g;
+    // (compile-time accumulator indices keep the accumulators in their AGPRs)
+    auto tile_row = [&](int j, v4f (&x)[4]) {
       static_for<TM>([&](auto j_c) {
         constexpr int jj = decltype(j_c)::value;
         if (j == jj) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            asm volatile("" : "+a"(acc[i4 + k][jj]));
             x[k] = acc[i4 + k][jj];
+            // (keeps the read, and what follows from it, inside the loop)
+            asm volatile("" : "+v"(x[k]));
           }
         }
       });
       transpose_groups(x);
-      if (m < m_rows && n < N) {
-        float z[16];
+    };
+    if (f.vec) {
+      float bias[16];
+      if (n < N) load_bias(bias, f, bias0, n);
+      const bool fetch = f.residual != nullptr && n < N;
+      ResidualRaw res;
+      if (fetch && m0 + r16 < m_rows) load_residual(res, f, row0 + m0 + r16, n, No);
+#pragma unroll 1
+      for (int j = 0; j < TM; ++j) {
+        const int m = m0 + 16 * j + r16;
+        v4f x[4];
+        tile_row(j, x);
+        if (m < m_rows && n < N) {
+          float z[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) z[q] = fmaf(x[q >> 2][q & 3], alpha, bias[q]);
-        if (f.vec)
+          for (int q = 0; q < 16; ++q) z[q] = fmaf(x[q >> 2][q & 3], alpha, bias[q]);
           finish_piece<OUT_BF16>(z, f, res, row0 + m, n, N, D, [&] {
             if (j + 1 < TM && m + 16 < m_rows) load_residual(res, f, row0 + m + 16, n, No);
           });
-        else
-          finish_piece_scalar<OUT_BF16>(z, f, row0 + m, n, N, D);
+        }
+      }
+    } else {
+      const int lane = threadIdx.x & 63, nc = nw + (f.gated ? 2 * (lane & 31) : lane);
+      const bool has = f.bias != nullptr && nc < N;
+      const float b0 = has ? load1(f.bias, bias0 + nc, f.bias_bf16) : 0.0f;
+      const float b1 = has && f.gated ? load1(f.bias, bias0 + nc + 1, f.bias_bf16) : 0.0f;
+#pragma unroll 1
+      for (int jh = 0; jh < 2 * TM; ++jh) {       // 8 rows at a time
+        const int m = m0 + 8 * jh;
+        if (m >= m_rows || nw >= N) break;        // (uniform)
+        v4f x[4];
+        tile_row(jh >> 1, x);
+        wave_lds_order();                         // the previous rows have been read
+        if ((r16 >> 3) == (jh & 1)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<v4f*>(strip + (r16 & 7) * kStripRow + 16 * g + 4 * q) = x[q];
+        }
+        wave_lds_order();
+        finish_strip<OUT_BF16>(strip, alpha, f, b0, b1, row0 + m, m_rows - m, nw, N, D);
       }
     }
   });
@@ -595,14 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(W) + t.w_row * rowb, 0,
                                              t.rows_w * rowb, kBufferWord3);
   };
-  auto rsrc_as = [&](const TileRows& t) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(as) + t.a_row * nsc, 0,
-                                             t.rows_a * nsc, kBufferWord3);
-  };
-  auto rsrc_ws = [&](const TileRows& t) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ws) + t.w_row * nsc, 0,
-                                             t.rows_w * nsc, kBufferWord3);
-  };
+  auto rsrc_as = [&](const TileRows& t) { return scale_range<SCALE_VEC>(as + t.a_row * nsc, t.rows_a * nsc); };
+  auto rsrc_ws = [&](const TileRows& t) { return scale_range<SCALE_VEC>(ws + t.w_row * nsc, t.rows_w * nsc); };
   // A grouped workgroup's one tile is looked up once.  Plain launches carry
   // the coordinates (tile row, tile column; -1 past the last tile) of the
   // current and the next tile from tile to tile, and derive the rest where it
@@ -662,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // an empty range: loads through it read zeros and touch no memory
   const __amdgpu_buffer_rsrc_t none =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A), 0, 0, kBufferWord3);
+  const ScaleRange no_scales{none, 0};
   const int ra0 = wm * 16 * kTM + r16, rw0 = wn * 16 * kTN + r16;
 
   // this lane's scale bytes of a stage (layout at store_scales).  MXFP4: tile i's
@@ -740,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (FUSED) {
       if (!MX) alpha = K > 0 ? ((*g_a) * g_b[t.e]) * g_d : 0.0f;
       store_fused<OUT == 2>(acc, alpha, fused, t.a_row - t.m0, t.m0 + wm * 16 * kTM, t.m_rows,
-                            t.n0 + wn * 16 * kTN, N, (int64_t)t.e * N, D, r16, g);
+                            t.n0 + wn * 16 * kTN, N, (int64_t)t.e * N, D,
+                            smem + Cfg<MX>::kLdsBytes + wave * kStripBytes, r16, g);
       return;
     }
     if (!MX) alpha = ((*g_a) * g_b[t.e]) * g_d;
@@ -770,22 +803,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Every loop body below is branch-free (a branch lets the compiler sink the
   // MFMAs past the stores and the barrier): stages past the last one are loaded
   // through the empty range (zeros into a buffer that is never read again).
-  StageScales<MX> ssa, ssw;   // a later stage's scale bytes, from global load to LDS store
+  StageScales<MX, SCALE_VEC> ssa, ssw;   // a later stage's scale bytes, from global load to LDS store
   if constexpr (MX) {
     // Stage s lives in buffer s & 1.  Loads run two stages ahead: stage kt + 2
     // is issued right after the barrier of iteration kt, into the buffer stage
     // kt has finished with, and must land by the next barrier.  The operand
     // fragments of the first k-step of stage kt + 1 are read during the second
     // k-step's MFMAs of stage kt, so no MFMA waits for LDS after a barrier.
-    load_scales<MX, SCALE_VEC>(ssa, rsrc_as(tile0), nsc, 0);
-    load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(tile0), nsc, 0);
+    load_scales<MX, SCALE_VEC>(ssa, rsrc_as(tile0), threadIdx.x, nsc, 0);
+    load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(tile0), threadIdx.x, nsc, 0);
     dma_tile<SCALE_VEC>(rsrc_a(tile0), tile_a(0), rowb, K, 0);
     dma_tile<SCALE_VEC>(rsrc_w(tile0), tile_w(0), rowb, K, 0);
-    store_scales<MX>(ssa, sc_a(0));
-    store_scales<MX>(ssw, sc_w(0));
+    store_scales<MX, SCALE_VEC>(ssa, nsc, sc_a(0));
+    store_scales<MX, SCALE_VEC>(ssw, nsc, sc_w(0));
     const bool two = nk > 1;
-    load_scales<MX, SCALE_VEC>(ssa, two ? rsrc_as(tile0) : none, nsc, BK);
-    load_scales<MX, SCALE_VEC>(ssw, two ? rsrc_ws(tile0) : none, nsc, BK);
+    load_scales<MX, SCALE_VEC>(ssa, two ? rsrc_as(tile0) : no_scales, threadIdx.x, nsc, BK);
+    load_scales<MX, SCALE_VEC>(ssw, two ? rsrc_ws(tile0) : no_scales, threadIdx.x, nsc, BK);
     dma_tile<SCALE_VEC>(two ? rsrc_a(tile0) : none, tile_a(1), rowb, K, BK);
     dma_tile<SCALE_VEC>(two ? rsrc_w(tile0) : none, tile_w(1), rowb, K, BK);
     wait_dma();
@@ -818,8 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fw1[2 * i - 7] = frag(tile_w(cb), rw0 + 32 * i - 112, 2 * g + 1);
         }
       });
-      store_scales<MX>(ssa, sc_a(nb));   // stage kt + 1
-      store_scales<MX>(ssw, sc_w(nb));
+      store_scales<MX, SCALE_VEC>(ssa, nsc, sc_a(nb));   // stage kt + 1
+      store_scales<MX, SCALE_VEC>(ssw, nsc, sc_w(nb));
       wait_dma();        // stage kt + 1 (issued during the previous stage) has landed
       __syncthreads();   // stage kt + 1 is in buffer nb; nobody reads buffer cb any more
       // k-step 1 of stage kt, issuing one block of each operand's stage kt + 2
@@ -827,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k_ld;
       const TileRows lt = load_tile(kt, k_ld);
       const __amdgpu_buffer_rsrc_t la = rsrc_a(lt), lw = rsrc_w(lt);
-      load_scales<MX, SCALE_VEC>(ssa, rsrc_as(lt), nsc, k_ld);
-      load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(lt), nsc, k_ld);
+      load_scales<MX, SCALE_VEC>(ssa, rsrc_as(lt), threadIdx.x, nsc, k_ld);
+      load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(lt), threadIdx.x, nsc, k_ld);
       mfma_lead();
       static_for<kTN>([&](auto i_c) {
         constexpr int i = decltype(i_c)::value;
@@ -867,15 +900,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // then issue the loads of stage kt + 2 (into this stage's buffer) and read
     // and dequantize the first codes of stage kt + 1, so no MFMA waits at a
     // stage boundary.
-    load_scales<MX, SCALE_VEC>(ssa, rsrc_as(tile0), nsc, 0);
-    load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(tile0), nsc, 0);
+    load_scales<MX, SCALE_VEC>(ssa, rsrc_as(tile0), threadIdx.x, nsc, 0);
+    load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(tile0), threadIdx.x, nsc, 0);
     dma_tile<SCALE_VEC>(rsrc_a(tile0), tile_a(0), rowb, K, 0);
     dma_tile<SCALE_VEC>(rsrc_w(tile0), tile_w(0), rowb, K, 0);
-    store_scales<MX>(ssa, sc_a(0));
-    store_scales<MX>(ssw, sc_w(0));
+    store_scales<MX, SCALE_VEC>(ssa, nsc, sc_a(0));
+    store_scales<MX, SCALE_VEC>(ssw, nsc, sc_w(0));
     const bool two = nk > 1;
-    load_scales<MX, SCALE_VEC>(ssa, two ? rsrc_as(tile0) : none, nsc, BK);
-    load_scales<MX, SCALE_VEC>(ssw, two ? rsrc_ws(tile0) : none, nsc, BK);
+    load_scales<MX, SCALE_VEC>(ssa, two ? rsrc_as(tile0) : no_scales, threadIdx.x, nsc, BK);
+    load_scales<MX, SCALE_VEC>(ssw, two ? rsrc_ws(tile0) : no_scales, threadIdx.x, nsc, BK);
     dma_tile<SCALE_VEC>(two ? rsrc_a(tile0) : none, tile_a(1), rowb, K, BK);
     dma_tile<SCALE_VEC>(two ? rsrc_w(tile0) : none, tile_w(1), rowb, K, BK);
     wait_dma();
@@ -926,12 +959,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kn = un >> 2;              // its k-step
         if constexpr (u == 6) {
           // every wave has read this stage's last codes (sub-step 7, read in 5)
-          store_scales<MX>(ssa, sc_a(nb));   // stage kt + 1
-          store_scales<MX>(ssw, sc_w(nb));
+          store_scales<MX, SCALE_VEC>(ssa, nsc, sc_a(nb));   // stage kt + 1
+          store_scales<MX, SCALE_VEC>(ssw, nsc, sc_w(nb));
           wait_dma();        // stage kt + 1 (issued during the previous stage) has landed
           __syncthreads();   // stage kt + 1 is in buffer nb; buffer cb is free
-          load_scales<MX, SCALE_VEC>(ssa, rsrc_as(lt), nsc, k_ld);
-          load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(lt), nsc, k_ld);
+          load_scales<MX, SCALE_VEC>(ssa, rsrc_as(lt), threadIdx.x, nsc, k_ld);
+          load_scales<MX, SCALE_VEC>(ssw, rsrc_ws(lt), threadIdx.x, nsc, k_ld);
           read_scales(nb, sa_n, sw_n);
         }
         mfma_lead();
@@ -1037,37 +1070,21 @@ __device__ __forceinline__ bool holds_a_scales() {
 }
 
 template <bool SCALE_VEC>
-__device__ __forceinline__ void load_scales8(StageScales<true>& r, __amdgpu_buffer_rsrc_t sa,
-                                             __amdgpu_buffer_rsrc_t sw, int nsc, int k0) {
-  const __amdgpu_buffer_rsrc_t src = holds_a_scales() ? sa : sw;
-  const int kb = k0 / 32;
-  const int sr = threadIdx.x & 255;
-  if (SCALE_VEC) {   // K % 256 == 0 and 16-byte aligned scale rows
-    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(src, sr * nsc + kb, 0, 0);
-    r.s[0] = v.x;
-    r.s[1] = v.y;
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = kb + 4 * q + i;
-        v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(src, b < nsc ? sr * nsc + b : kOutOfRange,
-                                                             0, 0) << (8 * i);
-      }
-      r.s[q] = v;
-    }
-  }
+__device__ __forceinline__ void load_scales8(StageScales<true, SCALE_VEC>& r, const ScaleRange& sa,
+                                             const ScaleRange& sw, int nsc, int k0) {
+  load_scales<true, SCALE_VEC>(r, holds_a_scales() ? sa : sw, threadIdx.x & 255, nsc, k0);
 }
 
-__device__ __forceinline__ void store_scales8(const StageScales<true>& r, uint8_t* __restrict__ sc_a,
-                                              uint8_t* __restrict__ sc_w) {
+template <bool SCALE_VEC>
+__device__ __forceinline__ void store_scales8(const StageScales<true, SCALE_VEC>& r, int nsc,
+                                              uint8_t* __restrict__ sc_a, uint8_t* __restrict__ sc_w) {
   const int t = threadIdx.x & 255, r16 = t & 15;
   const bool a = holds_a_scales();
+  uint32_t s[2];
+  placed_scales<true, SCALE_VEC>(s, r, t, nsc);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const uint16_t v = (uint16_t)(r.s[g >> 1] >> (16 * (g & 1)));
+    const uint16_t v = (uint16_t)(s[g >> 1] >> (16 * (g & 1)));
     if (a)   // A: (half h, g, r16, tile i of 8), as store_scales
       reinterpret_cast<uint16_t*>(sc_a)[(((t >> 7) * 4 + g) * 16 + r16) * 8 + ((t >> 4) & 7)] = v;
     else     // W: (quarter q, g, r16, tile i of 4)
@@ -1126,12 +1143,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                              t.rows_w * rowb, kBufferWord3);
   };
   auto rsrc_as = [&](const TileRows& t) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(as) + (int64_t)t.m0 * nsc, 0,
-                                             t.rows_a * nsc, kBufferWord3);
+    return scale_range<SCALE_VEC>(as + (int64_t)t.m0 * nsc, t.rows_a * nsc);
   };
   auto rsrc_ws = [&](const TileRows& t) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ws) + (int64_t)t.n0 * nsc, 0,
-                                             t.rows_w * nsc, kBufferWord3);
+    return scale_range<SCALE_VEC>(ws + (int64_t)t.n0 * nsc, t.rows_w * nsc);
   };
 
   v4f acc[kT8N][kTM];   // [W tile][A tile]
@@ -1150,6 +1165,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
   auto tile_w = [&](int b) { return smem + kTiles + 2 * kTileA + b * kTileW; };
   const __amdgpu_buffer_rsrc_t none =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A), 0, 0, kBufferWord3);
+  const ScaleRange no_scales{none, 0};
   const int ra0 = wm * 16 * kTM + r16, rw0 = wn * 16 * kT8N + r16;
 
   // this lane's scale bytes of a stage: A tile j's two bytes are bytes
@@ -1180,13 +1196,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
   // Stage s of a tile lives in buffer s & 1 (nk2 is even, so every tile starts
   // in buffer 0); loads run two stages ahead as in k_gemm's MXFP4 loop, every
   // loop body branch-free.
-  StageScales<true> ss;
+  StageScales<true, SCALE_VEC> ss;
   load_scales8<SCALE_VEC>(ss, rsrc_as(cur), rsrc_ws(cur), nsc, 0);
   dma_tile8<SCALE_VEC>(rsrc_a(cur), tile_a(0), rowb, K, 0);
   dma_tile8<SCALE_VEC>(rsrc_w(cur), tile_w(0), rowb, K, 0);
-  store_scales8(ss, sc_a(0), sc_w(0));
+  store_scales8<SCALE_VEC>(ss, nsc, sc_a(0), sc_w(0));
   const bool two = nk > 1;
-  load_scales8<SCALE_VEC>(ss, two ? rsrc_as(cur) : none, two ? rsrc_ws(cur) : none, nsc, BK);
+  load_scales8<SCALE_VEC>(ss, two ? rsrc_as(cur) : no_scales, two ? rsrc_ws(cur) : no_scales, nsc, BK);
   dma_tile8<SCALE_VEC>(two ? rsrc_a(cur) : none, tile_a(1), rowb, K, BK);
   dma_tile8<SCALE_VEC>(two ? rsrc_w(cur) : none, tile_w(1), rowb, K, BK);
   wait_dma();
@@ -1218,7 +1234,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
       fa1[2 * i + 1] = frag(tile_a(cb), ra0 + 32 * i + 16, 2 * g + 1);
       fw1[i] = frag(tile_w(cb), rw0 + 16 * i, 2 * g + 1);
     });
-    store_scales8(ss, sc_a(nb), sc_w(nb));   // the next stage
+    store_scales8<SCALE_VEC>(ss, nsc, sc_a(nb), sc_w(nb));   // the next stage
     wait_dma();        // the next stage (issued during the previous stage) has landed
     __syncthreads();   // it is in buffer nb; nobody reads buffer cb any more
     const int kl = kt + 2;
@@ -1256,7 +1272,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const int m0 = cur.m0, n0 = cur.n0;
     const int mb = m0 + wm * 16 * kTM + r16, nb = n0 + wn * 16 * kT8N + 4 * g;
     if constexpr (FUSED)
-      store_fused<OUT == 2>(acc, g_d, fused, 0, m0 + wm * 16 * kTM, M, n0 + wn * 16 * kT8N, N, 0, D, r16, g);
+      store_fused<OUT == 2>(acc, g_d, fused, 0, m0 + wm * 16 * kTM, M, n0 + wn * 16 * kT8N, N, 0, D,
+                            smem + Cfg<true>::kLdsBytes + wave * kStripBytes, r16, g);
     else if (vec_out && m0 + BM <= M && n0 + BN <= N)
       store_outputs<OUT, false, kT8N, kTM>(acc, g_d, s_glob, mb, nb, M, N, D, d_scales, true, r16, g);
     else
@@ -1300,7 +1317,8 @@ hipError_t launch_t(const uint8_t* A, const uint8_t* as, const uint8_t* W, const
   const int tiles_n = (N + BN - 1) / BN;
   // grouped: each group adds at most one partial row tile to ceil(M / BM)
   const int tiles_m = (M + BM - 1) / BM + (GROUPED ? gr.ngroups : 0);
-  constexpr int lds = Cfg<MX>::kLdsBytes;
+  constexpr int lds = Cfg<MX>::kLdsBytes + (FUSED ? (MX && !GROUPED ? kThreads8 : kThreads) / 64 * kStripBytes : 0);
+  static_assert(lds <= 160 * 1024, "LDS");
   // MXFP4: the 8-wave kernel (grouped launches: k_gemm, whose group lookup
   // would not fit the 8-wave kernel's 256 registers without spills); NVFP4: k_gemm
   constexpr bool kMx8 = MX && !GROUPED;

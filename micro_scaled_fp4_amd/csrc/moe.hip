@@ -15,13 +15,6 @@ using namespace fp4dev;
 
 namespace {
 
-// LDS traffic between the lanes of one wave: LDS operations of a wave complete
-// in order, so only the compiler has to keep them in order.
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // ------------------------------------------------------ lane reductions --
 // Rotation by R inside each row of 16 lanes (DPP row_ror).
 template <int R>
