@@ -2,18 +2,20 @@
 // fused epilogue: D = act(alpha A W^T + bias) + residual with at most a few tens
 // of rows per group, where W is read once and everything else is small.
 //
-// Work.  A unit is 16 RT rows of one group against kSlots * S strips of 16 W
-// rows; the units of all groups are numbered in a row (group, row chunk, strips)
-// and each workgroup (one per CU) takes an equal, contiguous part of them, so
-// empty groups cost nothing and full ones spread over the device.  Of the 8
-// waves, KS split K and 8 / KS take different strips; a wave adds its K range
-// for S strips, and the KS partial tiles meet in LDS once per unit (one barrier,
-// buffers alternating by unit), in wave order.
+// Work.  Of a workgroup's 8 waves (one workgroup per CU), KS split K and 8 / KS
+// take different 16-row strips of W.  A granule is 16 RT rows of one group
+// against 8 / KS strips; the granules of all groups are numbered in a row
+// (group, row chunk, strips) and each workgroup takes an equal, contiguous part
+// of them, so empty groups cost nothing, full ones spread over the device, and
+// the parts differ by one granule at most.  A unit is up to S granules of one
+// group: a wave adds its K range for S strips at once, and the KS partial tiles
+// meet in LDS once per unit, in wave order.
 //
 // A wave's K range goes by pairs of 128-value steps.  W is loaded 8 rows x 128
 // bytes per instruction (full lines) and turned to the MFMA's operand layout
-// through a wave-private XOR-swizzled LDS tile; the loads of the next two pairs
-// are in flight in registers, across units.  A's codes are read from L2 per
+// through a wave-private XOR-swizzled LDS tile; a pair's loads for all S strips
+// are in flight in registers while the pair before it computes, across units
+// (72 KB per CU in flight; two pairs ahead ran slower for want of registers).  A's codes are read from L2 per
 // pair, in the operand layout, and dequantized once for the S strips.
 // NVFP4: both operands to fp16 exactly (E2M1 x E4M3 has 6 significant bits),
 // v_mfma_f32_16x16x32_f16.  MXFP4: codes and E8M0 bytes straight into
@@ -37,7 +39,6 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr int kRing = 2;                        // pairs in flight per wave
 constexpr int kGroup = 4;                       // pairs per group of W scale bytes
 constexpr int kLoadNT = 2;                      // buffer load cache policy: nontemporal
 
@@ -56,11 +57,21 @@ struct FewArgs {
   FusedArgs f;
 };
 
+// LDS: transpose tiles [8 waves][S] x 2 KB | W scale groups [8 waves][S][16 rows]
+// x (MXFP4 8, NVFP4 16) kGroup | partial tiles [buffers][8 waves][S][RT] x 1 KB,
+// two buffers (alternating by unit) where they fit
+constexpr int lds_fixed(bool mx, int S) { return kWaves * S * (2048 + 16 * (mx ? 8 : 16) * kGroup); }
+constexpr int red_buffers(bool mx, int RT, int S) {
+  return lds_fixed(mx, S) + 2 * kWaves * S * RT * 1024 <= 160 * 1024 ? 2 : 1;
+}
+
 // SVEC: scale rows are 16-byte aligned and K is a multiple of 256; else scale
 // bytes are read as the aligned dwords that hold them and shifted into place,
 // with those past K as zeros.
 template <bool MX, int RT, int S, bool SVEC, bool OUT_BF16>
 __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
+  constexpr int kRows = 16 * RT;                // rows of an item
+  constexpr int kBufs = red_buffers(MX, RT, S);
   constexpr int kSB = MX ? 8 : 16;              // scale bytes of a row per pair
   constexpr int kSG = kSB * kGroup;             // of a row per group of pairs
   constexpr int kGD = kSG / 16;                 // dwords per lane of a group (MXFP4 2, NVFP4 4)
@@ -69,17 +80,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int r8 = lane >> 3, c8 = lane & 7;
-  const int KS = a.ks, slots = kWaves / KS;
+  const int KS = a.ks, slots = kWaves / KS, lslots = 31 - __builtin_clz(slots);
   const int part = wave % KS, slot = wave / KS;
   const int N = a.N, K = a.K;
   const int wrow = K / 2, srow = K / (MX ? 32 : 16);
-  const int strip_rows = 16 * S * slots;        // W rows per unit
-  const int sb_n = (N + strip_rows - 1) / strip_rows;
-  // LDS: transpose tiles [8 waves][2] x 2 KB | W scale groups [8 waves][S][16 rows] x kSG |
-  // partial tiles [2][8 waves][S][RT] x 1 KB
-  uint8_t* tile = lds + wave * 4096;
-  uint8_t* sgl = lds + kWaves * 4096 + wave * (S * 16 * kSG);
-  v4f* red = reinterpret_cast<v4f*>(lds + kWaves * 4096 + kWaves * S * 16 * kSG);
+  const int gran = 16 * slots;                  // W rows per granule
+  const int gn = (N + gran - 1) / gran;         // granules per item
+  uint8_t* tile = lds + wave * (S * 2048);
+  uint8_t* sgl = lds + kWaves * S * 2048 + wave * (S * 16 * kSG);
+  v4f* red = reinterpret_cast<v4f*>(lds + lds_fixed(MX, S));
 
   // ---- this workgroup's units
   const bool grouped = a.offsets != nullptr;
@@ -91,14 +100,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
       lo = min(max(a.offsets[e], 0), a.M);
       n = min(max(a.offsets[e + 1], lo), a.M) - lo;
     }
-    inc = (n + 16 * RT - 1) / (16 * RT);
+    inc = (n + kRows - 1) / kRows;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(inc, d, 64);
       if (lane >= d) inc += v;
     }
   };
-  int items = (a.M + 16 * RT - 1) / (16 * RT);
+  int items = (a.M + kRows - 1) / kRows;
   if (grouped) {
     items = 0;
     for (int c = 0; c < a.groups; c += 64) {
@@ -107,34 +116,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
       items += __shfl(inc, 63, 64);
     }
   }
-  const int64_t U = (int64_t)items * sb_n;
+  const int64_t U = (int64_t)items * gn;
   const int64_t u0 = U * blockIdx.x / gridDim.x, u1 = U * (blockIdx.x + 1) / gridDim.x;
-  const int nu = (int)(u1 - u0);
-  if (nu == 0) return;                          // (the whole workgroup)
+  if (u0 == u1) return;                         // (the whole workgroup)
 
-  // An item: 16 RT rows of a group.  row0: its first row, rows: how many, e: the
-  // group.  Unit u is item u / sb_n, strips from (u % sb_n) strip_rows on.
+  // An item: kRows rows of a group.  row0: its first row, rows: how many, e: the
+  // group.  Granule u is item u / gn, W rows from (u % gn) gran on.
   struct Item {
     int row0, rows, e;
   };
   auto item_of = [&](int it) {
-    Item r{it * 16 * RT, 0, 0};
+    Item r{it * kRows, 0, 0};
     if (!grouped) {
-      r.rows = min(16 * RT, a.M - r.row0);
+      r.rows = min(kRows, a.M - r.row0);
       return r;
     }
     int base = 0;
     for (int c = 0; c < a.groups; c += 64) {
       int lo, n, inc;
       chunk_of(c, lo, n, inc);
-      const int mine = (n + 16 * RT - 1) / (16 * RT), start = base + inc - mine;
+      const int mine = (n + kRows - 1) / kRows, start = base + inc - mine;
       const uint64_t hit = __ballot(it >= start && it < start + mine);
       if (hit) {
         const int src = __ffsll((unsigned long long)hit) - 1;
-        const int in = (it - __shfl(start, src, 64)) * 16 * RT;
+        const int in = (it - __shfl(start, src, 64)) * kRows;
         r.e = c + src;
         r.row0 = __shfl(lo, src, 64) + in;
-        r.rows = min(16 * RT, __shfl(n, src, 64) - in);
+        r.rows = min(kRows, __shfl(n, src, 64) - in);
         break;
       }
       base += __shfl(inc, 63, 64);
@@ -143,6 +151,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
     r.rows = __builtin_amdgcn_readfirstlane(r.rows);
     return r;
+  };
+
+  // A unit: an item, the first of its W rows and its granules.  next_unit walks
+  // this workgroup's units.
+  struct Unit {
+    Item item;
+    int n0, size;
+  };
+  int64_t left = u1 - u0;
+  int at_item = (int)(u0 / gn), at_gran = (int)(u0 - (int64_t)at_item * gn);
+  Item item = item_of(at_item);
+  auto next_unit = [&]() {
+    if (at_gran == gn) {
+      at_gran = 0;
+      item = item_of(++at_item);
+    }
+    const Unit u{item, at_gran * gran, (int)min((int64_t)min(S, gn - at_gran), left)};
+    at_gran += u.size;
+    left -= u.size;
+    return u;
   };
 
   // ---- this wave's pairs [pbeg, pbeg + E): dealt evenly, the longer parts first
@@ -160,42 +188,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     uint32_t sg[S][kGD + (SVEC ? 0 : 1)];       // W scale bytes of the group that starts here
     int xs_first, sg_first;                     // !SVEC: row 0's first byte in the ranges
   };
-  Elem ring[kRing];
+  Elem el;                                      // the element in flight
   const int w_lane = r8 * wrow + 16 * c8;
 
-  int lu = 0, le = 0;                           // next element to load: unit u0 + lu, pair pbeg + le
-  int l_it = -1, l_n0 = 0;
-  Item l_item{0, 0, 0};
-  auto load_unit = [&]() {                      // the unit's item and first W row of this slot
-    const int64_t u = u0 + lu;
-    const int it = (int)(u / sb_n);
-    if (it != l_it) {
-      l_item = item_of(it);
-      l_it = it;
-    }
-    l_n0 = (int)(u - (int64_t)it * sb_n) * strip_rows + slot * 16 * S;
-  };
-  auto load_elem = [&](Elem& el) {
+  Unit lun{item, 0, 0};                         // its unit
+  int le = 0;                                   // next element to load: pair pbeg + le of lun
+  bool live = false;                            // el holds an element
+  auto load_elem = [&]() {
     // past the last unit: empty ranges (no branch around the loads)
-    const bool live = lu < nu;
-    if (live && le == 0) load_unit();
+    if (le == 0) {
+      live = left > 0;
+      if (live) lun = next_unit();
+    }
     const int p = pbeg + le;
-    const int rows_w = live ? max(0, min(16 * S, N - l_n0)) : 0;
-    const int rows_a = live ? l_item.rows : 0;
-    const int64_t wr0 = (int64_t)l_item.e * N + l_n0;
+    // rows of the unit that exist, from this slot's first on; strip s lies s gran
+    // rows further
+    const int rows_w = live ? max(0, min(lun.size * gran, N - lun.n0) - 16 * slot) : 0;
+    const int rows_a = live ? lun.item.rows : 0;
+    const int64_t wr0 = (int64_t)lun.item.e * N + lun.n0 + 16 * slot;
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t*>(a.W) + wr0 * wrow, 0, rows_w * wrow, kBufferWord3);
     const ScaleRange rs = scale_range<SVEC>(a.ws + wr0 * srow, rows_w * srow);
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.A) + (int64_t)l_item.row0 * wrow, 0, rows_a * wrow, kBufferWord3);
-    const ScaleRange rsa = scale_range<SVEC>(a.as + (int64_t)l_item.row0 * srow, rows_a * srow);
+        const_cast<uint8_t*>(a.A) + (int64_t)lun.item.row0 * wrow, 0, rows_a * wrow, kBufferWord3);
+    const ScaleRange rsa = scale_range<SVEC>(a.as + (int64_t)lun.item.row0 * srow, rows_a * srow);
     if (le % kGroup == 0) {
       // lane (r16, g): the scale bytes of pair p + g of row r16 of each strip
       // (those past this wave's last pair are never used)
       el.sg_first = rs.lead + kSB * p;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const int off = (16 * s + r16) * srow + kSB * g;
+        const int off = (s * gran + r16) * srow + kSB * g;
         if constexpr (!SVEC) {
           const int at = (off + el.sg_first) & ~3;
 #pragma unroll
@@ -232,13 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      el.w[s][0] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_lane + 16 * s * wrow, 128 * p, kLoadNT);
-      el.w[s][1] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_lane + (16 * s + 8) * wrow, 128 * p, kLoadNT);
+      el.w[s][0] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_lane + s * gran * wrow, 128 * p, kLoadNT);
+      el.w[s][1] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_lane + (s * gran + 8) * wrow, 128 * p, kLoadNT);
     }
-    if (++le == E) {
-      le = 0;
-      ++lu;
-    }
+    if (++le == E) le = 0;
   };
 
   v4f acc[S][RT];
@@ -249,42 +269,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
       for (int t = 0; t < RT; ++t) acc[s][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   };
 
-  // ---- end of unit u0 + cu: partial tiles to LDS, then outputs by all threads,
-  // two columns each
-  int c_it = -1;
-  Item c_item{0, 0, 0};
-  auto finish = [&](int cu) {
-    v4f* buf = red + (cu & 1) * kWaves * S * RT * 64;
+  // ---- end of unit cun: partial tiles to LDS, then outputs by all threads, two
+  // columns each
+  Unit cun = lun;                               // unit being computed
+  int parity = 0;
+  const int cap = 31 - __builtin_clz(S * gran / 2);   // column pairs of a full unit: 1 << cap
+  auto finish = [&]() {
+    if (kBufs == 1) __syncthreads();            // the previous unit's tiles have been read
+    v4f* buf = red + parity * kWaves * S * RT * 64;
+    if (kBufs == 2) parity ^= 1;
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int t = 0; t < RT; ++t) buf[((wave * S + s) * RT + t) * 64 + lane] = acc[s][t];
-    const int64_t u = u0 + cu;
-    const int it = (int)(u / sb_n);
-    if (it != c_it) {
-      c_item = item_of(it);
-      c_it = it;
-    }
-    const int n0 = (int)(u - (int64_t)it * sb_n) * strip_rows;
     float alpha = a.g_d;
-    if (!MX) alpha = K > 0 ? ((*a.g_a) * a.g_b[c_item.e]) * a.g_d : 0.0f;
+    if (!MX) alpha = K > 0 ? ((*a.g_a) * a.g_b[cun.item.e]) * a.g_d : 0.0f;
     __syncthreads();
-    const int pairs = strip_rows / 2;
-    const float* fb = reinterpret_cast<const float*>(buf);
-    for (int i = threadIdx.x; i < c_item.rows * pairs; i += kThreads) {
-      const int m = i / pairs, c = 2 * (i - m * pairs);          // row and first column inside the unit
-      const int n = n0 + c;
-      if (n >= N) continue;
-      const int sl = c / (16 * S), s = (c / 16) % S, q = c & 3, gg = (c & 15) >> 2;
-      // lane (m % 16, gg) element q of tile (s, m / 16) of the slot's waves
-      const int at = (((sl * KS * S + s) * RT + m / 16) * 64 + gg * 16 + (m & 15)) * 4 + q;
-      float z0 = fb[at], z1 = fb[at + 1];
+    const int cols = min(cun.size * gran, N - cun.n0);
+    for (int i = threadIdx.x; i < cun.item.rows << cap; i += kThreads) {
+      const int m = i >> cap, c = 2 * (i - (m << cap));          // row and first column inside the unit
+      const int n = cun.n0 + c;
+      if (c >= cols) continue;
+      // (gran and the slots are powers of two)
+      const int s = c >> (4 + lslots), sl = (c >> 4) & (slots - 1), q = c & 3, gg = (c & 15) >> 2;
+      // lane (m % 16, gg), elements q and q + 1 of tile (s, m / 16) of the slot's waves
+      const float* v = reinterpret_cast<const float*>(buf) +
+                       (((sl * KS * S + s) * RT + m / 16) * 64 + gg * 16 + (m & 15)) * 4 + q;
+      float z0 = v[0], z1 = v[1];
       for (int k = 1; k < KS; ++k) {
-        z0 += fb[at + k * S * RT * 256];
-        z1 += fb[at + k * S * RT * 256 + 1];
+        z0 += v[k * S * RT * 256];
+        z1 += v[k * S * RT * 256 + 1];
       }
-      const int64_t row = c_item.row0 + m;
-      const int64_t b0 = (int64_t)c_item.e * N + n;
+      const int64_t row = cun.item.row0 + m;
+      const int64_t b0 = (int64_t)cun.item.e * N + n;
       const bool both = n + 1 < N;
       z0 = fmaf(z0, alpha, a.f.bias != nullptr ? load1(a.f.bias, b0, a.f.bias_bf16) : 0.0f);
       z1 = fmaf(z1, alpha, a.f.bias != nullptr && both ? load1(a.f.bias, b0 + 1, a.f.bias_bf16) : 0.0f);
@@ -315,8 +332,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   // tile, the ring slot refilled once its registers are in LDS
   const int wsw = (r8 ^ c8) << 4;
   const int rd = r16 * 128;
-  int cu = 0, ce = 0;                           // element being computed
-  auto elem = [&](Elem& el) {
+  int ce = 0;                                   // pair being computed
+  // 32 values of step st (two 16-value blocks; scale: the pair's 4 bytes) to fp16
+  auto dequant = [&](v8h (&q)[4], const u32x4& codes, uint32_t scale, int st) {
+    const v2h p = st ? e4m3_pair_h<true>(scale) : e4m3_pair_h<false>(scale);
+    const v2h h0 = v2h{p.x, p.x}, h1 = v2h{p.y, p.y};
+    q[0] = dq8(codes.x, h0);
+    q[1] = dq8(codes.y, h0);
+    q[2] = dq8(codes.z, h1);
+    q[3] = dq8(codes.w, h1);
+  };
+  auto elem = [&]() {
+    if (ce == 0) cun = lun;                     // el is its first pair
     if (ce % kGroup == 0) {
 #pragma unroll
       for (int s = 0; s < S; ++s) {
@@ -335,10 +362,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
           *reinterpret_cast<u32x4*>(dst) = u32x4{v[0], v[1], v[2], v[3]};
       }
     }
-    // A's operand, dequantized once for the S strips
+    // W's codes through the tiles, all strips at once: one LDS round trip per element
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      uint8_t* tb = tile + s * 2048;
+      *reinterpret_cast<u32x4*>(tb + r8 * 128 + wsw) = el.w[s][0];
+      *reinterpret_cast<u32x4*>(tb + (8 + r8) * 128 + (wsw ^ 64)) = el.w[s][1];
+    }
+    u32x4 codes[S][2];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int c = 2 * g + st;
+        codes[s][st] = *reinterpret_cast<const u32x4*>(
+            tile + s * 2048 + rd + ((c ^ (r16 & 7) ^ ((r16 >> 3) << 2)) << 4));
+      }
     u32x4 xc[RT][2];
-    uint32_t xs[RT];
-    v8h xq[MX ? 1 : RT][2][4];
+    uint32_t xs[RT], wsb[S];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       xc[t][0] = el.x[t][0];
@@ -351,85 +392,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
                        srow - kSB * (pbeg + ce) - (kSB / 4) * g);
         xs[t] = v[0];
       }
-      if constexpr (!MX) {
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const v2h hp = st ? e4m3_pair_h<true>(xs[t]) : e4m3_pair_h<false>(xs[t]);
-          const v2h h0 = v2h{hp.x, hp.x}, h1 = v2h{hp.y, hp.y};
-          xq[t][st][0] = dq8(xc[t][st].x, h0);
-          xq[t][st][1] = dq8(xc[t][st].y, h0);
-          xq[t][st][2] = dq8(xc[t][st].z, h1);
-          xq[t][st][3] = dq8(xc[t][st].w, h1);
-        }
-      }
     }
-    uint32_t wsb[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const uint8_t* src = sgl + (16 * s + r16) * kSG + kSB * (ce % kGroup) + (kSB / 4) * g;
       wsb[s] = MX ? (uint32_t)*reinterpret_cast<const uint16_t*>(src) : *reinterpret_cast<const uint32_t*>(src);
     }
+    load_elem();                                // el's registers are in use no more
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      uint8_t* tb = tile + (s & 1) * 2048;
-      *reinterpret_cast<u32x4*>(tb + r8 * 128 + wsw) = el.w[s][0];
-      *reinterpret_cast<u32x4*>(tb + (8 + r8) * 128 + (wsw ^ 64)) = el.w[s][1];
-      if (s == S - 1) load_elem(el);
+    for (int st = 0; st < 2; ++st) {
+      if constexpr (MX) {
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const int c = 2 * g + st;
-        const u32x4 codes = *reinterpret_cast<const u32x4*>(
-            tb + rd + ((c ^ (r16 & 7) ^ ((r16 >> 3) << 2)) << 4));
-        if constexpr (MX) {
-          const v8i wo = {(int)codes.x, (int)codes.y, (int)codes.z, (int)codes.w, 0, 0, 0, 0};
+        for (int s = 0; s < S; ++s) {
+          const u32x4 c = codes[s][st];
+          const v8i wo = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
-            const v8i xo = {(int)xc[t][st].x, (int)xc[t][st].y, (int)xc[t][st].z, (int)xc[t][st].w, 0, 0, 0, 0};
+            const u32x4 x = xc[t][st];
+            const v8i xo = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
             acc[s][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 wo, xo, acc[s][t], 4, 4, 0, st ? wsb[s] >> 8 : wsb[s], 0, st ? xs[t] >> 8 : xs[t]);
           }
-        } else {
-          const v2h wp = st ? e4m3_pair_h<true>(wsb[s]) : e4m3_pair_h<false>(wsb[s]);
-          const v2h w0 = v2h{wp.x, wp.x}, w1 = v2h{wp.y, wp.y};
-          const v8h q0 = dq8(codes.x, w0), q1 = dq8(codes.y, w0), q2 = dq8(codes.z, w1), q3 = dq8(codes.w, w1);
+        }
+      } else {
+        // the operand with fewer 16-row tiles stays dequantized, the other passes by
+        constexpr bool kHoldX = RT <= S;
+        constexpr int H = kHoldX ? RT : S, O = kHoldX ? S : RT;
+        v8h hold[H][4];
 #pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q0, xq[t][st][0], acc[s][t], 0, 0, 0);
-            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q1, xq[t][st][1], acc[s][t], 0, 0, 0);
-            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q2, xq[t][st][2], acc[s][t], 0, 0, 0);
-            acc[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q3, xq[t][st][3], acc[s][t], 0, 0, 0);
-          }
+        for (int h = 0; h < H; ++h) dequant(hold[h], kHoldX ? xc[h][st] : codes[h][st], kHoldX ? xs[h] : wsb[h], st);
+#pragma unroll
+        for (int o = 0; o < O; ++o) {
+          v8h pass[4];
+          dequant(pass, kHoldX ? codes[o][st] : xc[o][st], kHoldX ? wsb[o] : xs[o], st);
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v4f& c = kHoldX ? acc[o][h] : acc[h][o];
+              c = __builtin_amdgcn_mfma_f32_16x16x32_f16(kHoldX ? pass[k] : hold[h][k],
+                                                         kHoldX ? hold[h][k] : pass[k], c, 0, 0, 0);
+            }
         }
       }
     }
     if (++ce == E) {
       ce = 0;
-      finish(cu);
-      ++cu;
+      finish();
       clear();
     }
   };
 
   clear();
   if (E == 0) {                                 // no pair for this wave: zeros in every unit
-    for (cu = 0; cu < nu; ++cu) finish(cu);
+    while (left > 0) {
+      cun = next_unit();
+      finish();
+    }
     return;
   }
-#pragma unroll
-  for (int i = 0; i < kRing; ++i) load_elem(ring[i]);
-  // element j of the wave lives in ring slot j % kRing
-  const int64_t J = (int64_t)nu * E;
-  for (int64_t j = 0; j < J; j += kRing) {
-#pragma unroll
-    for (int i = 0; i < kRing; ++i)
-      if (j + i < J) elem(ring[i]);
-  }
+  load_elem();
+  while (live) elem();
 }
 
 template <bool MX, int RT, int S, bool SVEC, bool OUT_BF16>
 hipError_t launch_t(const FewArgs& a, hipStream_t stream) {
-  constexpr int kSG = (MX ? 8 : 16) * kGroup;
-  constexpr int lds = kWaves * 4096 + kWaves * S * 16 * kSG + 2 * kWaves * S * RT * 1024;
+  constexpr int lds = lds_fixed(MX, S) + red_buffers(MX, RT, S) * kWaves * S * RT * 1024;
   static_assert(lds <= 160 * 1024, "LDS");
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t e = fp4impl::set_lds_limit_once(
@@ -449,20 +477,21 @@ hipError_t launch_s(const FewArgs& a, bool svec, bool out_bf16, hipStream_t stre
 template <bool MX>
 hipError_t launch_m(const FewArgs& a, int64_t rows, bool svec, bool out_bf16, hipStream_t stream) {
   if (rows <= 16) return launch_s<MX, 1, 4>(a, svec, out_bf16, stream);
-  return launch_s<MX, 2, 2>(a, svec, out_bf16, stream);
+  if (rows <= 32) return launch_s<MX, 2, 4>(a, svec, out_bf16, stream);
+  if constexpr (!MX) return launch_s<MX, 4, 2>(a, svec, out_bf16, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 namespace fp4impl {
 
-// Average rows of a group up to which W's bytes, read once per 16 or 32 rows,
-// cost less than the 256-row tiles of the tile kernels.
-constexpr int64_t kFewRows = 32;
-
-bool few_rows(int64_t ngroups, int64_t M, int64_t N, int64_t K) {
-  (void)N;
-  return K > 0 && M <= kFewRows * (ngroups > 0 ? ngroups : 1);
+// Rows of a group, on average, up to which reading W once per 16, 32 or 64 rows
+// beats the 256-row tiles (us here / tiles; 27648 x 5120 dense, and 64 groups of
+// 4096 x 7168): NVFP4 64 rows 58.7 / 115, 561 / 671; MXFP4 32 rows 26 / 38, 240 /
+// 290, while MXFP4 64 rows took 46 / 39 and 451 / 300.
+bool few_rows(bool mx, int64_t ngroups, int64_t M, int64_t K) {
+  return K > 0 && M <= (mx ? 32 : 64) * (ngroups > 0 ? ngroups : 1);
 }
 
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
@@ -479,7 +508,7 @@ hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, c
                   (int)ngroups, D, f};
   const bool svec = K % 256 == 0 && (reinterpret_cast<uintptr_t>(a_scales) & 15) == 0 &&
                     (reinterpret_cast<uintptr_t>(w_scales) & 15) == 0;
-  const int64_t rows = ngroups > 0 ? M / ngroups : M;
+  const int64_t rows = ngroups > 0 ? (M + ngroups - 1) / ngroups : M;
   return mx ? launch_m<true>(a, rows, svec, out_bf16, stream)
             : launch_m<false>(a, rows, svec, out_bf16, stream);
 }

@@ -47,7 +47,7 @@ hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales,
       ((M + BM - 1) / BM + ngroups) * ((N + BN - 1) / BN) >= (int64_t)1 << 31)
     return hipErrorInvalidValue;
   hipError_t e;
-  if (few_rows(ngroups, M, N, K)) {
+  if (few_rows(mx, ngroups, M, K)) {
     e = launch_few_rows(mx, A, a_scales, g_a, W, w_scales, g_b, g_d, ngroups, offsets, M, N, K, ep, D,
                         out_bf16, stream);
   } else {
