@@ -287,4 +287,21 @@ __device__ __forceinline__ void load_bias(float (&b)[16], const FusedArgs& f, in
   }
 }
 
+// Rows of a grouped output (and its preact) past the last group's -- slots that
+// were dropped -- hold zeros, so that what reads the whole tensor next (a
+// quantizer's amax) sees none of the memory's earlier contents.  Every thread of
+// the launch takes a share; usually there are none.
+__device__ __forceinline__ void zero_tail(const int32_t* __restrict__ offsets, int groups, int M, int N,
+                                          const FusedArgs& f, bool out_bf16, void* D) {
+  const int lo = min(max(offsets[groups], 0), M);
+  if (lo == M) return;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  const int64_t No = f.gated ? N / 2 : N;
+  for (int64_t i = lo * No + first; i < M * No; i += step) store1(D, i, out_bf16, 0.0f);
+  if (f.preact != nullptr)
+    for (int64_t i = lo * (int64_t)N + first; i < M * (int64_t)N; i += step)
+      store1(f.preact, i, f.preact_bf16, 0.0f);
+}
+
 }  // namespace fp4dev

@@ -145,8 +145,7 @@ hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales,
 
 // ---- gemm_few_rows.hip ----------------------------------------------------
 // Whether a fused product has few enough rows per group for launch_few_rows,
-// which computes what launch_fused_gemm does (dense: ngroups 0) except for the
-// rows past the last group.
+// which computes what launch_fused_gemm does (dense: ngroups 0).
 bool few_rows(bool mx, int64_t ngroups, int64_t M, int64_t K);
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
                            const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,

@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
 
   // ---- this workgroup's units
   const bool grouped = a.offsets != nullptr;
+  if (grouped) zero_tail(a.offsets, a.groups, a.M, N, a.f, OUT_BF16, a.D);
   // rows and row chunks of groups c .. c + 63, one per lane
   auto chunk_of = [&](int c, int& lo, int& n, int& inc) {
     const int e = c + lane;

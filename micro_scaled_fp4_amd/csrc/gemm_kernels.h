@@ -586,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // in contiguous ranges; the column tile runs fastest, so the workgroups of an
   // XCD share the row tile of A in its L2
   const int T = GROUPED ? group_row_tiles(goff, ngroups, M) * tiles_n : tiles_m * tiles_n;
+  if constexpr (FUSED && GROUPED) zero_tail(goff, ngroups, M, N, fused, OUT == 2, D);
   int bid = blockIdx.x;
   if (bid >= T) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

@@ -64,24 +64,26 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// e^x to about 2 ulp: the product x log2 e in two floats, its tail applied to
-// the first order after v_exp_f32.
+// e^x, x <= 88, to about 2 ulp: the product x log2 e in two floats, its tail
+// applied to the first order after v_exp_f32.  Below e^-104 (-inf included) 0.
 __device__ __forceinline__ float exp_accurate(float x) {
   constexpr float kL = 0x1.715476p+0f, kLlo = 0x1.4ae0c0p-26f;
+  x = fmaxf(x, -110.0f);
   const float t = x * kL;
-  // (x = -inf or an overflowing t: no tail, which would be inf - inf)
-  const float r = fabsf(t) < 1e30f ? fmaf(x, kLlo, fmaf(x, kL, -t)) : 0.0f;
+  const float r = fmaf(x, kLlo, fmaf(x, kL, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e * r, 0x1.62e430p-1f, e);
 }
+// (v_rcp_f32: 1 ulp.)  Scores below e^-87 count as 0.
 __device__ __forceinline__ float sigmoid_accurate(float x) {
-  // e^-x past the float range gives 1 / inf = 0: scores below 2^-126 count as 0
-  const float e = x < -87.0f ? __builtin_inff() : exp_accurate(-x);
-  return 1.0f / (1.0f + e);
+  const float s = __builtin_amdgcn_rcpf(1.0f + exp_accurate(fminf(-x, 87.0f)));
+  return x < -87.0f ? 0.0f : s;
 }
 
-// Float -> integer that orders like the float (-0 equal to +0); 0 is kept for
-// masked experts and is below every finite value's key.
+// Float -> integer that orders like the float (-0 equal to +0).  Masked experts
+// have -inf's key, kKeyNone, which every finite value's is above; 0, below it, is
+// kept for experts that are taken.
+constexpr uint32_t kKeyNone = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -163,10 +165,52 @@ struct RouteArgs {
   const float* bias;
   int64_t T;
   int E, top_k, sigmoid, groups, top_groups, group_top, renorm, vec;
+  int bias_vec, lane_groups;   // lanes per group, 0: groups of no whole power of two of lanes
   float scale;
   int32_t* ids;
   float* weights;
 };
+
+// Bias of a lane's EPL experts from e0 on (0 without one and past E).
+template <int EPL>
+__device__ __forceinline__ void load_bias_row(const float* bias, int E, int e0, bool vec, float (&b)[EPL]) {
+  if (EPL % 4 == 0 && vec && bias != nullptr && e0 < E) {
+    if constexpr (EPL % 4 == 0) {
+#pragma unroll
+      for (int k = 0; k < EPL / 4; ++k) {
+        const f32x4 v = load4(bias, e0 + 4 * k, false);
+        b[4 * k] = v.x; b[4 * k + 1] = v.y; b[4 * k + 2] = v.z; b[4 * k + 3] = v.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) b[j] = bias != nullptr && e0 + j < E ? bias[e0 + j] : 0.0f;
+  }
+}
+
+// (m1, m2), the two largest of a set, joined with those of another (p1 >= p2)
+__device__ __forceinline__ void top_two(float& m1, float& m2, float p1, float p2) {
+  m2 = fmaxf(fminf(m1, p1), fmaxf(m2, p2));
+  m1 = fmaxf(m1, p1);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float quad_swap1(float v) { return dpp<0xb1>(v); }     // quad_perm [1, 0, 3, 2]
+__device__ __forceinline__ float quad_swap2(float v) { return dpp<0x4e>(v); }     // quad_perm [2, 3, 0, 1]
+__device__ __forceinline__ float half_mirror(float v) { return dpp<0x141>(v); }   // lane 7 - i of each 8
+__device__ __forceinline__ float row_mirror(float v) { return dpp<0x140>(v); }    // lane 15 - i of each 16
+
+// f(k of another lane of the row of 16, that lane) for the 15 other lanes.  Row
+// rotation by R hands lane i the value of lane (i - R) mod 16.
+template <int R = 1, typename F>
+__device__ __forceinline__ void rotations(uint32_t k, int ln, F&& f) {
+  if constexpr (R < 16) {
+    f(ror16<R>(k), (ln - R) & 15);
+    rotations<R + 1>(k, ln, f);
+  }
+}
 
 // ------------------------------------------------------------------ route --
 // A token per L lanes (16, so that a wave routes 4 tokens and reductions stay
@@ -205,22 +249,43 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
   }
   uint32_t key[EPL];
   if (by_score) {
+    float b[EPL];
+    load_bias_row<EPL>(a.bias, E, e0, a.bias_vec, b);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // one division a token, then 1 ulp
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      float v = kNegInf;
-      if (l[j] > kNegInf) {
-        v = a.sigmoid ? sigmoid_accurate(l[j]) : exp_accurate(l[j] - top) / total;
-        if (a.bias != nullptr && e0 + j < E) v += a.bias[e0 + j];
-      }
-      key[j] = v > kNegInf ? order_key(v) : 0u;
-      if (two || a.groups > 1) l[j] = key[j] ? v : kNegInf;   // the selection value from here on
+      const float s = a.sigmoid ? sigmoid_accurate(l[j]) : exp_accurate(l[j] - top) * inv;
+      const float v = s + b[j];                             // NaN: masked, like -inf
+      l[j] = l[j] > kNegInf && v > kNegInf ? v : kNegInf;   // the selection value from here on
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = l[j] > kNegInf ? order_key(l[j]) : 0u;
   }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) key[j] = order_key(l[j]);
 
-  if (a.groups > 1) {
+  if (a.groups > 1 && a.lane_groups > 0) {
+    // a group is lane_groups (1, 2, 4, 8 or 16) whole lanes: its two largest values
+    // in registers, then over the lanes, pairs first
+    float m1 = kNegInf, m2 = kNegInf;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) top_two(m1, m2, l[j], kNegInf);
+    if (a.lane_groups > 1) top_two(m1, m2, quad_swap1(m1), quad_swap1(m2));
+    if (a.lane_groups > 2) top_two(m1, m2, quad_swap2(m1), quad_swap2(m2));
+    if (a.lane_groups > 4) top_two(m1, m2, half_mirror(m1), half_mirror(m2));
+    if (a.lane_groups > 8) top_two(m1, m2, row_mirror(m1), row_mirror(m2));
+    const float mine_s = a.group_top == 2 && m2 > kNegInf ? m1 + m2 : m1;
+    // a group stays when fewer than top_groups are better (equal scores: the lower
+    // index is); the scores pass by, one lane of each group bearing its own
+    const bool bears = (ln & (a.lane_groups - 1)) == 0;
+    const uint32_t mine_k = order_key(mine_s);
+    const uint32_t out_k = bears ? mine_k : 0u;
+    int rank = 0;
+    auto pass = [&](uint32_t k, int from) { rank += k > mine_k || (k == mine_k && from < (ln & -a.lane_groups)); };
+    rotations(out_k, ln, pass);
+    if (rank >= a.top_groups) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = 0u;
+    }
+  } else if (a.groups > 1) {
     float* vs = v_s + tl * (E + 1);
     const int size = E / a.groups;
 #pragma unroll
@@ -239,8 +304,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
       gs_s[tl][g] = a.group_top == 2 && m2 > kNegInf ? m1 + m2 : m1;
     }
     wave_lds_order();
-    // a group stays when fewer than top_groups are better (equal scores: the
-    // lower index is)
+    // (kept as above)
     uint32_t keep = 0;                 // bit i: group ln + i L
     for (int g = ln, i = 0; g < a.groups; g += L, ++i) {
       const float mine = gs_s[tl][g];
@@ -274,17 +338,19 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
     const int src = __ffsll((unsigned long long)(L == 64 ? hit : hit & 0xffffu)) - 1;
     if (ln == src) {
       int e = -1;
-      if (best != 0) {
+      if (best > kKeyNone) {
         int at = 0;
-#pragma unroll
-        for (int j = EPL - 1; j >= 0; --j) at = key[j] == best ? j : at;
-        e = e0 + at;
+        bool taken = false;            // (wave masks: the logic on them is scalar work)
         mine = 0;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-          key[j] = j == at ? 0u : key[j];
+          const bool hit_j = key[j] == best, pick = hit_j && !taken;
+          taken |= hit_j;
+          key[j] = pick ? 0u : key[j];
+          at = pick ? j : at;
           mine = umax(mine, key[j]);
         }
+        e = e0 + at;
       }
       ids_s[tl][r] = e;
     }
@@ -856,11 +922,16 @@ hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, in
                         int group_top, int32_t* ids, float* weights, hipStream_t stream) {
   const int E = (int)p.E;
   RouteArgs a{p.logits, bias, p.T, E, p.top_k, p.sigmoid, groups, top_groups, group_top, p.renorm, 0,
-              p.scale, ids, weights};
+              0, 0, p.scale, ids, weights};
+  const int size = E / groups;
 #define FP4_CALL(EPL, L)                                                                              \
   a.vec = E % EPL == 0 && ok16(p.logits);                                                             \
+  a.bias_vec = E % EPL == 0 && ok16(bias);                                                            \
+  /* (16-lane tokens: rows of DPP; groups of whole lanes, a power of two of them) */                 \
+  const int lg = L == 16 && size % EPL == 0 ? size / EPL : 0;                                         \
+  a.lane_groups = lg > 0 && (lg & (lg - 1)) == 0 ? lg : 0;                                            \
   const int64_t grid = (p.T + kRouteThreads / L - 1) / (kRouteThreads / L);                           \
-  const size_t lds = groups > 1 ? sizeof(float) * (kRouteThreads / L) * (E + 1) : 0;                  \
+  const size_t lds = groups > 1 && a.lane_groups == 0 ? sizeof(float) * (kRouteThreads / L) * (E + 1) : 0;                  \
   if (p.bf16)                                                                                         \
     hipLaunchKernelGGL((k_route<true, EPL, L>), dim3(grid), dim3(kRouteThreads), lds, stream, a);     \
   else                                                                                                \
