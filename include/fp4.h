@@ -509,7 +509,7 @@ fp4_status moe_dispatch(fp4_format fmt, const void* x, fp4_dtype xt, int64_t T, 
  * Slots whose row is outside [0, M) add nothing.
  *   rows [M, H], residual [T, H] or NULL, y out [T, H]: FP4_F32 / FP4_BF16
  *   weights [T, top_k] float32;  slot_rows [T, top_k]
- * 1 <= top_k <= FP4_MOE_MAX_TOPK; T limits as moe_route; H <= FP4_GEMM_MAX_MN;
+ * 1 <= top_k <= FP4_MOE_MAX_TOPK; T limits as moe_route; H <= FP4_GEMM_MAX_K;
  * T * ceil(H / 256) < 2^31.  residual may be y itself (equal types).  Pointers
  * aligned to their element.  T == 0 or H == 0 is a no-op.
  */
@@ -522,7 +522,7 @@ fp4_status moe_combine(const void* rows, fp4_dtype rt, int64_t M, int64_t H, con
  * (M = T * top_k):  d_rows[slot_rows[t][j]] = weights[t][j] * dy[t], zeros for rows
  * of no slot (row_slots[r] < 0);  d_weights[t][j] = <dy[t], rows[slot_rows[t][j]]>
  * in float32, 0 for a dropped slot.  (The residual's gradient is dy.)
- * A row belongs to at most one slot.
+ * A row belongs to at most one slot.  Limits as moe_combine.
  */
 fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows, fp4_dtype rt,
                                 const float* weights, const int32_t* slot_rows,

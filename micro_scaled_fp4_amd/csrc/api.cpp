@@ -630,7 +630,7 @@ fp4_status moe_combine(const void* rows, fp4_dtype rt, int64_t M, int64_t H, con
                        fp4_dtype residual_type, void* y, fp4_dtype yt, hipStream_t stream) {
   if (!valid_dtype(rt) || !valid_dtype(yt) || (residual != nullptr && !valid_dtype(residual_type)))
     return FP4_ERR_DTYPE;
-  if (bad_slots(T, 1, top_k) || M < 0 || M > FP4_GEMM_MAX_MN || H < 0 || H > FP4_GEMM_MAX_MN)
+  if (bad_slots(T, 1, top_k) || M < 0 || M > FP4_GEMM_MAX_MN || H < 0 || H > FP4_GEMM_MAX_K)
     return FP4_ERR_SHAPE;
   if (T * ((H + 255) / 256) >= (int64_t)1 << 31) return FP4_ERR_SHAPE;
   if (T == 0 || H == 0) return FP4_OK;
@@ -653,7 +653,7 @@ fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows,
                                 const int32_t* row_slots, int64_t T, int top_k, int64_t H,
                                 void* d_rows, fp4_dtype drt, float* d_weights, hipStream_t stream) {
   if (!valid_dtype(dyt) || !valid_dtype(rt) || !valid_dtype(drt)) return FP4_ERR_DTYPE;
-  if (bad_slots(T, 1, top_k) || H < 0 || H > FP4_GEMM_MAX_MN) return FP4_ERR_SHAPE;
+  if (bad_slots(T, 1, top_k) || H < 0 || H > FP4_GEMM_MAX_K) return FP4_ERR_SHAPE;
   if (T == 0) return FP4_OK;
   if (weights == nullptr || slot_rows == nullptr || row_slots == nullptr || d_weights == nullptr)
     return FP4_ERR_NULL;

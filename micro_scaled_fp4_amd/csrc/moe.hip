@@ -10,6 +10,7 @@
 #include "epilogue.h"
 #include "fp4_device.h"
 #include "fp4_internal.h"
+#include "scale_bytes.h"
 
 using namespace fp4dev;
 
@@ -464,23 +465,33 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteGradArgs a) {
 
 // ------------------------------------------------------------------- sort --
 // Stable counting sort of the n = T top_k slots by expert id.  Workgroup c owns
-// the kChunk slots from c kChunk on: k_count writes its histogram, k_place sums
+// the `chunk` slots from c chunk on: k_count writes its histogram, k_place sums
 // the histograms before it (and over all, for the offsets) and ranks its own
 // slots, kSortThreads at a time: inside a wave by matching ids over their bits
 // (a ballot per bit), across waves by per-wave counts in LDS.  One chunk needs
 // no histograms from elsewhere: k_place counts for itself.  Ids outside [0, E)
-// have no row.
+// have no row.  Up to kOneChunk slots go in one chunk (a launch less); more in
+// chunks of kSortThreads slots, or of as many as make kMaxChunks chunks, since
+// every workgroup reads all histograms (32768 slots: k_place 10.6 us in chunks of
+// 4096, 5.1 in chunks of 1024).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kChunk = 4096;
+constexpr int kOneChunk = 4096;
+constexpr int kMaxChunks = 512;
 constexpr int kMaxExperts = 1024;    // FP4_MOE_MAX_EXPERTS
 
-__device__ __forceinline__ void count_chunk(const int32_t* __restrict__ ids, int64_t n, int64_t c, int E,
-                                            int* hist) {
+inline int64_t sort_chunk(int64_t n) {
+  if (n <= kOneChunk) return kOneChunk;
+  const int64_t per = (int64_t)kSortThreads * kMaxChunks;
+  return (n + per - 1) / per * kSortThreads;
+}
+
+__device__ __forceinline__ void count_chunk(const int32_t* __restrict__ ids, int64_t n, int64_t c, int chunk,
+                                            int E, int* hist) {
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < kChunk; i += blockDim.x) {
-    const int64_t s = c * kChunk + i;
+  for (int i = threadIdx.x; i < chunk; i += blockDim.x) {
+    const int64_t s = c * chunk + i;
     const int id = s < n ? ids[s] : -1;
     if (id >= 0 && id < E) atomicAdd(&hist[id], 1);   // LDS; a sum of ones has no order
   }
@@ -523,7 +534,7 @@ __device__ __forceinline__ uint32_t amax_part(const void* __restrict__ x, int64_
 struct PlaceArgs {
   const int32_t* ids;
   int64_t n;
-  int E, chunks;
+  int E, chunk, chunks;
   const int* counts;       // [chunks][E] (chunks > 1)
   int32_t* offsets;        // [E + 1]
   int32_t* slot_rows;      // [n]
@@ -539,14 +550,16 @@ __device__ __forceinline__ void place_chunk(const PlaceArgs& a, int64_t c) {
   const int E = a.E;
   int mine = 0, before = 0;                        // expert tid: all rows, and those of earlier chunks
   if (a.chunks > 1) {
-    if (tid < E)
+    if (tid < E) {
+#pragma unroll 8
       for (int k = 0; k < a.chunks; ++k) {
         const int v = a.counts[(int64_t)k * E + tid];
-        if (k < c) before += v;
+        before += k < c ? v : 0;
         mine += v;
       }
+    }
   } else {
-    count_chunk(a.ids, a.n, 0, E, start);
+    count_chunk(a.ids, a.n, 0, a.chunk, E, start);
     if (tid < E) mine = start[tid];
   }
   // exclusive scan of the experts' rows
@@ -571,10 +584,10 @@ __device__ __forceinline__ void place_chunk(const PlaceArgs& a, int64_t c) {
     for (int64_t r = (int64_t)all + tid; r < a.n; r += kSortThreads) a.row_slots[r] = -1;
   }
   const int bits = 32 - __clz(E);                  // ids 0 .. E (E: no expert)
-  for (int i0 = 0; i0 < kChunk && c * kChunk + i0 < a.n; i0 += kSortThreads) {
+  for (int i0 = 0; i0 < a.chunk && c * a.chunk + i0 < a.n; i0 += kSortThreads) {
     for (int e = tid; e < kSortWaves * kMaxExperts / 2; e += kSortThreads)
       reinterpret_cast<uint32_t*>(&wave_n[0][0])[e] = 0;
-    const int64_t s = c * kChunk + i0 + tid;
+    const int64_t s = c * a.chunk + i0 + tid;
     int id = s < a.n ? a.ids[s] : -1;
     const bool live = id >= 0 && id < E;
     if (!live) id = E;
@@ -617,7 +630,7 @@ __global__ void __launch_bounds__(kSortThreads)
     if (a.chunks == 1) {
       place_chunk(a, 0);
     } else {
-      count_chunk(a.ids, a.n, blockIdx.x, a.E, hist);
+      count_chunk(a.ids, a.n, blockIdx.x, a.chunk, a.E, hist);
       for (int e = threadIdx.x; e < a.E; e += kSortThreads) counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
     }
     return;
@@ -802,35 +815,110 @@ __device__ __forceinline__ void store_vals(void* p, int64_t i, bool bf16, const 
     store1(p, i, bf16, v[0]);
 }
 
+// the same past the caches, for what nothing reads soon
+template <int V>
+__device__ __forceinline__ void stream_vals(void* p, int64_t i, bool bf16, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    if (bf16) {
+      __builtin_nontemporal_store(u32x4{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]),
+                                        bf16_pack2(v[6], v[7])},
+                                  reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + i));
+    } else {
+      f32x4* q = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i);
+      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, q);
+      __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, q + 1);
+    }
+  } else {
+    store1(p, i, bf16, v[0]);
+  }
+}
+
 constexpr int kCombineThreads = 256;
+constexpr int kSlotBatch = 8;        // slots whose rows are in flight together
+
+// One slot's row: a descriptor of its H values, empty for a dropped slot (loads
+// through it read zeros, with no branch around them), and its weight, 0 then.
+struct SlotRow {
+  __amdgpu_buffer_rsrc_t rsrc;
+  float w;
+  int row;                           // -1: dropped
+};
+__device__ __forceinline__ SlotRow slot_row(const void* rows, bool bf16, int64_t M, int H,
+                                            const int32_t* slot_rows, const float* weights, int64_t slot,
+                                            bool exists) {
+  int row = exists ? slot_rows[slot] : -1;
+  if (row >= M) row = -1;
+  const int bytes = H * (bf16 ? 2 : 4);
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(rows) + (int64_t)max(row, 0) * bytes;
+  return {__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, row >= 0 ? bytes : 0, kBufferWord3),
+          row >= 0 ? weights[slot] : 0.0f, row};
+}
+// V values from column h on, as loaded (V 8: 16 or 32 bytes; V 1: one element)
+template <int V>
+struct RowRaw {
+  u32x4 v[V == 8 ? 2 : 1];
+};
+constexpr int kLoadNT = 2;           // buffer load cache policy: nontemporal
+template <int V>
+__device__ __forceinline__ void load_row(RowRaw<V>& r, const SlotRow& s, int h, bool bf16) {
+  if constexpr (V == 8) {
+    r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(s.rsrc, h * (bf16 ? 2 : 4), 0, kLoadNT);
+    if (!bf16) r.v[1] = __builtin_amdgcn_raw_buffer_load_b128(s.rsrc, h * 4 + 16, 0, kLoadNT);
+  } else {
+    r.v[0].x = bf16 ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(s.rsrc, h * 2, 0, 0) << 16
+                    : __builtin_amdgcn_raw_buffer_load_b32(s.rsrc, h * 4, 0, 0);
+  }
+}
+template <int V>
+__device__ __forceinline__ void row_values(float (&v)[V], const RowRaw<V>& r, bool bf16) {
+  if constexpr (V == 8) {
+    if (bf16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = bf16_lo(r.v[0][q]);
+        v[2 * q + 1] = bf16_hi(r.v[0][q]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r.v[q >> 2][q & 3]);
+    }
+  } else {
+    v[0] = __uint_as_float(r.v[0].x);
+  }
+}
 
 // y[t] = sum over slots of weight * row (+ residual), float32 in slot order; a
 // workgroup per piece of a token's columns, so the slots' rows and weights are
-// uniform and the loads of all slots are in flight together.
-template <int V>
+// uniform and the rows of kSlotBatch slots are in flight together.  HBM bound.
+template <int V, bool ROWS_BF16>
 __global__ void __launch_bounds__(kCombineThreads) k_combine(CombineArgs a, int pieces) {
   const int64_t t = blockIdx.x / pieces;
   const int h = ((int)(blockIdx.x - t * pieces) * kCombineThreads + (int)threadIdx.x) * V;
   if (h >= a.H) return;
-  float acc[V];
+  float acc[V], res[V];
 #pragma unroll
-  for (int q = 0; q < V; ++q) acc[q] = 0.0f;
-#pragma unroll 8
-  for (int j = 0; j < a.top_k; ++j) {
-    const int row = a.slot_rows[t * a.top_k + j];
-    if (row < 0 || row >= a.M) continue;
-    const float w = a.weights[t * a.top_k + j];
-    float v[V];
-    load_vals<V>(a.rows, (int64_t)row * a.H + h, a.rows_bf16, v);
+  for (int q = 0; q < V; ++q) acc[q] = res[q] = 0.0f;
+  if (a.residual != nullptr) load_vals<V>(a.residual, t * a.H + h, a.res_bf16, res);
+  for (int j0 = 0; j0 < a.top_k; j0 += kSlotBatch) {
+    float w[kSlotBatch];
+    RowRaw<V> raw[kSlotBatch];
 #pragma unroll
-    for (int q = 0; q < V; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    for (int j = 0; j < kSlotBatch; ++j) {
+      const SlotRow s = slot_row(a.rows, ROWS_BF16, a.M, a.H, a.slot_rows, a.weights,
+                                 t * a.top_k + j0 + j, j0 + j < a.top_k);
+      w[j] = s.w;
+      load_row<V>(raw[j], s, h, ROWS_BF16);
+    }
+#pragma unroll
+    for (int j = 0; j < kSlotBatch; ++j) {
+      float v[V];
+      row_values<V>(v, raw[j], ROWS_BF16);
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[q] = fmaf(w[j], v[q], acc[q]);
+    }
   }
-  if (a.residual != nullptr) {
-    float v[V];
-    load_vals<V>(a.residual, t * a.H + h, a.res_bf16, v);
 #pragma unroll
-    for (int q = 0; q < V; ++q) acc[q] += v[q];
-  }
+  for (int q = 0; q < V; ++q) acc[q] += res[q];
   store_vals<V>(a.y, t * a.H + h, a.y_bf16, acc);
 }
 
@@ -850,7 +938,7 @@ struct CombineGradArgs {
 // token reads dy once for all its slots; the dot products are summed per thread
 // over its columns, then over lanes and waves in a fixed order.  Rows of no
 // slot get zeros.
-template <int V>
+template <int V, bool ROWS_BF16>
 __global__ void __launch_bounds__(kCombineThreads) k_combine_grad(CombineGradArgs a) {
   __shared__ float red[kCombineThreads / 64][kMaxTopK];
   const int64_t t = blockIdx.x;
@@ -862,19 +950,26 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine_grad(CombineGradArg
     float dy[V];
     load_vals<V>(a.dy, t * a.H + h, a.dy_bf16, dy);
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= k) break;
-      const int row = a.slot_rows[t * k + j];
-      if (row < 0 || row >= a.M) continue;
-      const float w = a.weights[t * k + j];
-      float v[V], d[V];
-      load_vals<V>(a.rows, (int64_t)row * a.H + h, a.rows_bf16, v);
+    for (int j0 = 0; j0 < kMaxTopK; j0 += kSlotBatch) {
+      if (j0 >= k) break;
+      SlotRow s[kSlotBatch];
+      RowRaw<V> raw[kSlotBatch];
 #pragma unroll
-      for (int q = 0; q < V; ++q) {
-        dot[j] = fmaf(dy[q], v[q], dot[j]);
-        d[q] = w * dy[q];
+      for (int j = 0; j < kSlotBatch; ++j) {
+        s[j] = slot_row(a.rows, ROWS_BF16, a.M, a.H, a.slot_rows, a.weights, t * k + j0 + j, j0 + j < k);
+        load_row<V>(raw[j], s[j], h, ROWS_BF16);
       }
-      store_vals<V>(a.d_rows, (int64_t)row * a.H + h, a.dr_bf16, d);
+#pragma unroll
+      for (int j = 0; j < kSlotBatch; ++j) {
+        float v[V], d[V];
+        row_values<V>(v, raw[j], ROWS_BF16);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          dot[j0 + j] = fmaf(dy[q], v[q], dot[j0 + j]);
+          d[q] = s[j].w * dy[q];
+        }
+        if (s[j].row >= 0) stream_vals<V>(a.d_rows, (int64_t)s[j].row * a.H + h, a.dr_bf16, d);
+      }
     }
   }
 #pragma unroll
@@ -960,7 +1055,7 @@ hipError_t launch_route_grad(const RouteProblem& p, const float* dw, const int32
 
 // Workspace: kAmaxPartials partial maxima of x | histograms [chunks][E].
 size_t dispatch_workspace_bytes(int64_t n, int64_t E) {
-  const int64_t chunks = (n + kChunk - 1) / kChunk;
+  const int64_t chunk = sort_chunk(n), chunks = (n + chunk - 1) / chunk;
   return (size_t)kAmaxPartials * 4 + (chunks > 1 ? (size_t)chunks * E * 4 : 0);
 }
 
@@ -971,7 +1066,7 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
                        p.mx || p.amax_in != nullptr ? nullptr : p.amax_out, p.mx ? nullptr : p.scale_out);
     return hipGetLastError();
   }
-  const int64_t chunks = (n + kChunk - 1) / kChunk;
+  const int64_t chunk = sort_chunk(n), chunks = (n + chunk - 1) / chunk;
   uint32_t* partials = static_cast<uint32_t*>(p.workspace);
   int* counts = reinterpret_cast<int*>(partials + kAmaxPartials);
   const bool need_amax = !p.mx && p.amax_in == nullptr;
@@ -984,7 +1079,7 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
     const int64_t most = min((int64_t)kAmaxPartials, (int64_t)2 * num_cus());
     npart = (int)(want < most ? want : most);
   }
-  const PlaceArgs a{p.ids, n, (int)p.E, (int)chunks, counts, p.offsets, p.slot_rows, p.row_slots};
+  const PlaceArgs a{p.ids, n, (int)p.E, (int)chunk, (int)chunks, counts, p.offsets, p.slot_rows, p.row_slots};
   const dim3 grid((unsigned)(chunks + npart));
   if (p.bf16)
     hipLaunchKernelGGL((k_count<true>), grid, dim3(kSortThreads), 0, stream, a, counts, (int)chunks, p.x,
@@ -1027,10 +1122,14 @@ hipError_t launch_combine(const void* rows, bool rows_bf16, int64_t M, int64_t H
   const int64_t per = (int64_t)kCombineThreads * (vec ? 8 : 1);
   const int64_t pieces = (H + per - 1) / per;
   if (T * pieces >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  if (vec)
-    hipLaunchKernelGGL((k_combine<8>), dim3(T * pieces), dim3(kCombineThreads), 0, stream, a, (int)pieces);
-  else
-    hipLaunchKernelGGL((k_combine<1>), dim3(T * pieces), dim3(kCombineThreads), 0, stream, a, (int)pieces);
+#define FP4_COMBINE(VV, BF) \
+  hipLaunchKernelGGL((k_combine<VV, BF>), dim3(T * pieces), dim3(kCombineThreads), 0, stream, a, (int)pieces)
+  if (vec) {
+    if (rows_bf16) FP4_COMBINE(8, true); else FP4_COMBINE(8, false);
+  } else {
+    if (rows_bf16) FP4_COMBINE(1, true); else FP4_COMBINE(1, false);
+  }
+#undef FP4_COMBINE
   return hipGetLastError();
 }
 
@@ -1041,10 +1140,13 @@ hipError_t launch_combine_grad(const void* dy, bool dy_bf16, const void* rows, b
   const CombineGradArgs a{dy, rows, weights, slot_rows, row_slots, T, M, (int)H, top_k, dy_bf16,
                           rows_bf16, dr_bf16, d_rows, d_weights};
   const bool vec = H % 8 == 0 && ok16(dy) && ok16(rows) && ok16(d_rows);
-  if (vec)
-    hipLaunchKernelGGL((k_combine_grad<8>), dim3(T), dim3(kCombineThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((k_combine_grad<1>), dim3(T), dim3(kCombineThreads), 0, stream, a);
+#define FP4_COMBINE(VV, BF) hipLaunchKernelGGL((k_combine_grad<VV, BF>), dim3(T), dim3(kCombineThreads), 0, stream, a)
+  if (vec) {
+    if (rows_bf16) FP4_COMBINE(8, true); else FP4_COMBINE(8, false);
+  } else {
+    if (rows_bf16) FP4_COMBINE(1, true); else FP4_COMBINE(1, false);
+  }
+#undef FP4_COMBINE
   return hipGetLastError();
 }
 
