@@ -144,13 +144,14 @@ hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales,
                              const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream);
 
 // ---- gemm_few_rows.hip ----------------------------------------------------
-// Whether a fused product has few enough rows per group for launch_few_rows,
-// which computes what launch_fused_gemm does (dense: ngroups 0).
-bool few_rows(bool mx, int64_t ngroups, int64_t M, int64_t K);
+// Rows of an item (16, 32 or 64) with which launch_few_rows is expected to be
+// faster than the tile kernels, or 0.
+int few_rows(bool mx, int64_t ngroups, int64_t M, int64_t N, int64_t K);
+// What launch_fused_gemm does (dense: ngroups 0), `item` rows at a time.
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
                            const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
                            int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
-                           const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream);
+                           const Epilogue& ep, void* D, bool out_bf16, int item, hipStream_t stream);
 
 // ---- epilogue_grad.hip ----------------------------------------------------
 size_t epilogue_grad_workspace_bytes(int64_t groups, int64_t M, int64_t N);

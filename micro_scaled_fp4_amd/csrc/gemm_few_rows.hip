@@ -476,42 +476,69 @@ hipError_t launch_s(const FewArgs& a, bool svec, bool out_bf16, hipStream_t stre
 }
 
 template <bool MX>
-hipError_t launch_m(const FewArgs& a, int64_t rows, bool svec, bool out_bf16, hipStream_t stream) {
-  if (rows <= 16) return launch_s<MX, 1, 4>(a, svec, out_bf16, stream);
-  if (rows <= 32) return launch_s<MX, 2, 4>(a, svec, out_bf16, stream);
-  if constexpr (!MX) return launch_s<MX, 4, 2>(a, svec, out_bf16, stream);
-  return hipErrorInvalidValue;
+hipError_t launch_m(const FewArgs& a, int item, bool svec, bool out_bf16, hipStream_t stream) {
+  if (item == 16) return launch_s<MX, 1, 4>(a, svec, out_bf16, stream);
+  if (item == 32) return launch_s<MX, 2, 4>(a, svec, out_bf16, stream);
+  return launch_s<MX, 4, 2>(a, svec, out_bf16, stream);
 }
 
 }  // namespace
 
 namespace fp4impl {
 
-// Rows of a group, on average, up to which reading W once per 16, 32 or 64 rows
-// beats the 256-row tiles (us here / tiles; 27648 x 5120 dense, and 64 groups of
-// 4096 x 7168): NVFP4 64 rows 58.7 / 115, 561 / 671; MXFP4 32 rows 26 / 38, 240 /
-// 290, while MXFP4 64 rows took 46 / 39 and 451 / 300.
-bool few_rows(bool mx, int64_t ngroups, int64_t M, int64_t K) {
-  return K > 0 && M <= (mx ? 32 : 64) * (ngroups > 0 ? ngroups : 1);
+// Waves that split K: at least two pairs each, so that the partial tiles'
+// exchange is small beside the stream.
+inline int k_split(int64_t K) {
+  const int64_t P = (K + 255) / 256;
+  return P >= 16 ? 8 : P >= 8 ? 4 : P >= 4 ? 2 : 1;
+}
+
+// Which kernel: the modelled time of this one (16-, 32- or 64-row items) against
+// the 256 x 256 tiles', both from measured steps.
+//   here: a workgroup's granules, rounded up to its units, times K and the time of
+//     one strip's value of K (fs; 64 groups of 4096 x 7168: NVFP4 185 / 294 / 540
+//     us at 16 / 32 / 64 rows, MXFP4 157 / 238 / 451);
+//   tiles: rounds of tiles over the device times stages of 256 values (NVFP4 5.8,
+//     MXFP4 2.2 us a stage: 1021 x 5120 x 7168 in 162 and 61 us).
+// E.g. 64 x 27648 x 5120 NVFP4 59 us here, 115 in tiles; 128 x 512 x 4096 11.5 and
+// 94; MXFP4 64 x 27648 x 5120 46 and 39.  Groups are taken as equally full (their
+// sizes are on the device).  Returns the rows of an item, 0 for tiles.
+int few_rows(bool mx, int64_t ngroups, int64_t M, int64_t N, int64_t K) {
+  if (K == 0) return 0;
+  const int64_t groups = ngroups > 0 ? ngroups : 1, rows = (M + groups - 1) / groups, ncu = num_cus();
+  const double stage = mx ? 2.2e9 : 5.8e9;      // fs
+  const double tiles = (double)(groups * ((rows + 255) / 256)) * ((N + 255) / 256);
+  double best = (double)(int64_t)((tiles + ncu - 1) / ncu) * ((K + 255) / 256) * stage;
+  int item = 0;
+  const int slots = kWaves / k_split(K);
+  for (int rt = 1; rt <= 4; rt *= 2) {
+    const double strip = mx ? (rt == 1 ? 0.34e6 : rt == 2 ? 0.52e6 : 0.98e6)
+                            : (rt == 1 ? 0.40e6 : rt == 2 ? 0.64e6 : 1.20e6);
+    const int S = rt == 4 ? 2 : 4;
+    const int64_t items = groups * ((rows + 16 * rt - 1) / (16 * rt));
+    const double granules = (double)items * ((N + 16 * slots - 1) / (16 * slots));
+    const double units = (double)(int64_t)((granules + ncu * S - 1) / (ncu * S));
+    const double t = units * S * slots * K * strip;
+    if (t < best) {
+      best = t;
+      item = 16 * rt;
+    }
+  }
+  return item;
 }
 
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
                            const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
                            int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
-                           const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream) {
+                           const Epilogue& ep, void* D, bool out_bf16, int item, hipStream_t stream) {
   const FusedArgs f{ep.bias, ep.residual, ep.preact, ep.bias_bf16, ep.residual_bf16, ep.preact_bf16,
                     ep.activation, ep.gated, 0};
-  // waves that split K: at least two pairs each, so that the partial tiles'
-  // exchange is small beside the stream
-  const int64_t P = (K + 255) / 256;
-  const int ks = P >= 16 ? 8 : P >= 8 ? 4 : P >= 4 ? 2 : 1;
-  const FewArgs a{A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, ks, offsets,
+  const FewArgs a{A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, k_split(K), offsets,
                   (int)ngroups, D, f};
   const bool svec = K % 256 == 0 && (reinterpret_cast<uintptr_t>(a_scales) & 15) == 0 &&
                     (reinterpret_cast<uintptr_t>(w_scales) & 15) == 0;
-  const int64_t rows = ngroups > 0 ? (M + ngroups - 1) / ngroups : M;
-  return mx ? launch_m<true>(a, rows, svec, out_bf16, stream)
-            : launch_m<false>(a, rows, svec, out_bf16, stream);
+  return mx ? launch_m<true>(a, item, svec, out_bf16, stream)
+            : launch_m<false>(a, item, svec, out_bf16, stream);
 }
 
 }  // namespace fp4impl

@@ -30,9 +30,9 @@ hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales,
   if (M > (1 << 30) || N > (1 << 30) || K >= (1 << 23) || ngroups > (1 << 20) ||
       ((M + BM - 1) / BM + ngroups) * ((N + BN - 1) / BN) >= (int64_t)1 << 31)
     return hipErrorInvalidValue;
-  if (few_rows(mx, ngroups, M, K))
+  if (const int item = few_rows(mx, ngroups, M, N, K))
     return launch_few_rows(mx, A, a_scales, g_a, W, w_scales, g_b, g_d, ngroups, offsets, M, N, K, ep, D,
-                           out_bf16, stream);
+                           out_bf16, item, stream);
   FusedArgs f{ep.bias, ep.residual, ep.preact, ep.bias_bf16, ep.residual_bf16, ep.preact_bf16,
               ep.activation, ep.gated, 0};
   auto ok16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
