@@ -427,8 +427,9 @@ fp4_status fp4_grouped_gemm_fused(fp4_format fmt, const uint8_t* A, const uint8_
  *              outside every group get no dz; or NULL with num_groups == 1
  *   dbias      out float32, or NULL (then the workspace may be NULL)
  *   workspace  >= fp4_epilogue_backward_workspace_bytes bytes, 4-byte aligned
- * M, N <= FP4_GEMM_MAX_MN, num_groups <= FP4_GROUPED_MAX_GROUPS.  N == 0 is a
- * no-op; M == 0 writes dbias = 0.
+ * M, N <= FP4_GEMM_MAX_MN, num_groups <= FP4_GROUPED_MAX_GROUPS and num_groups *
+ * ceil(N / 512) < 2^28, else FP4_ERR_SHAPE.  N == 0 is a no-op; M == 0 writes
+ * dbias = 0.  dz may be z itself (equal types).
  */
 size_t fp4_epilogue_backward_workspace_bytes(int64_t num_groups, int64_t M, int64_t N);
 fp4_status fp4_epilogue_backward(const void* dD, fp4_dtype dD_type, const void* z, fp4_dtype z_type,

@@ -523,6 +523,7 @@ fp4_status fp4_epilogue_backward(const void* dD, fp4_dtype dD_type, const void* 
   if (gated != 0 && (gated != 1 || N % 2 != 0)) return FP4_ERR_SHAPE;
   if (num_groups < 1 || num_groups > FP4_GROUPED_MAX_GROUPS || (offsets == nullptr && num_groups != 1))
     return FP4_ERR_SHAPE;
+  if (num_groups * ((N + 511) / 512) >= (int64_t)1 << 28) return FP4_ERR_SHAPE;
   if (N == 0 || (M == 0 && dbias == nullptr)) return FP4_OK;
   if (M > 0 && (dD == nullptr || z == nullptr || dz == nullptr)) return FP4_ERR_NULL;
   if (dbias != nullptr &&

@@ -128,6 +128,16 @@ def test_more_tiles_than_compute_units(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,N,K,gated,pre", [(3001, 2995, 544, False, BF), (2900, 3008, 1088, True, F32),
+                                             (2817, 3010, 800, True, None)])
+def test_tile_sizes(fmt, M, N, K, gated, pre):
+    """Sizes that the 256 x 256 tiles take, with edges in every direction."""
+    announce(f"fused gemm tiles {fmt} {M}x{N}x{K}")
+    run_dense(fmt, M, N, K, ref.SILU, gated, BF, F32, F32, pre, M)
+    run_dense(fmt, M, N, K, ref.GELU_TANH, gated, None, BF, BF, None, N)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
 def test_equals_the_plain_gemm_without_an_epilogue(fmt):
     f = fp4.FP4_NVFP4 if fmt == "nv" else fp4.FP4_MXFP4
     M, N, K = 300, 304, 768
@@ -182,7 +192,7 @@ def test_empty_contraction_and_empty_sizes():
 # ---------------------------------------------------------------- grouped ----
 GROUPS = [([1], 16, 32), ([0, 1, 3, 0, 16, 17], 130, 320), ([2] * 60, 272, 1024), ([5, 0, 33, 64, 65, 1, 0], 96, 544),
           ([300], 96, 256), ([0, 17, 256, 300], 258, 1056), ([40, 0, 1, 513, 77, 0, 255, 256], 520, 512), ([0, 0], 32, 64),
-          ([1] * 100 + [31], 64, 7168)]
+          ([1] * 100 + [31], 64, 7168), ([700, 0, 1, 513, 900, 255, 256, 300], 3006, 544)]
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
