@@ -487,10 +487,10 @@ def _epilogue_args(M, N, activation, gated, bias, bias_shape, residual, preact_d
     bias, bt = _part(bias, bias_shape, "bias")
     residual, rt = _part(residual, (M, No), "residual")
     if out is None:
-        out = torch.empty((M, No), dtype=out_dtype, device=dev)
+        out = torch.empty(M, No, dtype=out_dtype, device=dev)
     elif tuple(out.shape) != (M, No) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous [{M}, {No}]")
-    z = None if preact_dtype is None else torch.empty((M, N), dtype=preact_dtype, device=dev)
+    z = None if preact_dtype is None else torch.empty(M, N, dtype=preact_dtype, device=dev)
     zt = FP4_F32 if z is None else _dtype_code(preact_dtype)
     args = (int(activation), int(bool(gated)), _ptr(bias), bt, _ptr(residual), rt, _ptr(z), zt, _ptr(out),
             _dtype_code(out.dtype), _stream(dev))
@@ -592,7 +592,7 @@ def fp4_epilogue_backward(dD: torch.Tensor, z: torch.Tensor, activation: int, ga
         offsets = offsets.contiguous()
         E = offsets.numel() - 1
     lib = load_library()
-    dz = torch.empty((M, N), dtype=out_dtype, device=dev)
+    dz = torch.empty(M, N, dtype=out_dtype, device=dev)
     dbias = None
     if bias_grad:
         dbias = torch.empty((N,) if offsets is None else (E, N), dtype=torch.float32, device=dev)
@@ -615,8 +615,8 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = FP4_SCORE_SOFTMAX,
     T, E = logits.shape
     _same_device(dev, bias=bias)
     bias = _typed(bias, torch.float32, (E,), "bias")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=dev)
     st = load_library().moe_route(_ptr(logits), _dtype_code(logits.dtype), T, E, int(top_k), int(score),
                                   _ptr(bias), int(num_groups), int(top_groups), int(group_top),
                                   int(bool(renormalize)), float(scale), _ptr(ids), _ptr(weights),
@@ -638,7 +638,7 @@ def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, ids: torch
     k = ids.shape[1]
     ids = _typed(ids, torch.int32, (T, k), "ids")
     d_weights = _typed(d_weights, torch.float32, (T, k), "d_weights")
-    dl = torch.empty((T, E), dtype=out_dtype or logits.dtype, device=dev)
+    dl = torch.empty(T, E, dtype=out_dtype or logits.dtype, device=dev)
     st = load_library().moe_route_backward(_ptr(d_weights), _ptr(logits), _dtype_code(logits.dtype),
                                            _ptr(ids), T, E, k, int(score), int(bool(renormalize)),
                                            float(scale), _ptr(dl), _dtype_code(dl.dtype), _stream(dev))
@@ -661,10 +661,10 @@ def moe_dispatch(fmt: int, x: torch.Tensor, ids: torch.Tensor, num_experts: int,
     ids = _typed(ids, torch.int32, (T, k), "ids")
     nv = fmt == FP4_NVFP4
     bs = NV_BLOCK if nv else MX_BLOCK
-    q = torch.empty((T * k, H // 2), dtype=torch.uint8, device=dev)
-    sc = torch.empty((T * k, H // bs), dtype=torch.uint8, device=dev)
+    q = torch.empty(T * k, H // 2, dtype=torch.uint8, device=dev)
+    sc = torch.empty(T * k, H // bs, dtype=torch.uint8, device=dev)
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    slot_rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+    slot_rows = torch.empty(T, k, dtype=torch.int32, device=dev)
     row_slots = torch.empty(T * k, dtype=torch.int32, device=dev)
     a = _amax_arg(amax, dev)
     given = a is not None
@@ -695,7 +695,7 @@ def moe_combine(rows: torch.Tensor, weights: torch.Tensor, slot_rows: torch.Tens
     weights = _typed(weights, torch.float32, (T, k), "weights")
     slot_rows = _typed(slot_rows, torch.int32, (T, k), "slot_rows")
     residual, rt = _part(residual, (T, H), "residual")
-    y = torch.empty((T, H), dtype=out_dtype, device=dev)
+    y = torch.empty(T, H, dtype=out_dtype, device=dev)
     st = load_library().moe_combine(_ptr(rows), _dtype_code(rows.dtype), M, H, _ptr(weights),
                                     _ptr(slot_rows), T, k, _ptr(residual), rt, _ptr(y),
                                     _dtype_code(out_dtype), _stream(dev))
@@ -720,7 +720,7 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, weights: torch.Te
     slot_rows = _typed(slot_rows, torch.int32, (T, k), "slot_rows")
     row_slots = _typed(row_slots, torch.int32, (T * k,), "row_slots")
     d_rows = torch.empty(rows.shape, dtype=out_dtype or rows.dtype, device=dev)
-    d_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    d_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
     st = load_library().moe_combine_backward(_ptr(dy), _dtype_code(dy.dtype), _ptr(rows),
                                              _dtype_code(rows.dtype), _ptr(weights), _ptr(slot_rows),
                                              _ptr(row_slots), T, k, H, _ptr(d_rows),

@@ -205,7 +205,8 @@ hipError_t launch_epilogue_grad(const void* dD, bool dD_bf16, const void* z, boo
   const int64_t splits = grad_splits(groups, M, N);
   const int64_t per = 64 * (vec ? 8 : 2), col_wgs = (N + per - 1) / per;
   if (groups * splits * col_wgs >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  float* partials = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
+  // (one split: its sums are the gradient)
+  float* partials = dbias == nullptr ? nullptr : splits == 1 ? dbias : static_cast<float*>(workspace);
   const GradArgs a{dD, z, dz, partials, offsets, dD_bf16, z_bf16, dz_bf16, M, (int)N, (int)groups,
                    (int)splits, gated, activation, (int)col_wgs};
   const dim3 grid((unsigned)(groups * splits * col_wgs));
@@ -214,7 +215,7 @@ hipError_t launch_epilogue_grad(const void* dD, bool dD_bf16, const void* z, boo
   else
     hipLaunchKernelGGL((k_epilogue_grad<2>), grid, dim3(kGradThreads), 0, stream, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || dbias == nullptr) return e;
+  if (e != hipSuccess || dbias == nullptr || splits == 1) return e;
   const int64_t cols = groups * N;
   hipLaunchKernelGGL(k_bias_grad, dim3((unsigned)((cols + 63) / 64)),
                      dim3(kGradThreads), 0, stream, partials, (int)splits, cols, (int)N, dbias);

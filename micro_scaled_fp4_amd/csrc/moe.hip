@@ -541,8 +541,12 @@ struct PlaceArgs {
   int32_t* row_slots;      // [n]
 };
 
-// Chunk c of the placement; every thread of the workgroup (kSortThreads) takes part.
-__device__ __forceinline__ void place_chunk(const PlaceArgs& a, int64_t c) {
+// Chunk c of the placement; every thread of the workgroup (kSortThreads) takes
+// part.  write: the index arrays are written (else another workgroup does); rows:
+// the rows of the chunk's first kSortThreads slots in LDS, or NULL.  Returns the
+// number of rows.
+__device__ __forceinline__ int place_chunk(const PlaceArgs& a, int64_t c, bool write = true,
+                                           int* rows = nullptr) {
   __shared__ int start[kMaxExperts];               // next row of each expert
   __shared__ int wsum[kSortWaves];
   __shared__ uint16_t wave_n[kSortWaves][kMaxExperts];
@@ -578,7 +582,7 @@ __device__ __forceinline__ void place_chunk(const PlaceArgs& a, int64_t c) {
     all += wsum[w];
   }
   if (tid < E) start[tid] = base + inc - mine + before;
-  if (c == 0) {
+  if (c == 0 && write) {
     if (tid < E) a.offsets[tid] = base + inc - mine;
     if (tid == 0) a.offsets[E] = all;
     for (int64_t r = (int64_t)all + tid; r < a.n; r += kSortThreads) a.row_slots[r] = -1;
@@ -600,14 +604,14 @@ __device__ __forceinline__ void place_chunk(const PlaceArgs& a, int64_t c) {
     __syncthreads();                               // wave_n is clear, start is ready
     if (live && rank == 0) wave_n[wave][id] = (uint16_t)__popcll(same);
     __syncthreads();
+    int r = -1;
     if (live) {
-      int r = start[id] + rank;
+      r = start[id] + rank;
       for (int w = 0; w < wave; ++w) r += wave_n[w][id];
-      a.slot_rows[s] = r;
-      a.row_slots[r] = (int32_t)s;
-    } else if (s < a.n) {
-      a.slot_rows[s] = -1;
+      if (write) a.row_slots[r] = (int32_t)s;
     }
+    if (write && s < a.n) a.slot_rows[s] = r;
+    if (rows != nullptr && i0 == 0) rows[tid] = r;
     __syncthreads();                               // every rank has read start
     if (tid < E) {
       int sum = 0;
@@ -617,6 +621,7 @@ __device__ __forceinline__ void place_chunk(const PlaceArgs& a, int64_t c) {
     }
     __syncthreads();                               // wave_n is read before it is cleared
   }
+  return all;
 }
 
 // First launch of a dispatch: workgroups [0, sort_wgs) count their chunk (or,
@@ -674,15 +679,101 @@ struct GatherArgs {
 
 constexpr int kGatherThreads = 256;
 
-// A thread quantizes one block of a token (16 values, MXFP4 32) exactly as
-// nvfp4_quantize / mxfp4_quantize do and writes it to each of the token's rows,
-// so a token is read and encoded once however many experts take it.  Rows of
-// dropped slots (offsets[E] on) are zeroed.
+// Quantizes block blk (16 values, MXFP4 32) of token t exactly as nvfp4_quantize /
+// mxfp4_quantize do and writes it to each of the token's rows (row_of(j)), so a
+// token is read and encoded once however many experts take it.
+template <bool MX, bool BF16, typename F>
+__device__ __forceinline__ void quantize_to_rows(const GatherArgs& a, int64_t t, int blk, float s_global,
+                                                 F&& row_of) {
+  constexpr int BS = MX ? 32 : 16;
+  const int nb = a.H / BS;
+  float v[BS];
+  const int64_t src = t * a.H + (int64_t)blk * BS;
+  if (a.vec) {
+    if (BF16) {
+      const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.x) + src);
+#pragma unroll
+      for (int k = 0; k < BS / 8; ++k) {
+        const u32x4 w = p[k];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[8 * k + 2 * q] = bf16_lo(w[q]);
+          v[8 * k + 2 * q + 1] = bf16_hi(w[q]);
+        }
+      }
+    } else {
+      const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.x) + src);
+#pragma unroll
+      for (int k = 0; k < BS / 4; ++k) {
+        const f32x4 w = p[k];
+        v[4 * k] = w.x; v[4 * k + 1] = w.y; v[4 * k + 2] = w.z; v[4 * k + 3] = w.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < BS; ++k) v[k] = load1(a.x, src + k, BF16);
+  }
+  uint32_t am = 0;
+#pragma unroll
+  for (int k = 0; k < BS; ++k) am = umax(am, __float_as_uint(v[k]) & 0x7fffffffu);
+  uint32_t sc;
+  float r;
+  if (MX) {
+    sc = e8m0_code(am);
+    r = e8m0_inv(sc);
+  } else {
+    nv_block_scale(__uint_as_float(am), s_global, sc, r);
+  }
+  uint32_t c[BS / 8];
+#pragma unroll
+  for (int k = 0; k < BS / 8; ++k) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[8 * k + q] *= r;
+    c[k] = e2m1_pack8(v + 8 * k);
+  }
+  for (int j = 0; j < a.top_k; ++j) {
+    const int row = row_of(j);
+    if (row < 0) continue;
+    uint8_t* dst = a.q + (int64_t)row * (a.H / 2) + blk * (BS / 2);
+    if constexpr (MX)
+      *reinterpret_cast<u32x4*>(dst) = u32x4{c[0], c[1], c[2], c[3]};
+    else
+      *reinterpret_cast<u32x2*>(dst) = u32x2{c[0], c[1]};
+    a.scales[(int64_t)row * nb + blk] = (uint8_t)sc;
+  }
+}
+
+// Codes and scales of the rows of dropped slots (from `first` on): zeros.
+template <bool MX>
+__device__ __forceinline__ void zero_rows(const GatherArgs& a, int64_t first) {
+  constexpr int BS = MX ? 32 : 16;
+  const int nb = a.H / BS;
+  const int64_t end = a.T * a.top_k * nb, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = first * nb + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < end; i += step) {
+    uint8_t* dst = a.q + i * (BS / 2);
+    if constexpr (MX)
+      *reinterpret_cast<u32x4*>(dst) = u32x4{0, 0, 0, 0};
+    else
+      *reinterpret_cast<u32x2*>(dst) = u32x2{0, 0};
+    a.scales[i] = 0;
+  }
+}
+
+// The tensor scale of max|x| = G, written once.
+__device__ __forceinline__ float tensor_scale(const GatherArgs& a, float G) {
+  const float s = nv_global_scale(G);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (a.amax_out != nullptr) *a.amax_out = G;
+    *a.scale_out = s;
+  }
+  return s;
+}
+
+// A thread per block.  HBM bound: 4096 x 7168 bf16 to 8 rows each, 191 MB in 32 us.
 template <bool MX, bool BF16>
 __global__ void __launch_bounds__(kGatherThreads) k_gather_quant(GatherArgs a) {
-  constexpr int BS = MX ? 32 : 16;
   __shared__ uint32_t red[kGatherThreads / 64];
-  const int nb = a.H / BS;
+  const int nb = a.H / (MX ? 32 : 16);
   float s_global = 1.0f;
   if (!MX) {
     float G;
@@ -698,81 +789,48 @@ __global__ void __launch_bounds__(kGatherThreads) k_gather_quant(GatherArgs a) {
       for (int i = 0; i < kGatherThreads / 64; ++i) m = umax(m, red[i]);
       G = __uint_as_float(m);
     }
-    s_global = nv_global_scale(G);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      if (a.amax_out != nullptr) *a.amax_out = G;
-      *a.scale_out = s_global;
-    }
+    s_global = tensor_scale(a, G);
   }
   const int64_t n = a.T * nb, step = (int64_t)gridDim.x * kGatherThreads;
   for (int64_t i = (int64_t)blockIdx.x * kGatherThreads + threadIdx.x; i < n; i += step) {
     const int64_t t = i / nb;
-    const int blk = (int)(i - t * nb);
-    float v[BS];
-    const int64_t src = t * a.H + (int64_t)blk * BS;
-    if (a.vec) {
-      if (BF16) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.x) + src);
-#pragma unroll
-        for (int k = 0; k < BS / 8; ++k) {
-          const u32x4 w = p[k];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[8 * k + 2 * q] = bf16_lo(w[q]);
-            v[8 * k + 2 * q + 1] = bf16_hi(w[q]);
-          }
-        }
-      } else {
-        const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.x) + src);
-#pragma unroll
-        for (int k = 0; k < BS / 4; ++k) {
-          const f32x4 w = p[k];
-          v[4 * k] = w.x; v[4 * k + 1] = w.y; v[4 * k + 2] = w.z; v[4 * k + 3] = w.w;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < BS; ++k) v[k] = load1(a.x, src + k, BF16);
-    }
-    uint32_t am = 0;
-#pragma unroll
-    for (int k = 0; k < BS; ++k) am = umax(am, __float_as_uint(v[k]) & 0x7fffffffu);
-    uint32_t sc;
-    float r;
-    if (MX) {
-      sc = e8m0_code(am);
-      r = e8m0_inv(sc);
-    } else {
-      nv_block_scale(__uint_as_float(am), s_global, sc, r);
-    }
-    uint32_t c[BS / 8];
-#pragma unroll
-    for (int k = 0; k < BS / 8; ++k) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[8 * k + q] *= r;
-      c[k] = e2m1_pack8(v + 8 * k);
-    }
-    for (int j = 0; j < a.top_k; ++j) {
-      const int row = a.slot_rows[t * a.top_k + j];
-      if (row < 0) continue;
-      uint8_t* dst = a.q + (int64_t)row * (a.H / 2) + blk * (BS / 2);
-      if constexpr (MX)
-        *reinterpret_cast<u32x4*>(dst) = u32x4{c[0], c[1], c[2], c[3]};
-      else
-        *reinterpret_cast<u32x2*>(dst) = u32x2{c[0], c[1]};
-      a.scales[(int64_t)row * nb + blk] = (uint8_t)sc;
-    }
+    quantize_to_rows<MX, BF16>(a, t, (int)(i - t * nb), s_global,
+                               [&](int j) { return a.slot_rows[t * a.top_k + j]; });
   }
-  const int64_t rows = a.T * a.top_k;
-  for (int64_t i = (int64_t)a.offsets[a.E] * nb + (int64_t)blockIdx.x * kGatherThreads + threadIdx.x;
-       i < rows * nb; i += step) {
-    uint8_t* dst = a.q + i * (BS / 2);
-    if constexpr (MX)
-      *reinterpret_cast<u32x4*>(dst) = u32x4{0, 0, 0, 0};
-    else
-      *reinterpret_cast<u32x2*>(dst) = u32x2{0, 0};
-    a.scales[i] = 0;
+  zero_rows<MX>(a, a.offsets[a.E]);
+}
+
+// A small dispatch in one launch: every workgroup sorts all slots (at most
+// kSortThreads) and reduces all of x (at most kSmallX values) for itself, and
+// workgroup 0 writes the index arrays.
+constexpr int64_t kSmallX = (int64_t)1 << 17;
+template <bool MX, bool BF16>
+__global__ void __launch_bounds__(kSortThreads) k_dispatch_small(PlaceArgs p, GatherArgs a) {
+  __shared__ int rows[kSortThreads];
+  __shared__ uint32_t red[kSortWaves];
+  const int nb = a.H / (MX ? 32 : 16);
+  float s_global = 1.0f;
+  if (!MX) {
+    float G;
+    if (a.amax_in != nullptr) {
+      G = *a.amax_in;
+    } else {
+      uint32_t m = wave_max_u32(amax_part<BF16>(a.x, a.T * a.H, 0, 1, a.vec));
+      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kSortWaves; ++i) m = umax(m, red[i]);
+      G = __uint_as_float(m);
+    }
+    s_global = tensor_scale(a, G);
   }
+  const int all = place_chunk(p, 0, blockIdx.x == 0, rows);   // (ends with a barrier)
+  const int n = (int)a.T * nb;
+  for (int i = blockIdx.x * kSortThreads + threadIdx.x; i < n; i += gridDim.x * kSortThreads) {
+    const int t = i / nb;
+    quantize_to_rows<MX, BF16>(a, t, i - t * nb, s_global, [&](int j) { return rows[t * a.top_k + j]; });
+  }
+  zero_rows<MX>(a, all);
 }
 
 // ---------------------------------------------------------------- combine --
@@ -951,7 +1009,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine_grad(CombineGradArg
     load_vals<V>(a.dy, t * a.H + h, a.dy_bf16, dy);
 #pragma unroll
     for (int j0 = 0; j0 < kMaxTopK; j0 += kSlotBatch) {
-      if (j0 >= k) break;
+      if (j0 >= k) continue;
       SlotRow s[kSlotBatch];
       RowRaw<V> raw[kSlotBatch];
 #pragma unroll
@@ -973,11 +1031,11 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine_grad(CombineGradArg
     }
   }
 #pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) {
-    if (j >= k) break;
-    const float s = lanes_sum<64>(dot[j]);
-    if (lane == 0) red[wave][j] = s;
-  }
+  for (int j = 0; j < kMaxTopK; ++j)
+    if (j < k) {
+      const float s = lanes_sum<64>(dot[j]);
+      if (lane == 0) red[wave][j] = s;
+    }
   __syncthreads();
   if ((int)threadIdx.x < k) {
     float s = 0.0f;
@@ -1072,6 +1130,24 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
   const bool need_amax = !p.mx && p.amax_in == nullptr;
   const int64_t nx = p.T * p.H;
   const bool vec = ok16(p.x);
+  const PlaceArgs a{p.ids, n, (int)p.E, (int)chunk, (int)chunks, counts, p.offsets, p.slot_rows, p.row_slots};
+  GatherArgs ga{p.x, p.T, (int)p.H, p.top_k, (int)p.E, p.slot_rows, p.offsets, p.q, p.scales,
+                p.amax_in, partials, 0, need_amax ? p.amax_out : nullptr, p.scale_out, vec};
+  const int64_t blocks = p.T * (p.H / (p.mx ? 32 : 16));
+  // (blocks < 2^30: 32-bit indexes there)
+  if (n <= kSortThreads && p.H > 0 && blocks < (1 << 30) && (!need_amax || nx <= kSmallX)) {
+    const int64_t wgs = (blocks + kSortThreads - 1) / kSortThreads;
+    const dim3 gs((unsigned)(wgs < num_cus() ? wgs : num_cus()));
+#define FP4_SMALL(MXV, BFV) \
+  hipLaunchKernelGGL((k_dispatch_small<MXV, BFV>), gs, dim3(kSortThreads), 0, stream, a, ga)
+    if (p.mx) {
+      if (p.bf16) FP4_SMALL(true, true); else FP4_SMALL(true, false);
+    } else {
+      if (p.bf16) FP4_SMALL(false, true); else FP4_SMALL(false, false);
+    }
+#undef FP4_SMALL
+    return hipGetLastError();
+  }
   // one partial per 32 KB of x, at most two workgroups per CU
   int npart = 0;
   if (need_amax) {
@@ -1079,7 +1155,7 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
     const int64_t most = min((int64_t)kAmaxPartials, (int64_t)2 * num_cus());
     npart = (int)(want < most ? want : most);
   }
-  const PlaceArgs a{p.ids, n, (int)p.E, (int)chunk, (int)chunks, counts, p.offsets, p.slot_rows, p.row_slots};
+  ga.npart = npart;
   const dim3 grid((unsigned)(chunks + npart));
   if (p.bf16)
     hipLaunchKernelGGL((k_count<true>), grid, dim3(kSortThreads), 0, stream, a, counts, (int)chunks, p.x,
@@ -1097,9 +1173,6 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
     if (!p.mx) return launch_empty_scales(p.amax_in != nullptr ? nullptr : p.amax_out, p.scale_out, stream);
     return hipSuccess;
   }
-  const GatherArgs ga{p.x, p.T, (int)p.H, p.top_k, (int)p.E, p.slot_rows, p.offsets, p.q, p.scales,
-                      p.amax_in, partials, npart, need_amax ? p.amax_out : nullptr, p.scale_out, vec};
-  const int64_t blocks = p.T * (p.H / (p.mx ? 32 : 16));
   const int64_t want = (blocks + kGatherThreads - 1) / kGatherThreads, most = (int64_t)16 * num_cus();
   const dim3 gg((unsigned)(want < most ? want : most));
 #define FP4_GATHER(MXV, BFV) \
