@@ -203,13 +203,13 @@ __device__ __forceinline__ float quad_swap2(float v) { return dpp<0x4e>(v); }   
 __device__ __forceinline__ float half_mirror(float v) { return dpp<0x141>(v); }   // lane 7 - i of each 8
 __device__ __forceinline__ float row_mirror(float v) { return dpp<0x140>(v); }    // lane 15 - i of each 16
 
-// f(k of another lane of the row of 16, that lane) for the 15 other lanes.  Row
-// rotation by R hands lane i the value of lane (i - R) mod 16.
-template <int R = 1, typename F>
+// f(k of another lane of the row of 16, that lane) for the lanes STEP, 2 STEP, ...
+// away.  Row rotation by R hands lane i the value of lane (i - R) mod 16.
+template <int R, int STEP, typename F>
 __device__ __forceinline__ void rotations(uint32_t k, int ln, F&& f) {
   if constexpr (R < 16) {
     f(ror16<R>(k), (ln - R) & 15);
-    rotations<R + 1>(k, ln, f);
+    rotations<R + STEP, STEP>(k, ln, f);
   }
 }
 
@@ -253,12 +253,18 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
     float b[EPL];
     load_bias_row<EPL>(a.bias, E, e0, a.bias_vec, b);
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // one division a token, then 1 ulp
+    // the selection values take the logits' place (NaN: masked, like -inf)
+    auto select_by = [&](auto score) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const float s = a.sigmoid ? sigmoid_accurate(l[j]) : exp_accurate(l[j] - top) * inv;
-      const float v = s + b[j];                             // NaN: masked, like -inf
-      l[j] = l[j] > kNegInf && v > kNegInf ? v : kNegInf;   // the selection value from here on
-    }
+      for (int j = 0; j < EPL; ++j) {
+        const float v = score(l[j]) + b[j];
+        l[j] = l[j] > kNegInf && v > kNegInf ? v : kNegInf;
+      }
+    };
+    if (a.sigmoid)
+      select_by([](float x) { return sigmoid_accurate(x); });
+    else
+      select_by([&](float x) { return exp_accurate(x - top) * inv; });
   }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) key[j] = order_key(l[j]);
@@ -275,13 +281,17 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
     if (a.lane_groups > 8) top_two(m1, m2, row_mirror(m1), row_mirror(m2));
     const float mine_s = a.group_top == 2 && m2 > kNegInf ? m1 + m2 : m1;
     // a group stays when fewer than top_groups are better (equal scores: the lower
-    // index is); the scores pass by, one lane of each group bearing its own
-    const bool bears = (ln & (a.lane_groups - 1)) == 0;
+    // index is); the scores of the other groups pass by
     const uint32_t mine_k = order_key(mine_s);
-    const uint32_t out_k = bears ? mine_k : 0u;
     int rank = 0;
     auto pass = [&](uint32_t k, int from) { rank += k > mine_k || (k == mine_k && from < (ln & -a.lane_groups)); };
-    rotations(out_k, ln, pass);
+    switch (a.lane_groups) {
+      case 1: rotations<1, 1>(mine_k, ln, pass); break;
+      case 2: rotations<2, 2>(mine_k, ln, pass); break;
+      case 4: rotations<4, 4>(mine_k, ln, pass); break;
+      case 8: rotations<8, 8>(mine_k, ln, pass); break;
+      default: break;                  // one group
+    }
     if (rank >= a.top_groups) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) key[j] = 0u;
@@ -382,7 +392,7 @@ struct RouteGradArgs {
   const void* logits;
   const int32_t* ids;
   int64_t T;
-  int E, top_k, sigmoid, renorm, vec;
+  int E, top_k, sigmoid, renorm, lvec, vec;   // lvec: whole-lane loads; vec: 16-byte stores
   float scale;
   void* dl;
   int dl_bf16;
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteGradArgs a) {
   const float li = id >= 0 ? load_logit<BF16>(a.logits, row * E + id) : kNegInf;
   float l[EPL];
   if (dense) {
-    load_logits<BF16, EPL>(a.logits, row, E, e0, a.vec, l);
+    load_logits<BF16, EPL>(a.logits, row, E, e0, a.lvec, l);
     softmax_stats<EPL, L>(l, top, total);
   } else if (!a.sigmoid) {
     const float m = lanes_maxf<L>(li);   // any common shift cancels in q
@@ -433,31 +443,30 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteGradArgs a) {
     mean = lanes_sum<L>(dw * s);
     g = dw * s;
   }
+  if (dense) {
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    float base = 0.0f;
-    if (dense && l[j] > kNegInf) base = -(exp_accurate(l[j] - top) / total) * mean;
-    vs[e0 + j] = base;
+    for (int j = 0; j < EPL; ++j)
+      vs[e0 + j] = l[j] > kNegInf ? -(exp_accurate(l[j] - top) / total) * mean : 0.0f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) vs[j * L + ln] = 0.0f;
   }
   wave_lds_order();
   if (id >= 0) vs[id] += g;
   wave_lds_order();
   if (t >= a.T) return;
-  if (a.vec && EPL >= 4) {
-    if (e0 >= E) return;
-    if constexpr (EPL >= 8) {
-      float o[EPL];
+  // the row in 16-byte pieces, contiguous over the lanes
+  if (a.vec && a.dl_bf16) {
+    for (int e = 8 * ln; e < E; e += 8 * L) {
+      float o[8];
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) o[j] = vs[e0 + j];
-      store_vec<EPL>(a.dl, t * E + e0, a.dl_bf16, o);
-    } else if constexpr (EPL == 4) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(vs + e0);
-      if (a.dl_bf16)
-        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.dl) + t * E + e0) =
-            u32x2{bf16_pack2(o.x, o.y), bf16_pack2(o.z, o.w)};
-      else
-        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.dl) + t * E + e0) = o;
+      for (int k = 0; k < 8; ++k) o[k] = vs[e + k];
+      store_vec<8>(a.dl, t * E + e, true, o);
     }
+  } else if (a.vec) {
+    for (int e = 4 * ln; e < E; e += 4 * L)
+      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.dl) + t * E + e) =
+          *reinterpret_cast<const f32x4*>(vs + e);
   } else {
     for (int e = ln; e < E; e += L) store1(a.dl, t * E + e, a.dl_bf16, vs[e]);
   }
@@ -507,12 +516,12 @@ __device__ __forceinline__ uint32_t amax_part(const void* __restrict__ x, int64_
   if (vec) {
     const u32x4* xv = reinterpret_cast<const u32x4*>(x);
     const int64_t nv = n / kPer, step = np * blockDim.x;
-    for (int64_t i = p * blockDim.x + threadIdx.x; i < nv; i += 4 * step) {
-      u32x4 v[4];
+    for (int64_t i = p * blockDim.x + threadIdx.x; i < nv; i += 8 * step) {
+      u32x4 v[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = i + u * step < nv ? xv[i + u * step] : u32x4{0, 0, 0, 0};
+      for (int u = 0; u < 8; ++u) v[u] = i + u * step < nv ? xv[i + u * step] : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t w = v[u][q];
@@ -1097,9 +1106,10 @@ hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, in
 hipError_t launch_route_grad(const RouteProblem& p, const float* dw, const int32_t* ids, void* dl,
                              bool dl_bf16, hipStream_t stream) {
   const int E = (int)p.E;
-  RouteGradArgs a{dw, p.logits, ids, p.T, E, p.top_k, p.sigmoid, p.renorm, 0, p.scale, dl, dl_bf16};
+  RouteGradArgs a{dw, p.logits, ids, p.T, E, p.top_k, p.sigmoid, p.renorm, 0, 0, p.scale, dl, dl_bf16};
 #define FP4_CALL(EPL, L)                                                                              \
-  a.vec = E % EPL == 0 && ok16(p.logits) && ok16(dl);                                                 \
+  a.lvec = E % EPL == 0 && ok16(p.logits);                                                            \
+  a.vec = E % 8 == 0 && ok16(dl);                                                                     \
   const int64_t grid = (p.T + kRouteThreads / L - 1) / (kRouteThreads / L);                           \
   const size_t lds = sizeof(float) * kRouteThreads * EPL;                                             \
   if (p.bf16)                                                                                         \
