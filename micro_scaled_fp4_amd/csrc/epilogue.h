@@ -222,13 +222,13 @@ __device__ __forceinline__ void finish_piece(float (&z)[16], const FusedArgs& f,
   }
 }
 
-// The same for sizes and alignments that take no whole pieces: a wave's 8 rows
-// of 64 columns, the accumulators in LDS rows of kStripRow floats; a lane takes
+// The same for sizes and alignments that take no whole pieces: a wave's ROWS
+// rows of 64 columns, the accumulators in LDS rows of kStripRow floats; a lane takes
 // one column (gated: one pair of columns) of each row, so every access of a row
-// is contiguous across the lanes.  Rows row0 .. row0 + 7 below m_rows (given as
+// is contiguous across the lanes.  Rows row0 .. row0 + ROWS - 1 below m_rows (given as
 // their count), columns n0 .. n0 + 63 below N; bias: of the lane's column(s).
 constexpr int kStripRow = 68;                  // 64 columns, rows 4 banks apart
-template <bool OUT_BF16>
+template <bool OUT_BF16, int ROWS>
 __device__ __forceinline__ void finish_strip(const float* strip, float alpha, const FusedArgs& f, float b0, float b1,
                                              int64_t row0, int rows, int n0, int N, void* D) {
   const int lane = threadIdx.x & 63;
@@ -236,16 +236,16 @@ __device__ __forceinline__ void finish_strip(const float* strip, float alpha, co
     const int n = n0 + 2 * (lane & 31);
     if (n >= N) return;
     const int64_t No = N / 2;
-    float r[4];
+    float r[ROWS / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < ROWS / 2; ++i) {
       const int m = 2 * i + (lane >> 5);
       r[i] = f.residual != nullptr && m < rows
                  ? load1(f.residual, (row0 + m) * No + n / 2, f.residual_bf16) : 0.0f;
     }
     with_act(f.activation, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < ROWS / 2; ++i) {
         const int m = 2 * i + (lane >> 5);
         if (m >= rows) continue;
         const float z0 = fmaf(strip[m * kStripRow + (n - n0)], alpha, b0);
@@ -260,14 +260,14 @@ __device__ __forceinline__ void finish_strip(const float* strip, float alpha, co
   } else {
     const int n = n0 + lane;
     if (n >= N) return;
-    float r[8];
+    float r[ROWS];
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
+    for (int m = 0; m < ROWS; ++m)
       r[m] = f.residual != nullptr && m < rows
                  ? load1(f.residual, (row0 + m) * N + n, f.residual_bf16) : 0.0f;
     with_act(f.activation, [&](auto a) {
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
+      for (int m = 0; m < ROWS; ++m) {
         if (m >= rows) continue;
         const float z = fmaf(strip[m * kStripRow + lane], alpha, b0);
         if (f.preact != nullptr) store1(f.preact, (row0 + m) * N + n, f.preact_bf16, z);

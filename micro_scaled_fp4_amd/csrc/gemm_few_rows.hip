@@ -21,6 +21,8 @@
 // v_mfma_f32_16x16x32_f16.  MXFP4: codes and E8M0 bytes straight into
 // v_mfma_scale_f32_16x16x128_f8f6f4.  W is the MFMA's first operand, so a lane
 // ends with 4 consecutive columns of one row.
+#include <math.h>
+
 #include <atomic>
 
 #include "epilogue.h"
@@ -488,43 +490,22 @@ namespace fp4impl {
 
 // Waves that split K: at least two pairs each, so that the partial tiles'
 // exchange is small beside the stream.
-inline int k_split(int64_t K) {
+static int k_split(int64_t K) {
   const int64_t P = (K + 255) / 256;
   return P >= 16 ? 8 : P >= 8 ? 4 : P >= 4 ? 2 : 1;
 }
 
-// Which kernel: the modelled time of this one (16-, 32- or 64-row items) against
-// the 256 x 256 tiles', both from measured steps.
-//   here: a workgroup's granules, rounded up to its units, times K and the time of
-//     one strip's value of K (fs; 64 groups of 4096 x 7168: NVFP4 185 / 294 / 540
-//     us at 16 / 32 / 64 rows, MXFP4 157 / 238 / 451);
-//   tiles: rounds of tiles over the device times stages of 256 values (NVFP4 5.8,
-//     MXFP4 2.2 us a stage: 1021 x 5120 x 7168 in 162 and 61 us).
-// E.g. 64 x 27648 x 5120 NVFP4 59 us here, 115 in tiles; 128 x 512 x 4096 11.5 and
-// 94; MXFP4 64 x 27648 x 5120 46 and 39.  Groups are taken as equally full (their
-// sizes are on the device).  Returns the rows of an item, 0 for tiles.
-int few_rows(bool mx, int64_t ngroups, int64_t M, int64_t N, int64_t K) {
-  if (K == 0) return 0;
-  const int64_t groups = ngroups > 0 ? ngroups : 1, rows = (M + groups - 1) / groups, ncu = num_cus();
-  const double stage = mx ? 2.2e9 : 5.8e9;      // fs
-  const double tiles = (double)(groups * ((rows + 255) / 256)) * ((N + 255) / 256);
-  double best = (double)(int64_t)((tiles + ncu - 1) / ncu) * ((K + 255) / 256) * stage;
-  int item = 0;
-  const int slots = kWaves / k_split(K);
-  for (int rt = 1; rt <= 4; rt *= 2) {
-    const double strip = mx ? (rt == 1 ? 0.34e6 : rt == 2 ? 0.52e6 : 0.98e6)
-                            : (rt == 1 ? 0.40e6 : rt == 2 ? 0.64e6 : 1.20e6);
-    const int S = rt == 4 ? 2 : 4;
-    const int64_t items = groups * ((rows + 16 * rt - 1) / (16 * rt));
-    const double granules = (double)items * ((N + 16 * slots - 1) / (16 * slots));
-    const double units = (double)(int64_t)((granules + ncu * S - 1) / (ncu * S));
-    const double t = units * S * slots * K * strip;
-    if (t < best) {
-      best = t;
-      item = 16 * rt;
-    }
-  }
-  return item;
+// Modelled time: a fixed part and, per value of K, one strip's time for each of the
+// strips that a slot goes through (whole units of S granules, every workgroup
+// waiting for the fullest).  Fitted to 24 sizes, dense and grouped.
+double few_rows_us(bool mx, int64_t groups, double row_items, int64_t N, int64_t K, int item) {
+  const int S = item == 64 ? 2 : 4, slots = kWaves / k_split(K);
+  const double granules = groups * row_items * ((N + 16 * slots - 1) / (16 * slots));
+  const double units = ceil(granules / (num_cus() * S));
+  const double strip = mx ? (item == 16 ? 0.33e-3 : item == 32 ? 0.48e-3 : 0.92e-3)
+                          : (item == 16 ? 0.45e-3 : item == 32 ? 0.62e-3 : 1.18e-3);
+  const double fixed = mx ? (item == 64 ? 6.8 : 5.1) : (item == 16 ? 6.7 : item == 32 ? 7.6 : 8.6);
+  return fixed + units * S * slots * K * strip;
 }
 
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,

@@ -117,12 +117,13 @@ __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int& 
 
 // Grouped GEMM (one launch over E groups, e.g. the experts of an MoE layer).
 // Group e's rows are goff[e] .. goff[e+1] (clamped into [0, M], so rows never
-// leave A or D); it has ceil(rows / BM) row tiles.  Each wave walks the
+// leave A or D); it has ceil(rows / ROWS) row tiles.  Each wave walks the
 // offsets 64 groups at a time with a lane prefix sum; the waves of a
 // workgroup reach the same results, so no barrier is needed.
 
 // Tile count of the groups c .. c + 63 held one per lane: (first row, one past
 // the last row, row tiles) of lane's group, and the inclusive prefix sum.
+template <int ROWS = BM>
 __device__ __forceinline__ void group_chunk(const int32_t* __restrict__ goff, int ngroups, int M,
                                             int c, int& l0, int& l1, int& tl, int& inc) {
   const int lane = threadIdx.x & 63;
@@ -131,7 +132,7 @@ __device__ __forceinline__ void group_chunk(const int32_t* __restrict__ goff, in
   if (e < ngroups) {
     l0 = min(max(goff[e], 0), M);
     l1 = min(max(goff[e + 1], l0), M);
-    tl = (l1 - l0 + BM - 1) / BM;
+    tl = (l1 - l0 + ROWS - 1) / ROWS;
   }
   inc = tl;
 #pragma unroll
@@ -142,11 +143,12 @@ __device__ __forceinline__ void group_chunk(const int32_t* __restrict__ goff, in
 }
 
 // Total row tiles over all groups.
+template <int ROWS = BM>
 __device__ __forceinline__ int group_row_tiles(const int32_t* __restrict__ goff, int ngroups, int M) {
   int total = 0;
   for (int c = 0; c < ngroups; c += 64) {
     int l0, l1, tl, inc;
-    group_chunk(goff, ngroups, M, c, l0, l1, tl, inc);
+    group_chunk<ROWS>(goff, ngroups, M, c, l0, l1, tl, inc);
     total += __shfl(inc, 63, 64);
   }
   return total;
@@ -154,12 +156,13 @@ __device__ __forceinline__ int group_row_tiles(const int32_t* __restrict__ goff,
 
 // Row tile `row_tile` -> group e, its first row lo, one past its last row hi,
 // and the tile's index tm inside the group.  False past the last group's tiles.
+template <int ROWS = BM>
 __device__ __forceinline__ bool group_tile_of(const int32_t* __restrict__ goff, int ngroups, int M,
                                               int row_tile, int& e_out, int& tm, int& lo, int& hi) {
   int base = 0;
   for (int c = 0; c < ngroups; c += 64) {
     int l0, l1, tl, inc;
-    group_chunk(goff, ngroups, M, c, l0, l1, tl, inc);
+    group_chunk<ROWS>(goff, ngroups, M, c, l0, l1, tl, inc);
     const int start = base + inc - tl;
     const uint64_t hit = __ballot(c + (int)(threadIdx.x & 63) < ngroups && row_tile >= start &&
                                   row_tile < start + tl);
@@ -486,13 +489,14 @@ __device__ __forceinline__ void transpose_groups(v4f (&x)[4]) {
 // the next 16 rows loading from where this one's is used up.
 //   row0  D's row of the group's row 0;  m0, n0  the wave's first row (inside
 //   its group, which has m_rows) and column;  bias0  the group's first bias element
-//   strip  this wave's LDS (kStripBytes) for sizes that take no 16-byte accesses
+//   strip  this wave's LDS for sizes that take no 16-byte accesses, ROWS (8 or 16)
+//   rows at a time (kStripBytes: 8)
 constexpr int kStripBytes = 8 * kStripRow * 4;
-template <bool OUT_BF16, int TN, int TM>
+template <bool OUT_BF16, int TN, int TM, int ROWS = 8>
 __device__ __forceinline__ void store_fused(v4f (&acc)[TN][TM], float alpha, const FusedArgs& f,
                                             int64_t row0, int m0, int m_rows, int n0, int N,
                                             int64_t bias0, void* D, uint8_t* strip_bytes, int r16, int g) {
-  static_assert(TN % 4 == 0 && TM == 8, "4 W tiles per transposition, 8 row tiles in the switch");
+  static_assert(TN % 4 == 0, "4 W tiles per transposition");
   const int No = f.gated ? N / 2 : N;
   float* strip = reinterpret_cast<float*>(strip_bytes);
   static_for<TN / 4>([&](auto i4_c) {
@@ -539,19 +543,19 @@ __device__ __forceinline__ void store_fused(v4f (&acc)[TN][TM], float alpha, con
       const float b0 = has ? load1(f.bias, bias0 + nc, f.bias_bf16) : 0.0f;
       const float b1 = has && f.gated ? load1(f.bias, bias0 + nc + 1, f.bias_bf16) : 0.0f;
 #pragma unroll 1
-      for (int jh = 0; jh < 2 * TM; ++jh) {       // 8 rows at a time
-        const int m = m0 + 8 * jh;
+      for (int jh = 0; jh < 16 / ROWS * TM; ++jh) {
+        const int m = m0 + ROWS * jh;
         if (m >= m_rows || nw >= N) break;        // (uniform)
         v4f x[4];
-        tile_row(jh >> 1, x);
+        tile_row(jh * ROWS / 16, x);
         wave_lds_order();                         // the previous rows have been read
-        if ((r16 >> 3) == (jh & 1)) {
+        if (ROWS == 16 || (r16 >> 3) == (jh & 1)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<v4f*>(strip + (r16 & 7) * kStripRow + 16 * g + 4 * q) = x[q];
+            *reinterpret_cast<v4f*>(strip + (r16 & (ROWS - 1)) * kStripRow + 16 * g + 4 * q) = x[q];
         }
         wave_lds_order();
-        finish_strip<OUT_BF16>(strip, alpha, f, b0, b1, row0 + m, m_rows - m, nw, N, D);
+        finish_strip<OUT_BF16, ROWS>(strip, alpha, f, b0, b1, row0 + m, m_rows - m, nw, N, D);
       }
     }
   });

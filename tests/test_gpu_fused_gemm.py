@@ -131,10 +131,40 @@ def test_more_tiles_than_compute_units(fmt):
 @pytest.mark.parametrize("M,N,K,gated,pre", [(3001, 2995, 544, False, BF), (2900, 3008, 1088, True, F32),
                                              (2817, 3010, 800, True, None)])
 def test_tile_sizes(fmt, M, N, K, gated, pre):
-    """Sizes that the 256 x 256 tiles take, with edges in every direction."""
+    """Sizes of many tiles, with edges in every direction."""
     announce(f"fused gemm tiles {fmt} {M}x{N}x{K}")
     run_dense(fmt, M, N, K, ref.SILU, gated, BF, F32, F32, pre, M)
     run_dense(fmt, M, N, K, ref.GELU_TANH, gated, None, BF, BF, None, N)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("M,N,K,gated,pre", [(4081, 4001, 1056, False, BF), (4096, 4016, 1280, True, F32)])
+def test_large_sizes(fmt, M, N, K, gated, pre):
+    """Outputs that fill the device with 256 x 256 tiles."""
+    announce(f"fused gemm large {fmt} {M}x{N}x{K}")
+    run_dense(fmt, M, N, K, ref.SILU, gated, BF, F32, F32, pre, M)
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("N,K", [(16404, 288), (16400, 544), (16400, 512)])
+def test_short_contractions_repeat(fmt, N, K):
+    """One to three stages per tile, several tiles per compute unit: the same bits
+    on every run, with other inputs' tiles in shared memory in between."""
+    announce(f"fused gemm short {fmt} N={N} K={K}")
+    f, M = (fp4.FP4_NVFP4 if fmt == "nv" else fp4.FP4_MXFP4), 1111
+    t = lambda g: None if g is None else torch.from_numpy(g).to(DEV)  # noqa: E731
+    args = []
+    for seed in (1, 2):
+        qa, sa, ga = operand(fmt, M, K, seed)
+        qw, sw, gw = operand(fmt, N, K, seed + 10)
+        args.append((f, to_gpu_u8(qa), to_gpu_u8(sa), t(ga), to_gpu_u8(qw), to_gpu_u8(sw), t(gw), K))
+    want = [fp4.fp4_scaled_gemm(*a, out_dtype=F32) for a in args]
+    for i in range(12):
+        got = fp4.fp4_scaled_gemm_fused(*args[i & 1], out_dtype=F32)
+        assert ((got - want[i & 1]).abs() <= 1e-4 * want[i & 1].abs().max()).all()
+        if i < 2:
+            first = (got,) if i == 0 else first + (got,)
+        assert torch.equal(got, first[i & 1])
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
@@ -192,7 +222,8 @@ def test_empty_contraction_and_empty_sizes():
 # ---------------------------------------------------------------- grouped ----
 GROUPS = [([1], 16, 32), ([0, 1, 3, 0, 16, 17], 130, 320), ([2] * 60, 272, 1024), ([5, 0, 33, 64, 65, 1, 0], 96, 544),
           ([300], 96, 256), ([0, 17, 256, 300], 258, 1056), ([40, 0, 1, 513, 77, 0, 255, 256], 520, 512), ([0, 0], 32, 64),
-          ([1] * 100 + [31], 64, 7168), ([700, 0, 1, 513, 900, 255, 256, 300], 3006, 544)]
+          ([1] * 100 + [31], 64, 7168), ([700, 0, 1, 513, 900, 255, 256, 300], 3006, 544),
+          ([0, 5, 130, 0, 128, 300, 1, 0], 200, 512), ([1800, 1850], 4002, 1056)]
 
 
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
