@@ -93,10 +93,10 @@ __device__ __forceinline__ void store_cols(void* p, int64_t row, int c, int N, b
 // every kGradWaves-th row of it, so a lane keeps its columns' sums in registers.
 // Bias partials: the waves' sums added in wave order, one row per split.
 // V 8: 16-byte accesses (N a multiple of 16, aligned pointers), contiguous over the
-// lanes (16 columns a lane, half lines per access, took 327 against 200 us at 8192 x
-// 28672); V 2: any size.
-// HBM bound: everything is read or written once (gated bf16 8192 x 28672: 1.17 GB
-// in 200 us, 5.9 TB/s; through the caches, in 8-byte accesses, 258 us).
+// lanes; V 2: any size.  HBM bound: everything is read or written once.  Gated bf16
+// 8192 x 28672, 1.17 GB: 236 us, 5.0 TB/s, a large copy's rate (the same tensors
+// again and again: 200; with 16 columns a lane, half lines per access, 327; through
+// the caches, in 8-byte accesses, 258).
 template <int V>
 __global__ void __launch_bounds__(kGradThreads) k_epilogue_grad(GradArgs a) {
   __shared__ float red[kGradWaves][64 * V];

@@ -21,6 +21,11 @@
 // v_mfma_f32_16x16x32_f16.  MXFP4: codes and E8M0 bytes straight into
 // v_mfma_scale_f32_16x16x128_f8f6f4.  W is the MFMA's first operand, so a lane
 // ends with 4 consecutive columns of one row.
+//
+// Bound: HBM, W's bytes.  1 x 27648 x 5120 NVFP4 20 us, 4.0 TB/s; 16 tokens to 8
+// of 64 experts of 4096 x 7168, 0.90 GB of them used, 154 to 160 us, 5.7 TB/s, near
+// the card's read rate.  From 32 rows on the unpacking of W, once per 16 to 64 rows,
+// costs more than its bytes (64 experts of 32 rows each: 292 us).
 #include <math.h>
 
 #include <atomic>
@@ -497,7 +502,7 @@ static int k_split(int64_t K) {
 
 // Modelled time: a fixed part and, per value of K, one strip's time for each of the
 // strips that a slot goes through (whole units of S granules, every workgroup
-// waiting for the fullest).  Fitted to 24 sizes, dense and grouped.
+// waiting for the fullest).  Fitted to 26 sizes, dense and grouped.
 double few_rows_us(bool mx, int64_t groups, double row_items, int64_t N, int64_t K, int item) {
   const int S = item == 64 ? 2 : 4, slots = kWaves / k_split(K);
   const double granules = groups * row_items * ((N + 16 * slots - 1) / (16 * slots));

@@ -487,6 +487,9 @@ __device__ __forceinline__ void transpose_groups(v4f (&x)[4]) {
 // meet in a lane.  Rows go one MFMA row tile (16 rows) at a time in a rolled
 // loop (the activation's code exists once, not once per tile), the residual of
 // the next 16 rows loading from where this one's is used up.
+// Bound: its bytes, beside the next tile's operand loads.  8192 x 28672 x 8192, bf16
+// output: MXFP4 1050 us with nothing of it, 1108 with bias and activation, 1204 with a
+// bf16 residual too (470 MB read); NVFP4 2675, 2745, 2892; unfused 1012 and 2637.
 //   row0  D's row of the group's row 0;  m0, n0  the wave's first row (inside
 //   its group, which has m_rows) and column;  bias0  the group's first bias element
 //   strip  this wave's LDS for sizes that take no 16-byte accesses, ROWS (8 or 16)
