@@ -24,16 +24,16 @@ hipError_t launch_fused_t(const uint8_t* A, const uint8_t* as, const uint8_t* W,
 // (gemm_few_rows.hip), 128 (gemm_mid.hip) or 256, by the least modelled time.
 // Few rows stream W once at memory speed but repeat its unpacking every 16 to 64
 // rows; 128 x 128 tiles fill the device from a quarter of the output that 256 x 256
-// tiles need, at two thirds of their rate.  Measured at the five (us, NVFP4):
-//   128 x 512 x 4096     11 /  14 /  16 /  42 /  93
-//   300 x 1000 x 7168    27 /  33 /  23 /  73 / 181
-//   128 x 27648 x 5120  126 /  93 /  93 /  55 / 115
-//   1021 x 5120 x 7168  222 / 159 / 163 / 108 / 154
-//   4096 x 4096 x 4096    - /   - /   - / 142 / 117
-//   64 groups of 4096 x 7168: 32 rows each 431 / 292 / 446 / 429 / 661,
-//                            256 rows 3255 / 2143 / 2092 / 947 / 771
-// Over 52 sizes and formats the chosen kernel takes 4% longer than the best of the
-// five in the mean, 1.55 times at worst (10 us).  Groups' sizes are on the device: each is
+// tiles need, at four fifths of their rate.  Measured at the five (us, NVFP4):
+//   128 x 512 x 4096     11 /  14 /  16 /  34 /  93
+//   300 x 1000 x 7168    27 /  33 /  23 /  58 / 181
+//   128 x 27648 x 5120  126 /  93 /  93 /  47 / 115
+//   1021 x 5120 x 7168  222 / 159 / 163 / 105 / 154
+//   4096 x 4096 x 4096    - /   - /   - / 134 / 117
+//   64 groups of 4096 x 7168: 32 rows each 431 / 292 / 446 / 428 / 661,
+//                            256 rows 3255 / 2143 / 2092 / 919 / 771
+// Over 56 sizes and formats the chosen kernel takes 3% longer than the best of the
+// five in the mean, 1.5 times at worst (23 us).  Groups' sizes are on the device: each is
 // taken as the mean, plus a quarter of a tile for their unequal ends.
 int choose(bool mx, int64_t ngroups, int64_t M, int64_t N, int64_t K) {
   if (K == 0) return 256;
@@ -45,7 +45,7 @@ int choose(bool mx, int64_t ngroups, int64_t M, int64_t N, int64_t K) {
   const double stages = (double)((K + BK - 1) / BK);
   const double rounds = ceil(groups * tiles(256) * ((N + BN - 1) / BN) / fp4impl::num_cus());
   int best = 256;
-  double us = mx ? 12.7 + 1.9 * rounds * stages : 20.0 + 5.3 * rounds * stages;
+  double us = mx ? 12.3 + 1.95 * rounds * stages : 19.6 + 5.4 * rounds * stages;
   auto offer = [&](int rows, double t) {
     if (t < us) {
       us = t;

@@ -3,23 +3,26 @@
 // of the device without work.
 //
 // Work.  A workgroup's 2 x 2 waves own 4 x 4 tiles of 16 x 16 each; K advances 256
-// values per stage through two LDS buffers that direct-to-LDS loads fill (operand
-// swizzle and edges as in gemm_kernels.h).  A stage's operands go to registers at
-// once (64 of them), so its buffer is free again before its MFMAs and the loads of
-// the stage after next run under two stages of them.  The wait for the next stage
-// counts the loads in flight instead of draining them.  The other workgroup of the
-// CU computes meanwhile: two of 68 (MXFP4) or 72 KB (NVFP4) fit its LDS, and 256
+// values per stage, in two steps, through two LDS buffers that direct-to-LDS loads
+// fill (operand swizzle and edges as in gemm_kernels.h).  The second step's operands
+// are read while the first one's MFMAs run; then one barrier, after which the stage's
+// buffer is free and the next stage has landed: its first operands are read and the
+// stage after next is loaded between the second step's MFMAs.  The other workgroup of
+// the CU computes meanwhile: two of 68 (MXFP4) or 72 KB (NVFP4) fit its LDS, and 256
 // registers a wave.  MXFP4 multiplies the codes under their E8M0 bytes; NVFP4
 // dequantizes both operands to fp16 (exact), each value twice per workgroup, where
 // the 256 x 256 tiles do it twice per four times the outputs.
 //
-// Bound: the latency of a stage with one tile per CU (MXFP4 0.84, NVFP4 2.2 us), LDS
-// reads (MXFP4) or dequantizing beside the MFMAs (NVFP4) with more (0.92 and 2.07 us
-// a tile and stage).  Measured: 1021 x 5120 x 7168 NVFP4 108 us (256 x 256 tiles
-// 154), MXFP4 42 (57); 128 x 27648 x 5120 55 (115) and 26 (43); 64 groups of 128
-// rows x 4096 x 7168 508 (694) and 279 (326).  8192 x 8192 x 8192, where the larger
-// tiles fill the device: 953 (782) and 405 (319).  Eight waves that split a stage's
-// K: 7 to 12% faster with a tile or less per CU, slower everywhere else.
+// Bound.  NVFP4: 4.3 vector instructions per MFMA, at 4 cycles each, and MFMAs at 16;
+// the counters' MFMA (46%) and vector cycles (51%) add up to all of the kernel's, so
+// the two do not overlap (256 x 256 tiles: 2.3 per MFMA, 63%).  MXFP4: LDS and the
+// barriers, MFMA busy a quarter of the time.  Per stage 1.8 (NVFP4) and 0.61 us
+// (MXFP4) with a tile per CU, 2.0 and 0.89 us a tile with more.  Measured: 1021 x 5120
+// x 7168 NVFP4 105 us (256 x 256 tiles 154), MXFP4 41 (57); 128 x 27648 x 5120 47
+// (115) and 24 (43); 64 groups of 128 rows x 4096 x 7168 490 (694) and 284 (326).
+// 4096 x 4096 x 4096, where the larger tiles fill the device: 134 (117) and 57 (48).
+// All operands of a stage read at once, two barriers, loads two stages ahead: 108, 42;
+// 55, 26; and eight waves that split a stage's K were slower than these.
 #include <math.h>
 
 #include <atomic>
@@ -114,25 +117,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
   const int nk = (K + BK - 1) / BK;
   constexpr int kBlocks = kTileBytes / 1024 / 4;   // 1 KB blocks per wave and operand
   using Scales = StageScales<MX, SVEC>;
-  // stage kt's loads into buffer b; past the last stage through empty ranges
-  auto load = [&](Scales& s, int kt, int b) {
-    const bool live = kt < nk;
-    const ScaleRange rs = scale_range<SVEC>(psc, live ? sc_bytes : 0);
-    load_scales<MX, SVEC>(s, rs, srow, nsc, kt * BK);
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(pa), 0, live ? rows_a * rowb : 0, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(pw), 0, live ? rows_w * rowb : 0, kBufferWord3);
-#pragma unroll
-    for (int q = 0; q < kBlocks; ++q) {
-      dma_block<SVEC>(ra, tile_a(b), rowb, K, kt * BK, q);
-      dma_block<SVEC>(rw, tile_w(b), rowb, K, kt * BK, q);
-    }
+  // stage kt's source ranges; past the last stage empty (zeros, no memory touched)
+  auto range_a = [&](int kt) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pa), 0, kt < nk ? rows_a * rowb : 0, kBufferWord3);
   };
-  // load instructions of a stage per wave, at least (the compiler may join the scale
-  // bytes' dwords into one): that many in flight leave no earlier stage's
-  constexpr int kLoads = 2 * kBlocks + 1;
-  static_assert(kLoads < 16, "one field of the wait's count");
+  auto range_w = [&](int kt) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pw), 0, kt < nk ? rows_w * rowb : 0, kBufferWord3);
+  };
+  auto load_sc = [&](Scales& s, int kt) {
+    load_scales<MX, SVEC>(s, scale_range<SVEC>(psc, kt < nk ? sc_bytes : 0), srow, nsc, kt * BK);
+  };
   // scale entry (h, g, r16, i): the bytes that lane (r16, g) of wave half h needs
   // for its tile i, the 4 tiles' contiguous
   auto store_sc = [&](const Scales& s, int b) {
@@ -157,92 +151,136 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
     for (int j = 0; j < kT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   const int ra0 = wm * 16 * kT + r16, rw0 = wn * 16 * kT + r16;
-  auto frag = [&](const uint8_t* tile, int row, int chunk) {
-    return *reinterpret_cast<const u32x4*>(tile + swz(row, chunk));
+  u32x4 f[2][2 * kT];                           // operands of a stage's two steps: A tiles, then W's
+  auto read_frag = [&](int b, int st, int x) {
+    const uint8_t* tile = x < kT ? tile_a(b) : tile_w(b);
+    const int row = x < kT ? ra0 + 16 * x : rw0 + 16 * (x - kT);
+    f[st][x] = *reinterpret_cast<const u32x4*>(tile + swz(row, 2 * g + st));
   };
-  auto stage = [&](Scales& cur, Scales& next, int kt, int b) {
-    // stage kt is in buffer b; its operands to registers
-    u32x4 fa[2][kT], fw[2][kT];
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int i = 0; i < kT; ++i) {
-        fa[st][i] = frag(tile_a(b), ra0 + 16 * i, 2 * g + st);
-        fw[st][i] = frag(tile_w(b), rw0 + 16 * i, 2 * g + st);
-      }
-    constexpr int kDw = MX ? 2 : 4;
-    uint32_t sa[kDw], sw[kDw];
-    const uint32_t* lsa = reinterpret_cast<const uint32_t*>(sc_a(b)) + ((wm * 4 + g) * 16 + r16) * kDw;
-    const uint32_t* lsw = reinterpret_cast<const uint32_t*>(sc_w(b)) + ((wn * 4 + g) * 16 + r16) * kDw;
+  constexpr int kDw = MX ? 2 : 4;
+  auto read_sc = [&](int b, uint32_t (&s)[2][kDw]) {
+    const uint32_t* la = reinterpret_cast<const uint32_t*>(sc_a(b)) + ((wm * 4 + g) * 16 + r16) * kDw;
+    const uint32_t* lw = reinterpret_cast<const uint32_t*>(sc_w(b)) + ((wn * 4 + g) * 16 + r16) * kDw;
 #pragma unroll
     for (int q = 0; q < kDw; ++q) {
-      sa[q] = lsa[q];
-      sw[q] = lsw[q];
+      s[0][q] = la[q];
+      s[1][q] = lw[q];
     }
-    wait_lgkm();
-    wave_barrier();                             // buffer b is free
-    load(cur, kt + 2, b);
-    __builtin_amdgcn_sched_barrier(0);          // issued before the MFMAs, waited on after them
-    if constexpr (MX) {
-      static_for<2>([&](auto st_c) {
-        constexpr int st = decltype(st_c)::value;
-        static_for<kT>([&](auto i_c) {
-          constexpr int i = decltype(i_c)::value;
-          const u32x4 w = fw[st][i];
-          const v8i wo = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-          static_for<kT>([&](auto j_c) {
-            constexpr int j = decltype(j_c)::value;
-            const u32x4 x = fa[st][j];
-            const v8i xo = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wo, xo, acc[i][j], 4, 4, 2 * (i & 1) + st, sw[i >> 1], 2 * (j & 1) + st, sa[j >> 1]);
-          });
-        });
-      });
-    } else {
-      static_for<2>([&](auto st_c) {
-        constexpr int st = decltype(st_c)::value;
-        v8h da[kT][4];
-        auto dequant = [&](v8h (&q)[4], const u32x4& codes, uint32_t scale) {
-          const v2h p = e4m3_pair_h<st == 1>(scale);
-          const v2h h0 = v2h{p.x, p.x}, h1 = v2h{p.y, p.y};
-          q[0] = dq8(codes.x, h0);
-          q[1] = dq8(codes.y, h0);
-          q[2] = dq8(codes.z, h1);
-          q[3] = dq8(codes.w, h1);
-        };
-#pragma unroll
-        for (int j = 0; j < kT; ++j) dequant(da[j], fa[st][j], sa[j]);
-#pragma unroll
-        for (int i = 0; i < kT; ++i) {
-          v8h dw[4];
-          dequant(dw, fw[st][i], sw[i]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int j = 0; j < kT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dw[k], da[j][k], acc[i][j], 0, 0, 0);
-        }
-      });
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    store_sc(next, b ^ 1);
-    __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);   // stage kt + 1 has landed; kt + 2 may be in flight
-    wait_lgkm();
-    wave_barrier();
+  };
+  // NVFP4: fp16 operands of the current and the next sub-step, block scale pairs of
+  // the two steps
+  v8h d[2][2 * kT];
+  v2h pair[2][2 * kT];
+  auto part = [&](int p, int x, uint32_t codes, const v2h& h, auto k_c, int u) {
+    constexpr int k = decltype(k_c)::value;
+    const v2h v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 256.0f, k);
+    const v2h r = v * ((u & 2) ? v2h{h.y, h.y} : v2h{h.x, h.x});
+    d[p][x][2 * k] = r.x;
+    d[p][x][2 * k + 1] = r.y;
   };
 
-  Scales s0, s1;
-  load(s0, 0, 0);
-  load(s1, 1, 1);
-  store_sc(s0, 0);
-  __builtin_amdgcn_s_waitcnt(0x0F70 | kLoads);
+  Scales s;
+  uint32_t sc[2][kDw];
+  load_sc(s, 0);
+#pragma unroll
+  for (int q = 0; q < kBlocks; ++q) {
+    dma_block<SVEC>(range_a(0), tile_a(0), rowb, K, 0, q);
+    dma_block<SVEC>(range_w(0), tile_w(0), rowb, K, 0, q);
+  }
+  store_sc(s, 0);
+  load_sc(s, 1);
+#pragma unroll
+  for (int q = 0; q < kBlocks; ++q) {
+    dma_block<SVEC>(range_a(1), tile_a(1), rowb, K, BK, q);
+    dma_block<SVEC>(range_w(1), tile_w(1), rowb, K, BK, q);
+  }
+  // stage 0 has landed when no more than stage 1's loads are in flight (at least
+  // 2 kBlocks + 1 instructions: the compiler may join the scale bytes' dwords)
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * kBlocks + 1));
   wait_lgkm();
   wave_barrier();
+  read_sc(0, sc);
+#pragma unroll
+  for (int x = 0; x < 2 * kT; ++x) read_frag(0, 0, x);
+  if constexpr (!MX) {
+    static_for<2 * kT>([&](auto x_c) {
+      constexpr int x = decltype(x_c)::value;
+      pair[0][x] = e4m3_pair_h<false>(sc[x / kT][x % kT]);
+      static_for<4>([&](auto k_c) { part(0, x, f[0][x].x, pair[0][x], k_c, 0); });
+    });
+  }
+
+  // Stage kt in buffer cb.  Its first step multiplies while the second's operands
+  // are read; then the next stage has to have landed, and this stage's buffer is
+  // free: its loads (stage kt + 2) and the next stage's first operands go between
+  // the second step's MFMAs, each MFMA in a slot of its own with its share of the
+  // other work.
+  auto stage = [&](int kt, auto cb_c) {
+    constexpr int cb = decltype(cb_c)::value, nb = cb ^ 1;
+    auto turn = [&] {
+      store_sc(s, nb);
+      wait_dma();
+      wait_lgkm();
+      wave_barrier();
+      load_sc(s, kt + 2);
+    };
+    const int k_ld = (kt + 2) * BK;
+    auto dma = [&](auto q_c) {
+      constexpr int q = decltype(q_c)::value;
+      if constexpr (q % 2 == 0) dma_block<SVEC>(range_a(kt + 2), tile_a(cb), rowb, K, k_ld, q / 2);
+      else dma_block<SVEC>(range_w(kt + 2), tile_w(cb), rowb, K, k_ld, q / 2);
+    };
+    if constexpr (MX) {
+      uint32_t sn[2][kDw];
+      static_for<2>([&](auto st_c) {
+        constexpr int st = decltype(st_c)::value;
+        static_for<16>([&](auto s_c) {
+          constexpr int sl = decltype(s_c)::value, i = sl >> 2, j = sl & 3;
+          const u32x4 w = f[st][kT + i], x = f[st][j];
+          const v8i wo = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+          const v8i xo = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              wo, xo, acc[i][j], 4, 4, 2 * (i & 1) + st, sc[1][i >> 1], 2 * (j & 1) + st, sc[0][j >> 1]);
+          if constexpr (st == 0 && sl < 2 * kT) read_frag(cb, 1, sl);
+          if constexpr (st == 1 && sl < 2 * kBlocks) dma(s_c);
+          if constexpr (st == 1 && sl >= 4 && sl < 4 + 2 * kT) read_frag(nb, 0, sl - 4);
+          if constexpr (st == 1 && sl == 2) read_sc(nb, sn);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (st == 0) turn();
+      });
+#pragma unroll
+      for (int q = 0; q < kDw; ++q) {
+        sc[0][q] = sn[0][q];
+        sc[1][q] = sn[1][q];
+      }
+    } else {
+      // 8 sub-steps of one code dword per tile row, the next one's dequantized meanwhile
+      static_for<8>([&](auto u_c) {
+        constexpr int u = decltype(u_c)::value, p = u & 1, un = (u + 1) & 7, st = un >> 2;
+        if constexpr (u == 4) turn();
+        static_for<16>([&](auto s_c) {
+          constexpr int sl = decltype(s_c)::value, i = sl >> 2, j = sl & 3, x = sl >> 1;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(d[p][kT + i], d[p][j], acc[i][j], 0, 0, 0);
+          using K0 = std::integral_constant<int, 2 * (sl & 1)>;
+          using K1 = std::integral_constant<int, 2 * (sl & 1) + 1>;
+          part(p ^ 1, x, f[st][x][un & 3], pair[st][x], K0{}, un);
+          part(p ^ 1, x, f[st][x][un & 3], pair[st][x], K1{}, un);
+          if constexpr (u == 0 && sl % 2 == 0) read_frag(cb, 1, x);
+          if constexpr (u == 1 && sl % 2 == 0) pair[1][x] = e4m3_pair_h<true>(sc[x / kT][x % kT]);
+          if constexpr (u == 4 && sl % 2 == 0) dma(std::integral_constant<int, x>{});
+          if constexpr (u == 5 && sl % 2 == 0) read_frag(nb, 0, x);
+          if constexpr (u == 5 && sl == 1) read_sc(nb, sc);
+          if constexpr (u == 6 && sl % 2 == 0) pair[0][x] = e4m3_pair_h<false>(sc[x / kT][x % kT]);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    }
+  };
   // two stages an iteration; an odd count runs one past the end (zeros)
   for (int kt = 0; kt < nk; kt += 2) {
-    stage(s0, s1, kt, 0);
-    stage(s1, s0, kt + 1, 1);
+    stage(kt, std::integral_constant<int, 0>{});
+    stage(kt + 1, std::integral_constant<int, 1>{});
   }
   wait_dma();                                   // the empty loads' zeros have landed: LDS is free
   __syncthreads();
@@ -277,13 +315,13 @@ hipError_t launch_mid_m(const MidArgs& a, bool svec, bool out_bf16, hipStream_t 
 
 namespace fp4impl {
 
-// Modelled time: a fixed part and the fullest CU's tiles times stages.  A lone tile
-// takes longer than half a pair: nothing runs while it waits.
+// Modelled time: a fixed part and the fullest CU's tiles times stages (two tiles on a
+// CU share its LDS and its MFMA pipes, so each takes longer than one alone).
 double mid_us(bool mx, int64_t groups, double row_tiles, int64_t N, int64_t K) {
   const double tiles = ceil(groups * row_tiles * ((N + kTile - 1) / kTile) / num_cus());
   const int64_t stages = (K + BK - 1) / BK;
-  if (tiles <= 1) return mx ? 7.2 + 0.84 * stages : 8.6 + 2.2 * stages;
-  return mx ? 7.2 + 0.92 * tiles * stages : 8.6 + 2.07 * tiles * stages;
+  if (tiles <= 1) return mx ? 7.1 + 0.61 * stages : 8.5 + 1.8 * stages;
+  return mx ? 7.1 + 0.89 * tiles * stages : 8.5 + 2.0 * tiles * stages;
 }
 
 hipError_t launch_mid(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a, const uint8_t* W,
