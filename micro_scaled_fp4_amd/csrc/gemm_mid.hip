@@ -13,11 +13,12 @@
 // dequantizes both operands to fp16 (exact), each value twice per workgroup, where
 // the 256 x 256 tiles do it twice per four times the outputs.
 //
-// Bound.  NVFP4: 4.3 vector instructions per MFMA, at 4 cycles each, and MFMAs at 16;
-// the counters' MFMA (46%) and vector cycles (51%) add up to all of the kernel's, so
-// the two do not overlap (256 x 256 tiles: 2.3 per MFMA, 63%).  MXFP4: LDS and the
-// barriers, MFMA busy a quarter of the time.  Per stage 1.8 (NVFP4) and 0.61 us
-// (MXFP4) with a tile per CU, 2.0 and 0.89 us a tile with more.  Measured: 1021 x 5120
+// Bound.  NVFP4: the vector issue.  A wave's MFMA takes 17 cycles alone or with 2
+// other vector instructions behind it, 29 with 4 (a loop of them); here it has 4.3, and
+// the counters give 34 cycles per MFMA, MFMA busy 46% (256 x 256 tiles, 2.3: 26
+// cycles, 63%).  MXFP4: LDS and the barriers, MFMA busy a quarter of the time.  Per
+// stage 1.8 (NVFP4) and 0.61 us (MXFP4) with a tile per CU, 2.0 and 0.89 us a tile
+// with more.  Measured: 1021 x 5120
 // x 7168 NVFP4 105 us (256 x 256 tiles 154), MXFP4 41 (57); 128 x 27648 x 5120 47
 // (115) and 24 (43); 64 groups of 128 rows x 4096 x 7168 490 (694) and 284 (326).
 // 4096 x 4096 x 4096, where the larger tiles fill the device: 134 (117) and 57 (48).
