@@ -423,8 +423,9 @@ fp4_status fp4_grouped_gemm_fused(fp4_format fmt, const uint8_t* A, const uint8_
  * order, of dz before its rounding.
  *   dD [M, No], z [M, N] (the forward's preact), dz out [M, N]: FP4_F32 / FP4_BF16
  *   offsets    device int32 [num_groups + 1] as fp4_grouped_gemm: dbias is
- *              [num_groups, N], a group's rows summed (none: zeros), and rows
- *              outside every group get no dz; or NULL with num_groups == 1
+ *              [num_groups, N], a group's rows summed (none: zeros), and dz of
+ *              the rows from offsets[num_groups] on is written as zeros, like the
+ *              forward's D and preact; or NULL with num_groups == 1
  *   dbias      out float32, or NULL (then the workspace may be NULL)
  *   workspace  >= fp4_epilogue_backward_workspace_bytes bytes, 4-byte aligned
  * M, N <= FP4_GEMM_MAX_MN, num_groups <= FP4_GROUPED_MAX_GROUPS and num_groups *

@@ -577,7 +577,8 @@ def fp4_epilogue_backward(dD: torch.Tensor, z: torch.Tensor, activation: int, ga
                           out_dtype: torch.dtype = torch.bfloat16,
                           workspace: Optional[torch.Tensor] = None):
     """(dz [M, N], dbias float32 [N], grouped [E, N], or None) of the fused epilogue
-    from dD [M, No] and the forward's pre-activations z [M, N]."""
+    from dD [M, No] and the forward's pre-activations z [M, N].  Rows past the last
+    group's (dropped slots) get zeros."""
     z = _gpu_2d(z, "z")
     dD = _gpu_2d(dD, "dD")
     dev = z.device

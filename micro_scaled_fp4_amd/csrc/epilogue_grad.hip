@@ -89,6 +89,25 @@ __device__ __forceinline__ void store_cols(void* p, int64_t row, int c, int N, b
   }
 }
 
+// dz of the rows past the last group's (slots that were dropped): zeros, as the
+// forward writes them in D and preact, so that a quantizer of all of dz sees none of
+// the memory's earlier contents.  Every thread of the launch takes a share, in 16-byte
+// pieces where rows are whole pieces (V 8).
+template <int V>
+__device__ __forceinline__ void zero_past_groups(const GradArgs& a) {
+  const int64_t lo = min(max((int64_t)a.offsets[a.groups], (int64_t)0), a.M);
+  if (lo == a.M) return;
+  const int64_t first = (int64_t)blockIdx.x * kGradThreads + threadIdx.x, step = (int64_t)gridDim.x * kGradThreads;
+  if constexpr (V == 8) {
+    const int per = a.dz_bf16 ? 8 : 4;             // values of a piece
+    u32x4* q = reinterpret_cast<u32x4*>(a.dz);
+    for (int64_t i = lo * a.N / per + first; i < a.M * a.N / per; i += step)
+      __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, q + i);
+  } else {
+    for (int64_t i = lo * a.N + first; i < a.M * a.N; i += step) store1(a.dz, i, a.dz_bf16, 0.0f);
+  }
+}
+
 // A workgroup takes 64 V columns and one split of a group's rows, its waves
 // every kGradWaves-th row of it, so a lane keeps its columns' sums in registers.
 // Bias partials: the waves' sums added in wave order, one row per split.
@@ -106,6 +125,7 @@ __global__ void __launch_bounds__(kGradThreads) k_epilogue_grad(GradArgs a) {
   const int e = part / a.splits, s = part - e * a.splits;
   int64_t lo = 0, hi = a.M;
   if (a.offsets != nullptr) {
+    zero_past_groups<V>(a);
     lo = min(max((int64_t)a.offsets[e], (int64_t)0), a.M);
     hi = min(max((int64_t)a.offsets[e + 1], lo), a.M);
   }
