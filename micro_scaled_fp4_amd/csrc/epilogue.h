@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "fp4_device.h"
+#include "grid.h"
 
 namespace fp4dev {
 
@@ -295,8 +296,8 @@ __device__ __forceinline__ void zero_tail(const int32_t* __restrict__ offsets, i
                                           const FusedArgs& f, bool out_bf16, void* D) {
   const int lo = min(max(offsets[groups], 0), M);
   if (lo == M) return;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  const int64_t first = (int64_t)workgroup() * blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)workgroups() * blockDim.x;
   const int64_t No = f.gated ? N / 2 : N;
   for (int64_t i = lo * No + first; i < M * No; i += step) store1(D, i, out_bf16, 0.0f);
   if (f.preact != nullptr)

@@ -7,6 +7,7 @@
 // The residual's gradient is dD itself.
 #include "epilogue.h"
 #include "fp4_internal.h"
+#include "grid.h"
 
 using namespace fp4dev;
 
@@ -97,7 +98,7 @@ template <int V>
 __device__ __forceinline__ void zero_past_groups(const GradArgs& a) {
   const int64_t lo = min(max((int64_t)a.offsets[a.groups], (int64_t)0), a.M);
   if (lo == a.M) return;
-  const int64_t first = (int64_t)blockIdx.x * kGradThreads + threadIdx.x, step = (int64_t)gridDim.x * kGradThreads;
+  const int64_t first = (int64_t)workgroup() * kGradThreads + threadIdx.x, step = (int64_t)workgroups() * kGradThreads;
   if constexpr (V == 8) {
     const int per = a.dz_bf16 ? 8 : 4;             // values of a piece
     u32x4* q = reinterpret_cast<u32x4*>(a.dz);
@@ -120,12 +121,14 @@ template <int V>
 __global__ void __launch_bounds__(kGradThreads) k_epilogue_grad(GradArgs a) {
   __shared__ float red[kGradWaves][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int part = blockIdx.x / a.col_wgs;
-  const int c = ((blockIdx.x - part * a.col_wgs) * 64 + lane) * V;
+  const uint32_t wg = workgroup();
+  const int part = wg / (uint32_t)a.col_wgs, col_wg = wg - (uint32_t)part * a.col_wgs;
+  const int c = (col_wg * 64 + lane) * V;
   const int e = part / a.splits, s = part - e * a.splits;
   int64_t lo = 0, hi = a.M;
+  if (a.offsets != nullptr) zero_past_groups<V>(a);
+  if (e >= a.groups) return;                       // (a grid's last row runs past the count)
   if (a.offsets != nullptr) {
-    zero_past_groups<V>(a);
     lo = min(max((int64_t)a.offsets[e], (int64_t)0), a.M);
     hi = min(max((int64_t)a.offsets[e + 1], lo), a.M);
   }
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kGradThreads) k_epilogue_grad(GradArgs a) {
 #pragma unroll
   for (int k = 0; k < V; ++k) red[wave][lane * V + k] = sum[k];
   __syncthreads();
-  const int c0 = (blockIdx.x - part * a.col_wgs) * 64 * V;
+  const int c0 = col_wg * 64 * V;
   for (int i = threadIdx.x; i < 64 * V && c0 + i < a.N; i += kGradThreads) {
     float t = red[0][i];
 #pragma unroll
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kGradThreads)
     k_bias_grad(const float* __restrict__ partials, int splits, int64_t cols, int N, float* __restrict__ dbias) {
   __shared__ float red[kGradWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t i = (int64_t)workgroup() * 64 + lane;
   float s = 0.0f;
   if (i < cols) {
     const int64_t e = i / N, c = i - e * N;
@@ -229,7 +232,7 @@ hipError_t launch_epilogue_grad(const void* dD, bool dD_bf16, const void* z, boo
   float* partials = dbias == nullptr ? nullptr : splits == 1 ? dbias : static_cast<float*>(workspace);
   const GradArgs a{dD, z, dz, partials, offsets, dD_bf16, z_bf16, dz_bf16, M, (int)N, (int)groups,
                    (int)splits, gated, activation, (int)col_wgs};
-  const dim3 grid((unsigned)(groups * splits * col_wgs));
+  const dim3 grid = grid_of(groups * splits * col_wgs);
   if (vec)
     hipLaunchKernelGGL((k_epilogue_grad<8>), grid, dim3(kGradThreads), 0, stream, a);
   else
@@ -237,7 +240,7 @@ hipError_t launch_epilogue_grad(const void* dD, bool dD_bf16, const void* z, boo
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || dbias == nullptr || splits == 1) return e;
   const int64_t cols = groups * N;
-  hipLaunchKernelGGL(k_bias_grad, dim3((unsigned)((cols + 63) / 64)),
+  hipLaunchKernelGGL(k_bias_grad, grid_of((cols + 63) / 64),
                      dim3(kGradThreads), 0, stream, partials, (int)splits, cols, (int)N, dbias);
   return hipGetLastError();
 }

@@ -52,7 +52,8 @@ int choose(bool mx, int64_t ngroups, int64_t M, int64_t N, int64_t K) {
       best = rows;
     }
   };
-  offer(128, fp4impl::mid_us(mx, groups, tiles(128), N, K));
+  if (((M + 127) / 128 + (ngroups < M ? ngroups : M)) * ((N + 127) / 128) < (int64_t)1 << 31)   // (a workgroup per tile)
+    offer(128, fp4impl::mid_us(mx, groups, tiles(128), N, K));
   for (int rows = 64; rows >= 16; rows /= 2)
     offer(rows, fp4impl::few_rows_us(mx, groups, tiles(rows), N, K, rows));
   return best;

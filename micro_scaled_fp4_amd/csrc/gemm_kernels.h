@@ -594,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // XCD share the row tile of A in its L2
   const int T = GROUPED ? group_row_tiles(goff, ngroups, M) * tiles_n : tiles_m * tiles_n;
   if constexpr (FUSED && GROUPED) zero_tail(goff, ngroups, M, N, fused, OUT == 2, D);
-  int bid = blockIdx.x;
-  if (bid >= T) return;
+  int bid = GROUPED ? (int)workgroup() : (int)blockIdx.x;
+  if ((uint32_t)bid >= (uint32_t)T) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / kWavesN, wn = wave % kWavesN;
   const int r16 = lane & 15, g = lane >> 4;
@@ -1323,8 +1323,10 @@ hipError_t launch_t(const uint8_t* A, const uint8_t* as, const uint8_t* W, const
                     const OutArgs& o, hipStream_t stream, const Groups& gr = Groups{nullptr, 0},
                     const FusedArgs& fused = FusedArgs{}) {
   const int tiles_n = (N + BN - 1) / BN;
-  // grouped: each group adds at most one partial row tile to ceil(M / BM)
-  const int tiles_m = (M + BM - 1) / BM + (GROUPED ? gr.ngroups : 0);
+  // grouped: each group that has rows adds at most one partial row tile to ceil(M / BM)
+  // (a bound by the groups alone would launch, for 2^20 groups of 5 rows, 2^20
+  // workgroups per column tile that look through all groups to find nothing)
+  const int tiles_m = (M + BM - 1) / BM + (GROUPED ? min(gr.ngroups, M) : 0);
   constexpr int lds = Cfg<MX>::kLdsBytes + (FUSED ? (MX && !GROUPED ? kThreads8 : kThreads) / 64 * kStripBytes : 0);
   static_assert(lds <= 160 * 1024, "LDS");
   // MXFP4: the 8-wave kernel (grouped launches: k_gemm, whose group lookup
@@ -1350,7 +1352,7 @@ hipError_t launch_t(const uint8_t* A, const uint8_t* as, const uint8_t* W, const
                        as, W, ws, g_d, M, N, K, o.D, o.d_scales, o.d_amax, o.d_gscale, tiles_m,
                        tiles_n, vec_out, fused);
   } else {
-    hipLaunchKernelGGL((k_gemm<MX, OUT, SCALE_VEC, GROUPED, FUSED>), dim3(grid),
+    hipLaunchKernelGGL((k_gemm<MX, OUT, SCALE_VEC, GROUPED, FUSED>), fp4impl::grid_of(grid),
                        dim3(kThreads), lds, stream, A, as, W, ws, g_a, g_b, g_d, M, N, K, o.D,
                        o.d_scales, o.d_amax, o.d_gscale, tiles_m, tiles_n, vec_out, gr.offsets,
                        gr.ngroups, fused);

@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
   const int M = a.M, N = a.N, K = a.K;
   const int T = GROUPED ? group_row_tiles<kTile>(a.offsets, a.groups, M) * a.tiles_n : a.tiles_m * a.tiles_n;
   if constexpr (GROUPED) zero_tail(a.offsets, a.groups, M, N, a.f, OUT_BF16, a.D);
-  if ((int)blockIdx.x >= T) return;
+  const int bid = (int)workgroup();
+  if (workgroup() >= (uint32_t)T) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, g = lane >> 4;
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
   int tm = 0, tn = 0, lo = 0, m_rows = M, e = 0;
   if constexpr (GROUPED) {
     int t, hi = 0;
-    xcd_tile(blockIdx.x, T, t);
+    xcd_tile(bid, T, t);
     group_tile_of<kTile>(a.offsets, a.groups, M, t / a.tiles_n, e, tm, lo, hi);
     tn = t % a.tiles_n;
     m_rows = hi - lo;
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
     lo = __builtin_amdgcn_readfirstlane(lo);
     m_rows = __builtin_amdgcn_readfirstlane(m_rows);
   } else {
-    tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+    tile_of(bid, a.tiles_m, a.tiles_n, tm, tn);
   }
   const int m0 = tm * kTile, n0 = tn * kTile;
   const int64_t a_row = (int64_t)lo + m0, w_row = (int64_t)e * N + n0;
@@ -298,7 +299,7 @@ hipError_t launch_mid_t(const MidArgs& a, hipStream_t stream) {
   const hipError_t e = fp4impl::set_lds_limit_once(
       lds_set, reinterpret_cast<const void*>(&k_gemm_mid<MX, SVEC, OUT_BF16, GROUPED>), MidCfg<MX>::kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_gemm_mid<MX, SVEC, OUT_BF16, GROUPED>), dim3(a.tiles_m * a.tiles_n), dim3(kThreads),
+  hipLaunchKernelGGL((k_gemm_mid<MX, SVEC, OUT_BF16, GROUPED>), fp4impl::grid_of((int64_t)a.tiles_m * a.tiles_n), dim3(kThreads),
                      MidCfg<MX>::kLds, stream, a);
   return hipGetLastError();
 }
@@ -334,7 +335,7 @@ hipError_t launch_mid(bool mx, const uint8_t* A, const uint8_t* a_scales, const 
   auto ok16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   f.vec = N % 16 == 0 && ok16(ep.bias) && ok16(ep.residual) && ok16(ep.preact) && ok16(D);
   const bool svec = K % BK == 0 && ok16(a_scales) && ok16(w_scales);
-  const int64_t tiles_m = (M + kTile - 1) / kTile + ngroups, tiles_n = (N + kTile - 1) / kTile;
+  const int64_t tiles_m = (M + kTile - 1) / kTile + (ngroups < M ? ngroups : M), tiles_n = (N + kTile - 1) / kTile;
   if (tiles_m * tiles_n >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const MidArgs a{A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, (int)tiles_m, (int)tiles_n,
                   offsets, (int)ngroups, D, f};

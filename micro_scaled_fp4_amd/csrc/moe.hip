@@ -10,6 +10,7 @@
 #include "epilogue.h"
 #include "fp4_device.h"
 #include "fp4_internal.h"
+#include "grid.h"
 #include "scale_bytes.h"
 
 using namespace fp4dev;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
   __shared__ float gs_s[kTokens][kMaxGroups];
   extern __shared__ float v_s[];   // [kTokens][E + 1] selection values (groups only)
   const int tl = threadIdx.x / L, ln = threadIdx.x % L;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + tl;
+  const int64_t t = (int64_t)workgroup() * kTokens + tl;
   const int64_t row = min(t, a.T - 1);   // lanes past the last token repeat it and store nothing
   const int E = a.E, e0 = ln * EPL;
   float l[EPL];
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteGradArgs a) {
   constexpr int kTokens = kRouteThreads / L;
   extern __shared__ float v_s[];   // [kTokens][L * EPL]
   const int tl = threadIdx.x / L, ln = threadIdx.x % L;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + tl;
+  const int64_t t = (int64_t)workgroup() * kTokens + tl;
   const int64_t row = min(t, a.T - 1);
   const int E = a.E, e0 = ln * EPL;
   float* vs = v_s + tl * (L * EPL);
@@ -970,9 +971,10 @@ __device__ __forceinline__ void row_values(float (&v)[V], const RowRaw<V>& r, bo
 // after the sum of the one before it: 128 us).
 template <int V, bool ROWS_BF16>
 __global__ void __launch_bounds__(kCombineThreads) k_combine(CombineArgs a, int pieces) {
-  const int64_t t = blockIdx.x / pieces;
-  const int h = ((int)(blockIdx.x - t * pieces) * kCombineThreads + (int)threadIdx.x) * V;
-  if (h >= a.H) return;
+  const uint32_t wg = workgroup();
+  const int64_t t = wg / (uint32_t)pieces;
+  const int h = ((int)(wg - t * pieces) * kCombineThreads + (int)threadIdx.x) * V;
+  if (t >= a.T || h >= a.H) return;
   float acc[V], res[V];
 #pragma unroll
   for (int q = 0; q < V; ++q) acc[q] = res[q] = 0.0f;
@@ -1020,7 +1022,8 @@ struct CombineGradArgs {
 template <int V, bool ROWS_BF16>
 __global__ void __launch_bounds__(kCombineThreads) k_combine_grad(CombineGradArgs a) {
   __shared__ float red[kCombineThreads / 64][kMaxTopK];
-  const int64_t t = blockIdx.x;
+  const int64_t t = workgroup();
+  if (t >= a.T) return;
   const int k = a.top_k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float dot[kMaxTopK];
 #pragma unroll
@@ -1107,9 +1110,9 @@ hipError_t launch_route(const RouteProblem& p, const float* bias, int groups, in
   const int64_t grid = (p.T + kRouteThreads / L - 1) / (kRouteThreads / L);                           \
   const size_t lds = groups > 1 && a.lane_groups == 0 ? sizeof(float) * (kRouteThreads / L) * (E + 1) : 0;                  \
   if (p.bf16)                                                                                         \
-    hipLaunchKernelGGL((k_route<true, EPL, L>), dim3(grid), dim3(kRouteThreads), lds, stream, a);     \
+    hipLaunchKernelGGL((k_route<true, EPL, L>), grid_of(grid), dim3(kRouteThreads), lds, stream, a);     \
   else                                                                                                \
-    hipLaunchKernelGGL((k_route<false, EPL, L>), dim3(grid), dim3(kRouteThreads), lds, stream, a)
+    hipLaunchKernelGGL((k_route<false, EPL, L>), grid_of(grid), dim3(kRouteThreads), lds, stream, a)
   FP4_ROUTE_SIZES(FP4_CALL)
 #undef FP4_CALL
   return hipGetLastError();
@@ -1125,9 +1128,9 @@ hipError_t launch_route_grad(const RouteProblem& p, const float* dw, const int32
   const int64_t grid = (p.T + kRouteThreads / L - 1) / (kRouteThreads / L);                           \
   const size_t lds = sizeof(float) * kRouteThreads * EPL;                                             \
   if (p.bf16)                                                                                         \
-    hipLaunchKernelGGL((k_route_grad<true, EPL, L>), dim3(grid), dim3(kRouteThreads), lds, stream, a); \
+    hipLaunchKernelGGL((k_route_grad<true, EPL, L>), grid_of(grid), dim3(kRouteThreads), lds, stream, a); \
   else                                                                                                \
-    hipLaunchKernelGGL((k_route_grad<false, EPL, L>), dim3(grid), dim3(kRouteThreads), lds, stream, a)
+    hipLaunchKernelGGL((k_route_grad<false, EPL, L>), grid_of(grid), dim3(kRouteThreads), lds, stream, a)
   FP4_ROUTE_SIZES(FP4_CALL)
 #undef FP4_CALL
   return hipGetLastError();
@@ -1218,7 +1221,7 @@ hipError_t launch_combine(const void* rows, bool rows_bf16, int64_t M, int64_t H
   const int64_t pieces = (H + per - 1) / per;
   if (T * pieces >= (int64_t)1 << 31) return hipErrorInvalidValue;
 #define FP4_COMBINE(VV, BF) \
-  hipLaunchKernelGGL((k_combine<VV, BF>), dim3(T * pieces), dim3(kCombineThreads), 0, stream, a, (int)pieces)
+  hipLaunchKernelGGL((k_combine<VV, BF>), grid_of(T * pieces), dim3(kCombineThreads), 0, stream, a, (int)pieces)
   if (vec) {
     if (rows_bf16) FP4_COMBINE(8, true); else FP4_COMBINE(8, false);
   } else {
@@ -1235,7 +1238,7 @@ hipError_t launch_combine_grad(const void* dy, bool dy_bf16, const void* rows, b
   const CombineGradArgs a{dy, rows, weights, slot_rows, row_slots, T, M, (int)H, top_k, dy_bf16,
                           rows_bf16, dr_bf16, d_rows, d_weights};
   const bool vec = H % 8 == 0 && ok16(dy) && ok16(rows) && ok16(d_rows);
-#define FP4_COMBINE(VV, BF) hipLaunchKernelGGL((k_combine_grad<VV, BF>), dim3(T), dim3(kCombineThreads), 0, stream, a)
+#define FP4_COMBINE(VV, BF) hipLaunchKernelGGL((k_combine_grad<VV, BF>), grid_of(T), dim3(kCombineThreads), 0, stream, a)
   if (vec) {
     if (rows_bf16) FP4_COMBINE(8, true); else FP4_COMBINE(8, false);
   } else {
