@@ -1065,7 +1065,9 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine_grad(CombineGradArg
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kCombineThreads / 64; ++w) s += red[w][threadIdx.x];
-    a.d_weights[t * k + threadIdx.x] = s;
+    // (a slot without a row: 0 also where dy times the zeros read for it is NaN)
+    const int row = a.slot_rows[t * k + threadIdx.x];
+    a.d_weights[t * k + threadIdx.x] = row >= 0 && row < a.M ? s : 0.0f;
   }
   // this workgroup's share of the rows: those of no slot
   const int64_t per = (a.M + a.T - 1) / a.T;
