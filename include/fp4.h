@@ -452,8 +452,9 @@ fp4_status fp4_epilogue_backward(const void* dD, fp4_dtype dD_type, const void* 
  *              largest (2; one where only one is unmasked); the experts of all but
  *              the top_groups best groups are masked
  *   ids        the top_k largest v, largest first; -1 once no expert is left
- *   weights    scale * s, renormalized: scale * s / (sum of the selected s), 0
- *              when that sum is 0 in float32; 0 where the id is -1
+ *   weights    scale * s, renormalized: scale * s / (sum of the selected s), by
+ *              the softmax scores' ratios also where the scores themselves are
+ *              too small for float32; 0 where the id is -1
  * Equal v and equal group scores go to the lower index.
  *   logits   [T, E] FP4_F32 / FP4_BF16;  bias device float32 [E] or NULL
  *   ids      out int32 [T, top_k];  weights out float32 [T, top_k]

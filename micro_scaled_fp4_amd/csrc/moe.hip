@@ -241,18 +241,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
   const bool two = a.groups > 1 && a.group_top == 2;
   const bool by_score = a.bias != nullptr || two;
   float top = 0.0f, total = 0.0f;
-  if (!a.sigmoid) {
-    if (by_score || !a.renorm) {
-      softmax_stats<EPL, L>(l, top, total);
-    } else {   // renormalized: only the selected scores' ratios matter
-      float m = l[0];
-#pragma unroll
-      for (int j = 1; j < EPL; ++j) m = fmaxf(m, l[j]);
-      m = lanes_maxf<L>(m);
-      top = m > kNegInf ? m : 0.0f;
-      total = 1.0f;
-    }
-  }
+  if (!a.sigmoid && (by_score || !a.renorm)) softmax_stats<EPL, L>(l, top, total);
   uint32_t key[EPL];
   if (by_score) {
     float b[EPL];
@@ -375,11 +364,15 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
 
   // lane r: slot r's score and weight
   const int id = ln < a.top_k ? ids_s[tl][ln] : -1;
-  float s = 0.0f;
-  if (id >= 0) {
-    const float li = load_logit<BF16>(a.logits, row * E + id);
-    s = a.sigmoid ? sigmoid_accurate(li) : exp_accurate(li - top);
+  const float li = id >= 0 ? load_logit<BF16>(a.logits, row * E + id) : kNegInf;
+  if (a.renorm && !a.sigmoid) {
+    // relative to the largest selected score: only their ratios matter, and a bias can
+    // select scores that are all too small for float32
+    const float m = lanes_maxf<L>(li);
+    top = m > kNegInf ? m : 0.0f;
   }
+  float s = 0.0f;
+  if (id >= 0) s = a.sigmoid ? sigmoid_accurate(li) : exp_accurate(li - top);
   if (a.renorm) {
     const float sum = lanes_sum<L>(s);
     s = sum > 0.0f ? s / sum : 0.0f;

@@ -1,11 +1,15 @@
-"""GPU parity at the edges of expert routing and combining."""
+"""GPU parity at the edges of expert routing and combining: gradients of dropped
+slots, and renormalized weights of scores that float32 cannot hold by themselves.
+Tolerances as in test_gpu_moe: a weight is a few float32 operations on exponentials
+within 3 ulp, 4e-6 relative."""
 import numpy as np
 import pytest
 import torch
 
 import micro_scaled_fp4_amd as fp4
+import moe_reference as ref
 from gpu_util import DEV, announce
-from test_gpu_moe import gpu, host
+from test_gpu_moe import check_route, gpu, host
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +37,25 @@ def test_dropped_slots_have_no_weight_gradient(H, dtype):
     assert (dw[:, 0] == 0).all() and (dw[:, 2] == 0).all()
     assert np.isposinf(dw[0, 1]) and np.isneginf(dw[1, 1]) and np.isnan(dw[2, 1]) and dw[4, 1] == H
     assert not dr[T:].float().ne(0).any()
+
+
+@pytest.mark.parametrize("E", [16, 64, 256, 700])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_renormalized_softmax_far_below_the_largest_logit(E, groups):
+    """A bias that selects experts whose scores are e^-90 to e^-300: their ratios are
+    well defined, forward and backward."""
+    announce(f"route far below the largest logit E={E} groups={groups}")
+    rng = np.random.default_rng(E)
+    T, k = 9, 4
+    logits = rng.normal(0, 2, (T, E)).astype(np.float32)
+    logits[:, : E // 2] -= rng.uniform(90, 300, (T, 1)).astype(np.float32)
+    logits[0, : E // 2] = -600.0       # (equal logits, equal weights)
+    bias = np.zeros(E, np.float32)
+    bias[: E // 2] = 4.0 + np.arange(E // 2) / 64
+    t, ids, w = check_route(logits, k, False, bias=bias, groups=groups, top_groups=max(1, groups // 2), scale=2.5)
+    assert (ids < E // 2).all() and (ids >= 0).all()
+    np.testing.assert_allclose(w.sum(1), 2.5, rtol=4e-6)
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32)
+    got = host(fp4.moe_route_backward(gpu(dw), t, gpu(ids), scale=2.5))
+    want = ref.route_grad(dw, logits, ids, False, True, 2.5)
+    np.testing.assert_allclose(got, want, rtol=2e-5, atol=4e-6 * 2.5 * np.abs(dw).max())
