@@ -453,8 +453,10 @@ fp4_status fp4_epilogue_backward(const void* dD, fp4_dtype dD_type, const void* 
  *              the top_groups best groups are masked
  *   ids        the top_k largest v, largest first; -1 once no expert is left
  *   weights    scale * s, renormalized: scale * s / (sum of the selected s), by
- *              the softmax scores' ratios also where the scores themselves are
- *              too small for float32; 0 where the id is -1
+ *              their ratios also where all of them are too small for float32
+ *              (sigmoid: down to about e^-700, then 0); 0 where the id is -1
+ * Scores below 2^-126 (subnormal in float32) may count as 0 in v, where they then
+ * tie, and in weights that are not renormalized.
  * Equal v and equal group scores go to the lower index.
  *   logits   [T, E] FP4_F32 / FP4_BF16;  bias device float32 [E] or NULL
  *   ids      out int32 [T, top_k];  weights out float32 [T, top_k]

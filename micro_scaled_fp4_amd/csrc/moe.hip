@@ -76,10 +76,20 @@ __device__ __forceinline__ float exp_accurate(float x) {
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e * r, 0x1.62e430p-1f, e);
 }
-// (v_rcp_f32: 1 ulp.)  Scores below e^-87 count as 0.
+// (v_rcp_f32: 1 ulp.)  Scores below 2^-126, float32's smallest normal number, are 0:
+// what holds them would be subnormal.
 __device__ __forceinline__ float sigmoid_accurate(float x) {
-  const float s = __builtin_amdgcn_rcpf(1.0f + exp_accurate(fminf(-x, 87.0f)));
-  return x < -87.0f ? 0.0f : s;
+  constexpr float kLeast = -0x1.5d589ep+6f;      // -126 ln 2
+  const float s = __builtin_amdgcn_rcpf(1.0f + exp_accurate(fminf(-x, -kLeast)));
+  return x < kLeast ? 0.0f : s;
+}
+// sigmoid(x) e^-c (c = 0 where x > 0) and, in rest, 1 - sigmoid(x), which loses no
+// digits next to 1.  A common c <= 0 near the largest x of a token keeps scores that
+// are all too small for float32 apart.
+__device__ __forceinline__ float sigmoid_over(float x, float c, float& rest) {
+  const float e = exp_accurate(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
+  rest = x > 0.0f ? e * r : r;
+  return x > 0.0f ? r : exp_accurate(x - c) * r;
 }
 
 // Float -> integer that orders like the float (-0 equal to +0).  Masked experts
@@ -156,6 +166,17 @@ __device__ __forceinline__ void softmax_stats(const float (&l)[EPL], float& top,
 #pragma unroll
   for (int j = 0; j < EPL; ++j) s += l[j] > kNegInf ? exp_accurate(l[j] - top) : 0.0f;
   total = lanes_sum<L>(s);
+}
+
+// What a token's selected logits li (-inf: none) are taken relative to when their scores
+// are renormalized: only the ratios matter then, and all of the scores can be too
+// small for float32 (softmax scores that a bias selects, sigmoid scores of logits far
+// below 0).  Sigmoid scores are 0 from about e^-700 down, so that logits of a type's
+// lowest value mask an expert.
+template <int L>
+__device__ __forceinline__ float shared_shift(float li, bool sigmoid) {
+  const float m = lanes_maxf<L>(li);
+  return sigmoid ? fminf(fmaxf(m, -700.0f), 0.0f) : m > kNegInf ? m : 0.0f;
 }
 
 constexpr int kRouteThreads = 256;
@@ -365,14 +386,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
   // lane r: slot r's score and weight
   const int id = ln < a.top_k ? ids_s[tl][ln] : -1;
   const float li = id >= 0 ? load_logit<BF16>(a.logits, row * E + id) : kNegInf;
-  if (a.renorm && !a.sigmoid) {
-    // relative to the largest selected score: only their ratios matter, and a bias can
-    // select scores that are all too small for float32
-    const float m = lanes_maxf<L>(li);
-    top = m > kNegInf ? m : 0.0f;
-  }
-  float s = 0.0f;
-  if (id >= 0) s = a.sigmoid ? sigmoid_accurate(li) : exp_accurate(li - top);
+  if (a.renorm) top = shared_shift<L>(li, a.sigmoid);
+  float s = 0.0f, rest;
+  if (id >= 0) s = a.sigmoid ? sigmoid_over(li, top, rest) : exp_accurate(li - top);
   if (a.renorm) {
     const float sum = lanes_sum<L>(s);
     s = sum > 0.0f ? s / sum : 0.0f;
@@ -425,20 +441,20 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteGradArgs a) {
   if (dense) {
     load_logits<BF16, EPL>(a.logits, row, E, e0, a.lvec, l);
     softmax_stats<EPL, L>(l, top, total);
-  } else if (!a.sigmoid) {
-    const float m = lanes_maxf<L>(li);   // any common shift cancels in q
-    top = m > kNegInf ? m : 0.0f;
+  } else if (a.renorm) {
+    top = shared_shift<L>(li, a.sigmoid);
   }
-  float s = li > kNegInf ? (a.sigmoid ? sigmoid_accurate(li) : exp_accurate(li - top)) : 0.0f;
+  float s = 0.0f, rest = 0.0f;             // (rest: 1 - s)
+  if (li > kNegInf) s = a.sigmoid ? sigmoid_over(li, top, rest) : exp_accurate(li - top);
   float g, mean = 0.0f;
   if (a.renorm) {
     const float sum = lanes_sum<L>(s);
     const float q = sum > 0.0f ? s / sum : 0.0f;
     mean = lanes_sum<L>(dw * q);
     g = q * (dw - mean);
-    if (a.sigmoid) g *= 1.0f - s;
+    if (a.sigmoid) g *= rest;
   } else if (a.sigmoid) {
-    g = dw * s * (1.0f - s);
+    g = dw * s * rest;
   } else {
     s = total > 0.0f ? s / total : 0.0f;
     mean = lanes_sum<L>(dw * s);
