@@ -99,7 +99,9 @@ __device__ __forceinline__ void act_both(float x, float& v, float& d) {
   } else {
     const float s = sigmoid_fast(2.0f * kGeluC * fmaf(kGeluA * x * x, x, x));
     v = x * s;
-    d = fmaf(v * (1.0f - s), 2.0f * kGeluC * fmaf(3.0f * kGeluA * x, x, 1.0f), s);
+    // (|x| >= 16: s is 0 or 1 and the first product 0, whose other factor must stay finite)
+    const float y = __builtin_amdgcn_fmed3f(x, -16.0f, 16.0f);
+    d = fmaf(v * (1.0f - s), 2.0f * kGeluC * fmaf(3.0f * kGeluA * y, y, 1.0f), s);
   }
 }
 
