@@ -54,6 +54,14 @@ __device__ __forceinline__ void wave_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// A point that no memory access moves across, in either direction: for waits that
+// count the loads issued after it.  (The comment marks it in the assembly.)
+__device__ __forceinline__ void order_point() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("; order point" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 struct MidArgs {
   const uint8_t* A;
   const uint8_t* as;
@@ -189,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
     dma_block<SVEC>(range_a(0), tile_a(0), rowb, K, 0, q);
     dma_block<SVEC>(range_w(0), tile_w(0), rowb, K, 0, q);
   }
+  order_point();                                // the wait below counts what comes after
   store_sc(s, 0);
   load_sc(s, 1);
 #pragma unroll
@@ -196,8 +205,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
     dma_block<SVEC>(range_a(1), tile_a(1), rowb, K, BK, q);
     dma_block<SVEC>(range_w(1), tile_w(1), rowb, K, BK, q);
   }
-  // stage 0 has landed when no more than stage 1's loads are in flight (at least
-  // 2 kBlocks + 1 instructions: the compiler may join the scale bytes' dwords)
+  order_point();
+  // stage 0 has landed when no more than stage 1's loads, those between the two order
+  // points, are in flight (at least 2 kBlocks + 1 instructions: the compiler may join
+  // the scale bytes' dwords)
   __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * kBlocks + 1));
   wait_lgkm();
   wave_barrier();
