@@ -474,7 +474,30 @@ def _part(t: Optional[torch.Tensor], shape, name: str):
 
 
 def _workspace(workspace: Optional[torch.Tensor], need: int, dev) -> torch.Tensor:
-    return torch.empty(max(need, 4), dtype=torch.uint8, device=dev) if workspace is None else workspace
+    if workspace is None:
+        return torch.empty(max(need, 4), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace
+
+
+def _check_operands(fmt: int, A, a_scales, g_a, W, w_scales, g_b, K: int):
+    """Codes, scale bytes and tensor scales of a product that reads them: the kernels take
+    the scales' sizes from the codes'."""
+    bs = {FP4_NVFP4: NV_BLOCK, FP4_MXFP4: MX_BLOCK}.get(fmt)
+    if A.shape[0] == 0 or W.numel() == 0 or bs is None or K % 32:
+        return                                   # nothing is read, or the library refuses the call
+    for t, name in ((A, "A"), (W, "W"), (a_scales, "a_scales"), (w_scales, "w_scales")):
+        if t.element_size() != 1:
+            raise TypeError(f"{name} must hold bytes")
+    if tuple(a_scales.shape) != (A.shape[0], K // bs):
+        raise ValueError(f"a_scales must have shape {(A.shape[0], K // bs)}, not {tuple(a_scales.shape)}")
+    rows = W.numel() // (K // 2)
+    if w_scales.shape[-1] != K // bs or w_scales.numel() != rows * (K // bs):
+        raise ValueError(f"w_scales must hold {K // bs} bytes for each of W's {rows} rows, not {tuple(w_scales.shape)}")
+    for t, name in ((g_a, "g_a"), (g_b, "g_b")):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32")
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -518,6 +541,7 @@ def fp4_scaled_gemm_fused(fmt: int, A: torch.Tensor, a_scales: torch.Tensor, g_a
     M, N = A.shape[0], W.shape[0]
     if A.shape[1] != K // 2 or W.shape[1] != K // 2:
         raise ValueError("A and W must be [rows, K/2] packed codes")
+    _check_operands(fmt, A, a_scales, g_a, W, w_scales, g_b, K)
     ga = None if g_a is None else g_a.reshape(1).contiguous()
     gb = None if g_b is None else g_b.reshape(1).contiguous()
     args, D, z, _held = _epilogue_args(M, N, activation, gated, bias, (N,), residual, preact_dtype,
@@ -548,6 +572,7 @@ def fp4_grouped_gemm_fused(fmt: int, A: torch.Tensor, a_scales: torch.Tensor, g_
     if offsets.dtype != torch.int32 or offsets.numel() != E + 1 or offsets.device != dev:
         raise ValueError("offsets must be int32 [E+1] on the operands' device")
     _same_device(dev, a_scales=a_scales, W=W, w_scales=w_scales, g_a=g_a, g_b=g_b)
+    _check_operands(fmt, A, a_scales, g_a, W, w_scales, g_b, K)
     W = W.contiguous()
     w_scales = w_scales.contiguous()
     offsets = offsets.contiguous()
