@@ -144,9 +144,6 @@ hipError_t launch_fused_gemm(bool mx, const uint8_t* A, const uint8_t* a_scales,
                              const Epilogue& ep, void* D, bool out_bf16, hipStream_t stream);
 
 // ---- gemm_few_rows.hip ----------------------------------------------------
-// Expected time (us) of launch_few_rows: `groups` (dense: 1) of row_items items of
-// `item` (16, 32 or 64) rows each.
-double few_rows_us(bool mx, int64_t groups, double row_items, int64_t N, int64_t K, int item);
 // What launch_fused_gemm does (dense: ngroups 0), `item` rows at a time.
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
                            const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
@@ -154,8 +151,6 @@ hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, c
                            const Epilogue& ep, void* D, bool out_bf16, int item, hipStream_t stream);
 
 // ---- gemm_mid.hip ---------------------------------------------------------
-// Expected time (us) of launch_mid, `groups` (dense: 1) of row_tiles tiles each.
-double mid_us(bool mx, int64_t groups, double row_tiles, int64_t N, int64_t K);
 // What launch_fused_gemm does, on 128 x 128 tiles (K > 0).
 hipError_t launch_mid(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a, const uint8_t* W,
                       const uint8_t* w_scales, const float* g_b, float g_d, int64_t ngroups,

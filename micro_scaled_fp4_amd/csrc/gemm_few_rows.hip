@@ -26,13 +26,12 @@
 // of 64 experts of 4096 x 7168, 0.90 GB of them used, 154 to 160 us, 5.7 TB/s, near
 // the card's read rate.  From 32 rows on the unpacking of W, once per 16 to 64 rows,
 // costs more than its bytes (64 experts of 32 rows each: 292 us).
-#include <math.h>
-
 #include <atomic>
 
 #include "epilogue.h"
 #include "fp4_device.h"
 #include "fp4_internal.h"
+#include "product_choice.h"
 #include "scale_bytes.h"
 
 using namespace fp4dev;
@@ -493,33 +492,13 @@ hipError_t launch_m(const FewArgs& a, int item, bool svec, bool out_bf16, hipStr
 
 namespace fp4impl {
 
-// Waves that split K: at least two pairs each, so that the partial tiles'
-// exchange is small beside the stream.
-static int k_split(int64_t K) {
-  const int64_t P = (K + 255) / 256;
-  return P >= 16 ? 8 : P >= 8 ? 4 : P >= 4 ? 2 : 1;
-}
-
-// Modelled time: a fixed part and, per value of K, one strip's time for each of the
-// strips that a slot goes through (whole units of S granules, every workgroup
-// waiting for the fullest).  Fitted to 26 sizes, dense and grouped.
-double few_rows_us(bool mx, int64_t groups, double row_items, int64_t N, int64_t K, int item) {
-  const int S = item == 64 ? 2 : 4, slots = kWaves / k_split(K);
-  const double granules = groups * row_items * ((N + 16 * slots - 1) / (16 * slots));
-  const double units = ceil(granules / (num_cus() * S));
-  const double strip = mx ? (item == 16 ? 0.33e-3 : item == 32 ? 0.48e-3 : 0.92e-3)
-                          : (item == 16 ? 0.45e-3 : item == 32 ? 0.62e-3 : 1.18e-3);
-  const double fixed = mx ? (item == 64 ? 6.8 : 5.1) : (item == 16 ? 6.7 : item == 32 ? 7.6 : 8.6);
-  return fixed + units * S * slots * K * strip;
-}
-
 hipError_t launch_few_rows(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a,
                            const uint8_t* W, const uint8_t* w_scales, const float* g_b, float g_d,
                            int64_t ngroups, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
                            const Epilogue& ep, void* D, bool out_bf16, int item, hipStream_t stream) {
   const FusedArgs f{ep.bias, ep.residual, ep.preact, ep.bias_bf16, ep.residual_bf16, ep.preact_bf16,
                     ep.activation, ep.gated, 0};
-  const FewArgs a{A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, k_split(K), offsets,
+  const FewArgs a{A, a_scales, W, w_scales, g_a, g_b, g_d, (int)M, (int)N, (int)K, few_rows_split(K), offsets,
                   (int)ngroups, D, f};
   const bool svec = K % 256 == 0 && (reinterpret_cast<uintptr_t>(a_scales) & 15) == 0 &&
                     (reinterpret_cast<uintptr_t>(w_scales) & 15) == 0;

@@ -24,8 +24,6 @@
 // 4096 x 4096 x 4096, where the larger tiles fill the device: 134 (117) and 57 (48).
 // All operands of a stage read at once, two barriers, loads two stages ahead: 108, 42;
 // 55, 26; and eight waves that split a stage's K were slower than these.
-#include <math.h>
-
 #include <atomic>
 
 #include "gemm_kernels.h"
@@ -327,15 +325,6 @@ hipError_t launch_mid_m(const MidArgs& a, bool svec, bool out_bf16, hipStream_t 
 }  // namespace
 
 namespace fp4impl {
-
-// Modelled time: a fixed part and the fullest CU's tiles times stages (two tiles on a
-// CU share its LDS and its MFMA pipes, so each takes longer than one alone).
-double mid_us(bool mx, int64_t groups, double row_tiles, int64_t N, int64_t K) {
-  const double tiles = ceil(groups * row_tiles * ((N + kTile - 1) / kTile) / num_cus());
-  const int64_t stages = (K + BK - 1) / BK;
-  if (tiles <= 1) return mx ? 7.1 + 0.61 * stages : 8.5 + 1.8 * stages;
-  return mx ? 7.1 + 0.89 * tiles * stages : 8.5 + 2.0 * tiles * stages;
-}
 
 hipError_t launch_mid(bool mx, const uint8_t* A, const uint8_t* a_scales, const float* g_a, const uint8_t* W,
                       const uint8_t* w_scales, const float* g_b, float g_d, int64_t ngroups,
