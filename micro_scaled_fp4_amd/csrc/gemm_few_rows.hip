@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
     return u;
   };
 
-  // ---- this wave's pairs [pbeg, pbeg + E): dealt evenly, the longer parts first
+  // ---- this wave's pairs [pbeg, pbeg + E): dealt evenly, the longer parts first (E > 0:
+  // K > 0, and there are no more waves to split it than pairs)
   const int P = (K + 255) / 256;
   const int pbase = P / KS, prem = P % KS;
   const int pbeg = part * pbase + min(part, prem), E = pbase + (part < prem ? 1 : 0);
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) buf[((wave * S + s) * RT + t) * 64 + lane] = acc[s][t];
     float alpha = a.g_d;
-    if (!MX) alpha = K > 0 ? ((*a.g_a) * a.g_b[cun.item.e]) * a.g_d : 0.0f;
+    if (!MX) alpha = ((*a.g_a) * a.g_b[cun.item.e]) * a.g_d;
     __syncthreads();
     const int cols = min(cun.size * gran, N - cun.n0);
     for (int i = threadIdx.x; i < cun.item.rows << cap; i += kThreads) {
@@ -451,13 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   };
 
   clear();
-  if (E == 0) {                                 // no pair for this wave: zeros in every unit
-    while (left > 0) {
-      cun = next_unit();
-      finish();
-    }
-    return;
-  }
   load_elem();
   while (live) elem();
 }
