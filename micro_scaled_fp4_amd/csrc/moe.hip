@@ -76,12 +76,10 @@ __device__ __forceinline__ float exp_accurate(float x) {
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e * r, 0x1.62e430p-1f, e);
 }
-// (v_rcp_f32: 1 ulp.)  Scores below 2^-126, float32's smallest normal number, are 0:
-// what holds them would be subnormal.
-__device__ __forceinline__ float sigmoid_accurate(float x) {
-  constexpr float kLeast = -0x1.5d589ep+6f;      // -126 ln 2
-  const float s = __builtin_amdgcn_rcpf(1.0f + exp_accurate(fminf(-x, -kLeast)));
-  return x < kLeast ? 0.0f : s;
+// Sigmoid as a selection value (v_rcp_f32: 1 ulp).  Values below 2^-126, float32's
+// smallest normal number, tie: from x = -88 down they are the same, at most e^-88.
+__device__ __forceinline__ float sigmoid_value(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_accurate(fminf(-x, 88.0f)));
 }
 // sigmoid(x) e^-c (c = 0 where x > 0) and, in rest, 1 - sigmoid(x), which loses no
 // digits next to 1.  A common c <= 0 near the largest x of a token keeps scores that
@@ -89,7 +87,8 @@ __device__ __forceinline__ float sigmoid_accurate(float x) {
 __device__ __forceinline__ float sigmoid_over(float x, float c, float& rest) {
   const float e = exp_accurate(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
   rest = x > 0.0f ? e * r : r;
-  return x > 0.0f ? r : exp_accurate(x - c) * r;
+  if (x > 0.0f) return r;
+  return (c < 0.0f ? exp_accurate(x - c) : e) * r;
 }
 
 // Float -> integer that orders like the float (-0 equal to +0).  Masked experts
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
       }
     };
     if (a.sigmoid)
-      select_by([](float x) { return sigmoid_accurate(x); });
+      select_by([](float x) { return sigmoid_value(x); });
     else
       select_by([&](float x) { return exp_accurate(x - top) * inv; });
   }
