@@ -15,8 +15,9 @@
 // bytes per instruction (full lines) and turned to the MFMA's operand layout
 // through a wave-private XOR-swizzled LDS tile; a pair's loads for all S strips
 // are in flight in registers while the pair before it computes, across units
-// (72 KB per CU in flight; two pairs ahead ran slower for want of registers).  A's codes are read from L2 per
-// pair, in the operand layout, and dequantized once for the S strips.
+// (72 KB per CU in flight; two pairs ahead ran slower for want of registers).  A's
+// codes are read from L2 per pair, in the operand layout, and dequantized once for the
+// S strips.
 // NVFP4: both operands to fp16 exactly (E2M1 x E4M3 has 6 significant bits),
 // v_mfma_f32_16x16x32_f16.  MXFP4: codes and E8M0 bytes straight into
 // v_mfma_scale_f32_16x16x128_f8f6f4.  W is the MFMA's first operand, so a lane
@@ -24,8 +25,9 @@
 //
 // Bound: HBM, W's bytes.  1 x 27648 x 5120 NVFP4 20 us, 4.0 TB/s; 16 tokens to 8
 // of 64 experts of 4096 x 7168, 0.90 GB of them used, 154 to 160 us, 5.7 TB/s, near
-// the card's read rate.  From 32 rows on the unpacking of W, once per 16 to 64 rows,
-// costs more than its bytes (64 experts of 32 rows each: 292 us).
+// the card's read rate.  From about 24 rows on the instructions bound it, the unpacking
+// of W once per 16 to 64 rows and the loops around the loads (64 experts of 32 rows
+// each: 292 us, 213 at the copy's rate).
 #include <atomic>
 
 #include "epilogue.h"
@@ -203,7 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_few_rows(FewArgs a) {
   int le = 0;                                   // next element to load: pair pbeg + le of lun
   bool live = false;                            // el holds an element
   auto load_elem = [&]() {
-    // past the last unit: empty ranges (no branch around the loads)
+    // past the last unit: empty ranges, not a branch.  (Units come from the groups' counts
+    // by lane shuffles, so the compiler does not see that the ranges are the same in all
+    // lanes and puts each load in a loop over the distinct ones, which runs once.)
     if (le == 0) {
       live = left > 0;
       if (live) lun = next_unit();

@@ -620,6 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       xcd_tile(b, T, tt);
       if (!group_tile_of(goff, ngroups, M, tt / tiles_n, t.e, tm, lo, hi)) return t;
       tn = tt % tiles_n;
+      // (uniform, which the compiler does not see: a grouped launch's loads are in loops
+      // over distinct ranges that run once)
       t.m_rows = hi - lo;
     } else {
       tile_of(b, tiles_m, tiles_n, tm, tn);

@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemm_mid(MidArgs a) {
     int t, hi = 0;
     xcd_tile(bid, T, t);
     group_tile_of<kTile>(a.offsets, a.groups, M, t / a.tiles_n, e, tm, lo, hi);
-    tn = t % a.tiles_n;
+    tn = t % a.tiles_n;                         // (uniform too, which the compiler does not see:
+                                                // W's loads are in loops that run once)
     m_rows = hi - lo;
     e = __builtin_amdgcn_readfirstlane(e);
     tm = __builtin_amdgcn_readfirstlane(tm);
