@@ -243,7 +243,7 @@ __device__ __forceinline__ void rotations(uint32_t k, int ln, F&& f) {
 // index, and selected or masked experts have key 0.
 // Bound: vector instructions, most of them in the rounds, where the lane that loses
 // its largest key looks through the others.
-// 32768 x 256 float32, sigmoid, bias, 4 of 8 groups, top 8: 22.6 us, 1.6 TB/s;
+// 32768 x 256 float32, sigmoid, bias, 4 of 8 groups, top 8: 22.4 us, 1.6 TB/s;
 // reading the logits by way of LDS, contiguous over the lanes, took 29.  1 x 64: 3 us.
 template <bool BF16, int EPL, int L>
 __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
