@@ -534,6 +534,116 @@ fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows,
                                 const int32_t* row_slots, int64_t T, int top_k, int64_t H,
                                 void* d_rows, fp4_dtype drt, float* d_weights, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A paged key/value cache held in FP4: tokens quantized as they are written,
+ * positions read back, and attention over the cache.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The cache of one layer: num_pages pages of page_size tokens, each with num_heads
+ * key and value rows of head_dim channels:
+ *   k_codes, v_codes    [num_pages, num_heads, page_size, head_dim / 2] packed E2M1 codes
+ *   k_scales, v_scales  [num_pages, num_heads, page_size, head_dim / bs] scale bytes:
+ *                       E4M3 per 16 channels (NVFP4) or E8M0 per 32 (MXFP4)
+ *   k_amax, v_amax      NVFP4: device floats, the given (calibrated) amax of all keys
+ *                       and of all values, as global_amax of nvfp4_quantize with
+ *                       amax_given; MXFP4: NULL
+ * format FP4_NVFP4 / FP4_MXFP4; 1 <= num_heads <= FP4_KV_MAX_HEADS; head_dim a multiple
+ * of 32 up to 256; page_size a power of two from 16 to 65536; 0 <= num_pages < 2^31.
+ * The four arrays are 16-byte aligned.  The struct is read during the call only.
+ *
+ * Sequences.  The calls take num_seqs (B) sequences:
+ *   offsets  device int32 [B + 1], non-decreasing: rows offsets[b] .. offsets[b+1] of
+ *            the [T, ...] operands belong to sequence b.  Rows past offsets[B] belong to
+ *            none: they are not read and their outputs not written.
+ *   lengths  device int32 [B]: positions of each sequence, those of its rows included
+ *   pages    device int32 [B, max_pages]: position t of sequence b sits in page
+ *            pages[b][t / page_size], slot t % page_size.  An entry outside
+ *            [0, num_pages) is a hole: its positions are not written, read as zeros and
+ *            are seen by no query.
+ * Row i of the n rows of a sequence sits at position lengths[b] - n + i.  All of them are
+ * read on the device (the calls can be captured in a graph and replayed with other
+ * contents).  Offsets outside [0, T] and lengths outside [0, max_pages * page_size] are
+ * clamped, so no memory outside the arrays is touched; offsets that decrease leave the
+ * outputs unspecified.  0 <= B <= FP4_KV_MAX_SEQS, 0 <= T <= FP4_KV_MAX_ROWS, max_pages *
+ * page_size <= 2^30, B * max_pages < 2^40, else FP4_ERR_SHAPE.
+ */
+#define FP4_KV_MAX_HEADS 1024
+#define FP4_KV_MAX_SEQS (1LL << 16)
+#define FP4_KV_MAX_ROWS (1LL << 24)
+typedef struct {
+  fp4_format format;
+  int num_heads;
+  int head_dim;
+  int page_size;
+  int64_t num_pages;
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_amax;
+  const float* v_amax;
+} fp4_kv_cache;
+
+/*
+ * kv_cache_write -- quantizes the rows of k and v [T, num_heads, head_dim] (FP4_F32 or
+ * FP4_BF16) into their positions of the cache, bit for bit as nvfp4_quantize with
+ * amax_given or mxfp4_quantize do for each row.
+ *   k_stride, v_stride  elements from one token to the next (0 <= stride; heads and
+ *                       channels are contiguous), so keys and values can be read out of
+ *                       a joint projection's rows
+ * Rows at negative positions (more rows than lengths[b]) and in holes are skipped.
+ * Bytes of other positions are left as they are; a slot that several rows of the call
+ * map to holds unspecified bytes.  k and v aligned to their element.
+ */
+fp4_status kv_cache_write(const fp4_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, fp4_dtype t, int64_t T, int64_t num_seqs,
+                          const int32_t* offsets, const int32_t* lengths, const int32_t* pages,
+                          int64_t max_pages, hipStream_t stream);
+
+/*
+ * kv_cache_read -- the values of cached positions: row offsets[b] + i gets position
+ * starts[b] + i of sequence b (starts NULL: the sequence's last rows, lengths[b] - n + i),
+ * zeros where that is not in [0, lengths[b]) or in a hole.
+ *   starts  device int32 [B] or NULL
+ *   k, v    out [T, num_heads, head_dim] FP4_F32 or FP4_BF16, as fp4_dequantize
+ */
+fp4_status kv_cache_read(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs, const int32_t* offsets,
+                         const int32_t* starts, const int32_t* lengths, const int32_t* pages,
+                         int64_t max_pages, void* k, void* v, fp4_dtype t, hipStream_t stream);
+
+/*
+ * kv_cache_attention -- attention of query rows over their sequences' cached positions:
+ *   out[r, h] = sum_t p_t v_t,  p = softmax over the seen t of scale * <q[r, h], k_t>,
+ *   lse[r, h] = log(sum over the seen t of exp(scale * <q[r, h], k_t>))
+ * with k, v the dequantized rows of head h / (num_q_heads / num_heads).  The row at
+ * position p of a sequence sees the positions t < lengths[b] outside holes with
+ *   t <= p (causal != 0) and t > p - window (window > 0).
+ * A row that sees nothing gets out = 0 and lse = -inf.  (A prompt is written, then
+ * attends; so does a single decoded token.)
+ *   q         [T, num_q_heads, head_dim] FP4_F32 or FP4_BF16, q_stride elements from one
+ *             token to the next (heads and channels contiguous)
+ *   scale     finite; window >= 0, and 0 unless causal is set
+ *   out       [T, num_q_heads, head_dim] FP4_F32 or FP4_BF16
+ *   lse       out float32 [T, num_q_heads], or NULL
+ *   workspace >= kv_cache_attention_workspace_bytes bytes, 16-byte aligned; its contents
+ *             matter only within the call
+ * Scores, softmax and sums are float32.  With bf16 q and out the softmax weights meet the
+ * values as fp16 (half a step: 2^-12 of a weight); float32 operands are split into two fp16
+ * parts.  A key or value below 2^-36 of the largest scale among 64 positions may count as 0
+ * (MXFP4).
+ * num_q_heads a multiple of num_heads up to 2^16, T * num_q_heads <= 2^30, else
+ * FP4_ERR_SHAPE.
+ */
+size_t kv_cache_attention_workspace_bytes(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
+                                          int num_q_heads);
+fp4_status kv_cache_attention(const fp4_kv_cache* cache, const void* q, int64_t q_stride, fp4_dtype qt,
+                              int64_t T, int num_q_heads, int64_t num_seqs, const int32_t* offsets,
+                              const int32_t* lengths, const int32_t* pages, int64_t max_pages,
+                              float scale, int causal, int64_t window, void* out, fp4_dtype ot,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
 /* Human-readable text of a status (static storage). */
 const char* fp4_status_string(fp4_status s);
 

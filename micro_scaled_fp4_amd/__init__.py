@@ -94,6 +94,14 @@ SIGNATURES = {
     "moe_combine_backward": (ctypes.c_int, [_c_p, ctypes.c_int, _c_p, ctypes.c_int, _c_p, _c_p,
                                             _c_p, _c_i64, ctypes.c_int, _c_i64, _c_p, ctypes.c_int,
                                             _c_p, _c_p]),
+    "kv_cache_write": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_i64, ctypes.c_int, _c_i64, _c_i64, _c_p,
+                                      _c_p, _c_p, _c_i64, _c_p]),
+    "kv_cache_read": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p,
+                                     ctypes.c_int, _c_p]),
+    "kv_cache_attention_workspace_bytes": (ctypes.c_size_t, [_c_p, _c_i64, _c_i64, ctypes.c_int]),
+    "kv_cache_attention": (ctypes.c_int, [_c_p, _c_p, _c_i64, ctypes.c_int, _c_i64, ctypes.c_int, _c_i64, _c_p,
+                                          _c_p, _c_p, _c_i64, ctypes.c_float, ctypes.c_int, _c_i64, _c_p,
+                                          ctypes.c_int, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "fp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fp4_last_hip_error": (ctypes.c_char_p, []),
 }
@@ -753,3 +761,169 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, weights: torch.Te
                                              _dtype_code(d_rows.dtype), _ptr(d_weights), _stream(dev))
     _check(st, "moe_combine_backward")
     return d_rows, d_weights
+
+
+# --------------------------------------------------------- key/value cache ----
+class _KVCacheStruct(ctypes.Structure):
+    """fp4_kv_cache of include/fp4.h."""
+    _fields_ = [("format", ctypes.c_int), ("num_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", _c_i64), ("k_codes", _c_p), ("k_scales", _c_p),
+                ("v_codes", _c_p), ("v_scales", _c_p), ("k_amax", _c_p), ("v_amax", _c_p)]
+
+
+class KVCache:
+    """One layer's paged key/value cache in FP4: k_codes, v_codes u8 [num_pages, num_heads,
+    page_size, head_dim / 2], k_scales, v_scales u8 [num_pages, num_heads, page_size,
+    head_dim / bs] and, for NVFP4, the given amax of all keys and of all values (a float or a
+    one-element tensor; float32[1] on the device afterwards).  page_size is a power of two
+    from 16 on, head_dim a multiple of 32 up to 256.  The tensors are used in place."""
+
+    __slots__ = ("fmt", "num_pages", "num_heads", "page_size", "head_dim", "device", "k_codes", "k_scales",
+                 "v_codes", "v_scales", "k_amax", "v_amax", "_struct", "_address")
+
+    def __init__(self, fmt: int, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor, k_amax=None, v_amax=None):
+        bs = {FP4_NVFP4: NV_BLOCK, FP4_MXFP4: MX_BLOCK}.get(fmt)
+        if bs is None:
+            raise ValueError("fmt must be FP4_NVFP4 or FP4_MXFP4")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [num_pages, num_heads, page_size, head_dim / 2]")
+        pages, heads, page, half = k_codes.shape
+        dim = 2 * half
+        if dim % 32 or not 32 <= dim <= 256:
+            raise ValueError("head_dim must be a multiple of 32 from 32 to 256")
+        if page < 16 or page > 65536 or page & (page - 1):
+            raise ValueError("page_size must be a power of two from 16 to 65536")
+        for t, name, last in ((k_codes, "k_codes", half), (k_scales, "k_scales", dim // bs),
+                              (v_codes, "v_codes", half), (v_scales, "v_scales", dim // bs)):
+            if not t.is_cuda or t.device != k_codes.device:
+                raise ValueError(f"{name} must be a GPU tensor on k_codes' device")
+            if t.element_size() != 1:
+                raise TypeError(f"{name} must hold bytes")
+            if tuple(t.shape) != (pages, heads, page, last) or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {(pages, heads, page, last)}, not {tuple(t.shape)}")
+        if (fmt == FP4_NVFP4) != (k_amax is not None and v_amax is not None) or \
+                (k_amax is None) != (v_amax is None):
+            raise ValueError("k_amax and v_amax are given for NVFP4 and only there")
+        self.fmt, self.num_pages, self.num_heads, self.page_size, self.head_dim = fmt, pages, heads, page, dim
+        self.device = k_codes.device
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_amax, self.v_amax = _amax_arg(k_amax, self.device), _amax_arg(v_amax, self.device)
+        self._struct = _KVCacheStruct(fmt, heads, dim, page, pages, _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
+                                      _ptr(v_scales), _ptr(self.k_amax), _ptr(self.v_amax))
+        self._address = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, fmt: int, num_pages: int, num_heads: int, page_size: int, head_dim: int, k_amax=None,
+              v_amax=None, device="cuda"):
+        """A cache with pages of its own (their contents undefined until written)."""
+        bs = NV_BLOCK if fmt == FP4_NVFP4 else MX_BLOCK
+
+        def part(last):
+            return torch.empty(num_pages, num_heads, page_size, last, dtype=torch.uint8, device=device)
+
+        return cls(fmt, part(head_dim // 2), part(head_dim // bs), part(head_dim // 2), part(head_dim // bs),
+                   k_amax, v_amax)
+
+
+def _call_on(dev: torch.device, fn, *args) -> int:
+    """fn(*args, the device's current stream) with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(dev))
+
+
+def _sequences(cache: KVCache, offsets: torch.Tensor, lengths: torch.Tensor, pages: torch.Tensor):
+    """(B, offsets, lengths, pages, max_pages) of a cache call, checked."""
+    B = lengths.numel()
+    if pages.dim() != 2:
+        raise ValueError("pages must be [B, max_pages]")
+    if offsets.device != cache.device or lengths.device != cache.device or pages.device != cache.device:
+        raise ValueError(f"offsets, lengths and pages must be on {cache.device}")
+    offsets = _typed(offsets, torch.int32, (B + 1,), "offsets")
+    lengths = _typed(lengths, torch.int32, (B,), "lengths")
+    pages = _typed(pages, torch.int32, (B, pages.shape[1]), "pages")
+    return B, offsets, lengths, pages, pages.shape[1]
+
+
+def _head_rows(t: torch.Tensor, heads: Optional[int], dim: int, dev, name: str):
+    """t [T, heads, dim] with contiguous heads (copied where they are not) and its token stride."""
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {heads or 'num_q_heads'}, {dim}], not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        t = t.contiguous()
+    return t, t.stride(0)
+
+
+def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
+                   lengths: torch.Tensor, pages: torch.Tensor) -> None:
+    """Quantizes k and v [T, num_heads, head_dim] bf16/f32 into their positions: rows offsets[b] ..
+    offsets[b + 1] are the last positions before lengths[b] of sequence b, whose position t sits in page
+    pages[b, t // page_size] (int32; outside [0, num_pages): skipped).  Views of a joint projection's rows
+    are read in place."""
+    dev = cache.device
+    k, ks = _head_rows(k, cache.num_heads, cache.head_dim, dev, "k")
+    v, vs = _head_rows(v, cache.num_heads, cache.head_dim, dev, "v")
+    if v.shape[0] != k.shape[0] or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same rows and type")
+    B, offsets, lengths, pages, wide = _sequences(cache, offsets, lengths, pages)
+    _check(_call_on(dev, load_library().kv_cache_write, cache._address, _ptr(k), ks, _ptr(v), vs,
+                    _dtype_code(k.dtype), k.shape[0], B, _ptr(offsets), _ptr(lengths), _ptr(pages), wide),
+           "kv_cache_write")
+
+
+def kv_cache_read(cache: KVCache, offsets: torch.Tensor, lengths: torch.Tensor, pages: torch.Tensor, rows: int,
+                  starts: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16, out=None):
+    """(k, v) [rows, num_heads, head_dim]: row offsets[b] + i holds position starts[b] + i of sequence b
+    (without starts: its last rows), zeros outside [0, lengths[b]) and in holes.  Rows past offsets[B] are not
+    written.  out: (k, v) to write into."""
+    dev = cache.device
+    B, offsets, lengths, pages, wide = _sequences(cache, offsets, lengths, pages)
+    if starts is not None:
+        _same_device(dev, starts=starts)
+        starts = _typed(starts, torch.int32, (B,), "starts")
+    shape = (int(rows), cache.num_heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+    for t in out:
+        if tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev or t.dtype != out[0].dtype:
+            raise ValueError(f"out must be two contiguous {shape} tensors of one type on {dev}")
+    k, v = out
+    _check(_call_on(dev, load_library().kv_cache_read, cache._address, shape[0], B, _ptr(offsets), _ptr(starts),
+                    _ptr(lengths), _ptr(pages), wide, _ptr(k), _ptr(v), _dtype_code(k.dtype)), "kv_cache_read")
+    return k, v
+
+
+def kv_cache_attention(cache: KVCache, q: torch.Tensor, offsets: torch.Tensor, lengths: torch.Tensor,
+                       pages: torch.Tensor, scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                       out_dtype: Optional[torch.dtype] = None, return_lse: bool = False,
+                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Attention of q [T, num_q_heads, head_dim] bf16/f32 over the cached positions of each row's sequence
+    (query head h over key/value head h // (num_q_heads / num_heads)): out [T, num_q_heads, head_dim]
+    (out_dtype: q's unless given) or, with return_lse, (out, lse float32 [T, num_q_heads]).  Row i of n sits at
+    position lengths[b] - n + i and sees the positions up to its own (causal) and after its own minus window
+    (window > 0); 0 and -inf where it sees none.  scale: 1 / sqrt(head_dim) unless given.  Rows past offsets[B]
+    are not written."""
+    dev = cache.device
+    q, qs = _head_rows(q, None, cache.head_dim, dev, "q")
+    T, heads = q.shape[0], q.shape[1]
+    if heads < 1 or heads % cache.num_heads:
+        raise ValueError(f"q's {heads} heads must be a multiple of the cache's {cache.num_heads}")
+    B, offsets, lengths, pages, wide = _sequences(cache, offsets, lengths, pages)
+    if out is None:
+        out = torch.empty(T, heads, cache.head_dim, dtype=out_dtype or q.dtype, device=dev)
+    elif tuple(out.shape) != tuple(q.shape) or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be contiguous {tuple(q.shape)} on {dev}")
+    lse = torch.empty(T, heads, dtype=torch.float32, device=dev) if return_lse else None
+    lib = load_library()
+    need = lib.kv_cache_attention_workspace_bytes(cache._address, T, B, heads)
+    workspace = _workspace(workspace, need, dev)
+    _check(_call_on(dev, lib.kv_cache_attention, cache._address, _ptr(q), qs, _dtype_code(q.dtype), T, heads, B,
+                    _ptr(offsets), _ptr(lengths), _ptr(pages), wide,
+                    cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),
+                    _ptr(out), _dtype_code(out.dtype), _ptr(lse), _ptr(workspace), _nbytes(workspace)),
+           "kv_cache_attention")
+    return (out, lse) if return_lse else out

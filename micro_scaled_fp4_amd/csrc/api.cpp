@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -669,6 +670,124 @@ fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows,
                                               weights, slot_rows, row_slots, T, top_k, d_rows,
                                               drt == FP4_BF16, d_weights, stream),
                  "moe_combine_backward");
+  return FP4_OK;
+}
+
+namespace {
+
+// Checks of what the three cache calls share; *none: there is nothing to do.
+fp4_status check_kv(const fp4_kv_cache* c, int64_t T, int64_t B, const int32_t* offsets, const int32_t* lengths,
+                    const int32_t* pages, int64_t max_pages, bool* none) {
+  *none = false;
+  if (c == nullptr) return FP4_ERR_NULL;
+  if (c->format != FP4_NVFP4 && c->format != FP4_MXFP4) return FP4_ERR_DTYPE;
+  if (c->num_heads < 1 || c->num_heads > FP4_KV_MAX_HEADS || c->head_dim < 32 || c->head_dim > 256 ||
+      c->head_dim % 32 != 0 || c->page_size < 16 || c->page_size > 65536 ||
+      (c->page_size & (c->page_size - 1)) != 0 || c->num_pages < 0 || c->num_pages >= (int64_t)1 << 31)
+    return FP4_ERR_SHAPE;
+  if (T < 0 || T > FP4_KV_MAX_ROWS || B < 0 || B > FP4_KV_MAX_SEQS || max_pages < 0 ||
+      max_pages > ((int64_t)1 << 30) / c->page_size)
+    return FP4_ERR_SHAPE;
+  const bool mx = c->format == FP4_MXFP4;
+  if (mx && (c->k_amax != nullptr || c->v_amax != nullptr)) return FP4_ERR_DTYPE;
+  *none = T == 0 || B == 0;
+  if (*none) return FP4_OK;
+  if (offsets == nullptr || lengths == nullptr || (max_pages > 0 && pages == nullptr)) return FP4_ERR_NULL;
+  if (!mx && (c->k_amax == nullptr || c->v_amax == nullptr)) return FP4_ERR_NULL;
+  if (c->num_pages > 0 && (c->k_codes == nullptr || c->k_scales == nullptr || c->v_codes == nullptr ||
+                           c->v_scales == nullptr))
+    return FP4_ERR_NULL;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
+      !aligned(c->v_scales, 16) || !aligned(c->k_amax, 4) || !aligned(c->v_amax, 4) || !aligned(offsets, 4) ||
+      !aligned(lengths, 4) || !aligned(pages, 4))
+    return FP4_ERR_ALIGN;
+  return FP4_OK;
+}
+
+fp4impl::KvCache kv_of(const fp4_kv_cache* c, int64_t T, int64_t B, const int32_t* offsets, const int32_t* lengths,
+                       const int32_t* pages, int64_t max_pages) {
+  return {c->format == FP4_MXFP4, c->num_heads, c->head_dim, __builtin_ctz((unsigned)c->page_size), c->num_pages,
+          c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->k_amax, c->v_amax, (int)T, (int)B, offsets,
+          lengths, pages, max_pages, (int)(max_pages * c->page_size)};
+}
+
+}  // namespace
+
+fp4_status kv_cache_write(const fp4_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, fp4_dtype t, int64_t T, int64_t num_seqs,
+                          const int32_t* offsets, const int32_t* lengths, const int32_t* pages,
+                          int64_t max_pages, hipStream_t stream) {
+  if (!valid_dtype(t)) return FP4_ERR_DTYPE;
+  bool none;
+  fp4_status st = check_kv(cache, T, num_seqs, offsets, lengths, pages, max_pages, &none);
+  if (st != FP4_OK) return st;
+  if (k_stride < 0 || v_stride < 0 || k_stride > (int64_t)1 << 32 || v_stride > (int64_t)1 << 32)
+    return FP4_ERR_SHAPE;
+  if (none) return FP4_OK;
+  if (k == nullptr || v == nullptr) return FP4_ERR_NULL;
+  if (!elem_aligned(k, t) || !elem_aligned(v, t)) return FP4_ERR_ALIGN;
+  if ((st = check_arch()) != FP4_OK) return st;
+  FP4_TRY_LAUNCH(fp4impl::launch_kv_write(kv_of(cache, T, num_seqs, offsets, lengths, pages, max_pages), k, k_stride,
+                                          v, v_stride, t == FP4_BF16, stream),
+                 "kv_cache_write");
+  return FP4_OK;
+}
+
+fp4_status kv_cache_read(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs, const int32_t* offsets,
+                         const int32_t* starts, const int32_t* lengths, const int32_t* pages,
+                         int64_t max_pages, void* k, void* v, fp4_dtype t, hipStream_t stream) {
+  if (!valid_dtype(t)) return FP4_ERR_DTYPE;
+  bool none;
+  fp4_status st = check_kv(cache, T, num_seqs, offsets, lengths, pages, max_pages, &none);
+  if (st != FP4_OK) return st;
+  if (none) return FP4_OK;
+  if (k == nullptr || v == nullptr) return FP4_ERR_NULL;
+  if (!elem_aligned(k, t) || !elem_aligned(v, t) || !aligned(starts, 4)) return FP4_ERR_ALIGN;
+  if (k == v) return FP4_ERR_ALIAS;
+  if ((st = check_arch()) != FP4_OK) return st;
+  FP4_TRY_LAUNCH(fp4impl::launch_kv_read(kv_of(cache, T, num_seqs, offsets, lengths, pages, max_pages), starts, k, v,
+                                         t == FP4_BF16, stream),
+                 "kv_cache_read");
+  return FP4_OK;
+}
+
+size_t kv_cache_attention_workspace_bytes(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
+                                          int num_q_heads) {
+  if (cache == nullptr || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 ||
+      num_q_heads > 1 << 16 || T < 1 || T > FP4_KV_MAX_ROWS || num_seqs < 1 || num_seqs > FP4_KV_MAX_SEQS ||
+      cache->head_dim < 32 || cache->head_dim > 256)
+    return 0;
+  return fp4impl::kv_attention_workspace_bytes(T, num_seqs, num_q_heads, cache->num_heads, cache->head_dim);
+}
+
+fp4_status kv_cache_attention(const fp4_kv_cache* cache, const void* q, int64_t q_stride, fp4_dtype qt,
+                              int64_t T, int num_q_heads, int64_t num_seqs, const int32_t* offsets,
+                              const int32_t* lengths, const int32_t* pages, int64_t max_pages,
+                              float scale, int causal, int64_t window, void* out, fp4_dtype ot,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  if (!valid_dtype(qt) || !valid_dtype(ot)) return FP4_ERR_DTYPE;
+  bool none;
+  fp4_status st = check_kv(cache, T, num_seqs, offsets, lengths, pages, max_pages, &none);
+  if (st != FP4_OK) return st;
+  if (num_q_heads < 1 || num_q_heads > 1 << 16 || num_q_heads % cache->num_heads != 0 ||
+      T * num_q_heads > (int64_t)1 << 30 || q_stride < 0 || q_stride > (int64_t)1 << 32 || window < 0 ||
+      (window > 0 && !causal) || !(std::fabs(scale) <= 3.0e38f))
+    return FP4_ERR_SHAPE;
+  if (none) return FP4_OK;
+  if (q == nullptr || out == nullptr) return FP4_ERR_NULL;
+  if (workspace_bytes < kv_cache_attention_workspace_bytes(cache, T, num_seqs, num_q_heads) ||
+      workspace == nullptr)
+    return FP4_ERR_WORKSPACE;
+  if (!elem_aligned(q, qt) || !elem_aligned(out, ot) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return FP4_ERR_ALIGN;
+  if (out == q || out == (void*)lse) return FP4_ERR_ALIAS;
+  if ((st = check_arch()) != FP4_OK) return st;
+  const fp4impl::AttendProblem p{q, q_stride, qt == FP4_BF16, ot == FP4_BF16, num_q_heads, scale, causal != 0,
+                                 (int)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30), out, lse, workspace};
+  FP4_TRY_LAUNCH(fp4impl::launch_kv_attention(kv_of(cache, T, num_seqs, offsets, lengths, pages, max_pages), p,
+                                              stream),
+                 "kv_cache_attention");
   return FP4_OK;
 }
 

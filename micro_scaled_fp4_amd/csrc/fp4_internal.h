@@ -208,6 +208,40 @@ hipError_t launch_combine_grad(const void* dy, bool dy_bf16, const void* rows, b
                                const int32_t* row_slots, int64_t T, int top_k, void* d_rows, bool dr_bf16,
                                float* d_weights, hipStream_t stream);
 
+// ---- kv_cache.hip, kv_attention.hip ------------------------------------------
+// The cache and the sequences of a call, as the kernels take them (the arrays as
+// include/fp4.h describes them).
+struct KvCache {
+  bool mx;
+  int heads, dim, page_shift;
+  int64_t num_pages;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const float *k_amax, *v_amax;
+  int rows, seqs;                // T, B
+  const int32_t *offsets, *lengths, *pages;
+  int64_t max_pages;
+  int capacity;                  // max_pages * page_size
+};
+hipError_t launch_kv_write(const KvCache& c, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           bool bf16, hipStream_t stream);
+hipError_t launch_kv_read(const KvCache& c, const int32_t* starts, void* k, void* v, bool bf16,
+                          hipStream_t stream);
+
+struct AttendProblem {
+  const void* q;
+  int64_t q_stride;
+  bool q_bf16, out_bf16;
+  int q_heads;
+  float scale;
+  bool causal;
+  int window;                    // 0: none
+  void* out;
+  float* lse;
+  void* workspace;
+};
+size_t kv_attention_workspace_bytes(int64_t T, int64_t seqs, int q_heads, int heads, int dim);
+hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& p, hipStream_t stream);
+
 // *out = s_global of the tensor amax *amax (one thread).
 hipError_t launch_nv_global_scale(const float* amax, float* out, hipStream_t stream);
 
