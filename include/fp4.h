@@ -623,7 +623,7 @@ fp4_status kv_cache_read(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
  * attends; so does a single decoded token.)
  *   q         [T, num_q_heads, head_dim] FP4_F32 or FP4_BF16, q_stride elements from one
  *             token to the next (heads and channels contiguous)
- *   scale     finite; window >= 0, and 0 unless causal is set
+ *   scale     |scale| <= 2^120; window >= 0, and 0 unless causal is set
  *   out       [T, num_q_heads, head_dim] FP4_F32 or FP4_BF16
  *   lse       out float32 [T, num_q_heads], or NULL
  *   workspace >= kv_cache_attention_workspace_bytes bytes, 16-byte aligned; its contents

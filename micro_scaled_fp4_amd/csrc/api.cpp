@@ -772,7 +772,7 @@ fp4_status kv_cache_attention(const fp4_kv_cache* cache, const void* q, int64_t 
   if (st != FP4_OK) return st;
   if (num_q_heads < 1 || num_q_heads > 1 << 16 || num_q_heads % cache->num_heads != 0 ||
       T * num_q_heads > (int64_t)1 << 30 || q_stride < 0 || q_stride > (int64_t)1 << 32 || window < 0 ||
-      (window > 0 && !causal) || !(std::fabs(scale) <= 3.0e38f))
+      (window > 0 && !causal) || !(std::fabs(scale) <= 0x1p120f))
     return FP4_ERR_SHAPE;
   if (none) return FP4_OK;
   if (q == nullptr || out == nullptr) return FP4_ERR_NULL;

@@ -1,0 +1,204 @@
+// What the two attention kernels over a paged FP4 cache share: operands on their way to the
+// fp16 MFMAs, query rows, masks, and a row's results.
+//
+// Mathematics.  Scores are taken as S^T = K Q^T and outputs as O^T = V^T P^T, so a query row is
+// a lane (of 16 or 32) in both products: its maximum, sum and factors are per-lane values, and
+// the weights leave the first product's accumulators in the order of positions in which the
+// second takes them, if V's rows are picked in that order too.  Softmax in base 2 with a running
+// maximum m and sum l:
+//   x = c s,  c = |scale| log2(e) (factors of q's and k's scaling),  P = 2^(x - m + 15).
+//
+// Why fp16.  A value of the cache is E2M1 x its block scale.  NVFP4: E2M1 x E4M3 has at most 6
+// significant bits and lies in [2^-10, 2688], exact in fp16; the tensor scale joins c and the
+// output.  MXFP4: E8M0 scales are taken relative to the largest (2^(byte - ref) 2^13), exact
+// down to 2^-36 of it; the reference joins c (keys) and is a running one like m (values).  A row
+// of q is scaled by a power of two to a maximum in [2^14, 2^15): bf16 values are exact then
+// (down to 2^-29 of the maximum), float32 ones are taken as two fp16 parts (22 bits).  P is
+// rounded to fp16, half a step being 2^-12 of a weight, against 2^-8 of the bf16 output; its
+// factor 2^15 keeps weights down to 2^-29 of the largest at full precision, which many small
+// weights next to one large need.  With float32 operands P is two fp16 parts as well.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp4_device.h"
+#include "fp4_internal.h"
+#include "kv_units.h"
+#include "scale_bytes.h"
+
+namespace fp4dev {
+
+using fp4impl::AttendProblem;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kWeightBits = 15.0f;            // P is 2^15 at the maximum
+
+// The larger of v in lanes l and l ^ 32, or l and l ^ 16.
+__device__ __forceinline__ float max_over_halves(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_over_rows(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_over_halves(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Largest of all lanes' v (v >= 0), the same in all.
+__device__ __forceinline__ int wave_max_lanes(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// Eight values of one dword of codes.  NVFP4: s is the block's E4M3 value x 2^-8 twice
+// (e4m3_h2); MXFP4: fs is a power of two.
+__device__ __forceinline__ f16x8 mx8(uint32_t codes, float fs) {
+  const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, fs, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, fs, 1);
+  const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, fs, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, fs, 3);
+  return f16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+// 2^(byte - ref + 13), 2^-126 at the least (a value of at most 6 x that is 0 in fp16).
+__device__ __forceinline__ float mx_factor(uint32_t byte, int ref) {
+  return __uint_as_float((uint32_t)max((int)byte - ref + 140, 1) << 23);
+}
+
+// A descriptor of `bytes` bytes from p on, the same in all lanes by construction (the compiler
+// would put a loop around each load otherwise).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const uint8_t* p, int bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0, __builtin_amdgcn_readfirstlane(bytes),
+                                           kBufferWord3);
+}
+
+// A query row of a tile: token row r of the call and query head h, or none.
+struct QueryRow {
+  int64_t r;
+  int h;
+  int first, last;               // positions that it sees: first <= t <= last
+};
+
+// Row `rho` (packed) of unit u.  Where there is none (h < 0) no position is masked: the row's q is
+// taken as 0 and its results go nowhere.
+__device__ __forceinline__ QueryRow query_row(const Unit& u, const UnitPlan& p, int head, int rho, int rows_end, int t1) {
+  QueryRow q{0, -1, 0, 0x7fffffff};
+  if (rho >= rows_end) return q;
+  const int i = rho / p.group;
+  q.r = u.begin + i;
+  q.h = head * p.group + (rho - i * p.group);
+  const int pos = u.length - u.n + i;
+  q.first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  q.last = p.causal ? min(pos, t1 - 1) : t1 - 1;
+  return q;
+}
+
+// Eight consecutive values of a query row.  VEC: 16-byte aligned.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* q, int64_t i, bool vec, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(q) + i;
+    if (vec) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(w[j]);
+        v[2 * j + 1] = bf16_hi(w[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
+    }
+  } else {
+    const float* p = static_cast<const float*>(q) + i;
+    if (vec) {
+      const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p[j];
+    }
+  }
+}
+
+// The power of two that brings a row of maximum `top` into [2^14, 2^15), and its inverse.
+__device__ __forceinline__ void row_factors(float top, float& f, float& inverse) {
+  const int e = max((int)(__float_as_uint(top) >> 23), 15);
+  f = __uint_as_float((uint32_t)(268 - e) << 23);
+  inverse = __uint_as_float((uint32_t)(e - 14) << 23);
+}
+
+// Two fp16 parts of eight float32 values (hi + lo, 22 bits); lo is left out where !SPLIT.
+template <bool SPLIT>
+__device__ __forceinline__ void to_f16(const float (&v)[8], f16x8& hi, f16x8& lo) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    hi[j] = (_Float16)v[j];
+    if constexpr (SPLIT) lo[j] = (_Float16)(v[j] - (float)hi[j]);
+  }
+}
+
+// Four consecutive output values.
+__device__ __forceinline__ void store4(void* out, bool bf16, bool vec, int64_t i, f32x4 v) {
+  if (bf16) {
+    uint16_t* p = static_cast<uint16_t*>(out) + i;
+    const u32x2 w{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])};
+    if (vec) {
+      *reinterpret_cast<u32x2*>(p) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(out) + i;
+    if (vec) {
+      *reinterpret_cast<f32x4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = v[j];
+    }
+  }
+}
+
+// A part's results in the workspace: for each of its rows m and l, then the outputs [rows][DP]
+// as sums of P v, in the values' own unit.
+__device__ __forceinline__ float* part_of(const UnitPlan& p, int heads, int head, int part, int dp) {
+  return p.parts + ((int64_t)part * heads + head) * p.rows * (dp + 2);
+}
+
+// lse of a row with running maximum m and sum l.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0 ? (m + __builtin_amdgcn_logf(l) - kWeightBits) * kLn2 : -INFINITY;
+}
+
+// Whether the parts of u's tile have room in the workspace (always, unless offsets decrease).
+__device__ __forceinline__ bool has_room(const UnitPlan& p, const Unit& u) {
+  return u.count == 1 || (u.part0 >= 0 && u.part0 + u.count <= p.max_parts);
+}
+
+// Records unit u's tile for k_join_parts (by the first part), and how many tiles there are.
+__device__ __forceinline__ void note_tile(const UnitPlan& p, const Unit& u, int unit, int rows) {
+  if (threadIdx.x != 0) return;
+  if (unit == 0) static_cast<TileParts*>(p.tiles)[p.max_slots].begin = u.slots;
+  if (u.any && u.part == 0 && u.slot >= 0 && u.slot < p.max_slots)
+    static_cast<TileParts*>(p.tiles)[u.slot] = {u.begin, u.tile * p.rows, rows, u.part0, u.count, {0, 0, 0}};
+}
+
+}  // namespace fp4dev

@@ -1,108 +1,113 @@
-// Attention over a paged key/value cache in FP4 (include/fp4.h, kv_cache_attention).
-//
-// One wave per query row and head, in float32: 64 positions at a time, a lane per
-// position for the scores, a lane per channel for the weighted sum, with the running
-// maximum and sum of the softmax.
+// Attention over a paged key/value cache in FP4 (include/fp4.h, kv_cache_attention): the
+// choice of kernel, and the kernel that joins the parts of long contexts.
+#include <type_traits>
+
 #include "fp4_device.h"
 #include "fp4_internal.h"
 #include "grid.h"
-#include "kv_cache.h"
+#include "kv_attention.h"
+#include "kv_attention_few.h"
 
 using namespace fp4dev;
 using fp4impl::AttendProblem;
 using fp4impl::KvCache;
+using fp4impl::TileParts;
+using fp4impl::UnitPlan;
 
 namespace {
 
-__device__ __forceinline__ float block_value(bool mx, uint32_t byte, float s_global) {
-  return mx ? e8m0_value(byte) : s_global * e4m3_value(byte);
-}
-
-__device__ __forceinline__ float wave_max(float v) {
+// One workgroup per tile and head: rows of tiles cut into parts, 16 threads a row.
+__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, int dp, bool out_vec) {
+  const int slot = workgroup() / c.heads, head = workgroup() % c.heads;
+  const TileParts* tiles = static_cast<const TileParts*>(p.tiles);
+  const int slots = tiles[p.max_slots].begin;
+  if (slot >= slots || slots > p.max_slots) return;
+  const TileParts t = tiles[slot];
+  if (t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts) return;
+  const int c16 = threadIdx.x & 15;
+  for (int q = threadIdx.x >> 4; q < t.rows; q += 16) {
+    const int rho = t.first_row + q, i = rho / p.group;
+    const int64_t at = (int64_t)(t.begin + i) * a.q_heads + head * p.group + (rho - i * p.group);
+    float top = -INFINITY, total = 0;
+    for (int k = 0; k < t.count; ++k) top = fmaxf(top, part_of(p, c.heads, head, t.part0 + k, dp)[2 * q]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    f32x4 sum[4] = {};
+    for (int k = 0; k < t.count; ++k) {
+      const float* left = part_of(p, c.heads, head, t.part0 + k, dp);
+      const float w = __builtin_amdgcn_exp2f(left[2 * q] - base);
+      total += left[2 * q + 1] * w;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
+      for (int j = 0; j < 4; ++j)
+        if (4 * (c16 + 16 * j) < c.dim) sum[j] += *reinterpret_cast<const f32x4*>(left + 2 * p.rows + q * dp + 4 * (c16 + 16 * j)) * w;
+    }
+    const float inverse = total > 0 ? 1.0f / total : 0.0f;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+    for (int j = 0; j < 4; ++j)
+      if (4 * (c16 + 16 * j) < c.dim) store4(a.out, a.out_bf16, out_vec, at * c.dim + 4 * (c16 + 16 * j), sum[j] * inverse);
+    if (c16 == 0 && a.lse != nullptr) a.lse[at] = row_lse(top, total);
+  }
 }
 
-__global__ void __launch_bounds__(64) k_attend(KvCache c, AttendProblem a) {
-  __shared__ float q[256];
-  const int lane = threadIdx.x;
-  const int r = workgroup() / a.q_heads, h = workgroup() % a.q_heads;
-  if (r >= c.rows) return;
-  const int b = seq_of_row(c, r);
-  if (b < 0) return;
-  const int begin = seq_begin(c, b), end = seq_end(c, b, begin), length = seq_length(c, b);
-  if (r >= end) return;
-  const int pos = length - (end - r);
-  const int hi = a.causal ? min(length, pos + 1) : length, lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int head = h / (a.q_heads / c.heads), bs = c.mx ? 32 : 16;
-  const float gk = c.mx ? 1.0f : nv_global_scale(*c.k_amax), gv = c.mx ? 1.0f : nv_global_scale(*c.v_amax);
-  for (int d = lane; d < c.dim; d += 64) {
-    const int64_t i = r * a.q_stride + (int64_t)h * c.dim + d;
-    q[d] = a.q_bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.q)[i] << 16)
-                    : static_cast<const float*>(a.q)[i];
-  }
-  __syncthreads();
-  float acc[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0;
-  for (int t0 = lo; t0 < hi; t0 += 64) {
-    const int t = t0 + lane, page = t < hi ? page_of(c, b, t) : -1;
-    float s = -INFINITY;
-    if (page >= 0) {
-      const int64_t row = cache_row(c, page, head, t);
-      float sum = 0;
-      for (int w = 0; w < c.dim / 8; ++w) {
-        const uint32_t codes = reinterpret_cast<const uint32_t*>(c.k_codes)[row * (c.dim / 8) + w];
-        const float sb = block_value(c.mx, c.k_scales[row * (c.dim / bs) + w * 8 / bs], gk);
-        float part = 0;
-        for (int j = 0; j < 8; ++j) part += q[8 * w + j] * e2m1_value((codes >> (4 * j)) & 15u);
-        sum += part * sb;
-      }
-      s = a.scale * sum;
-    }
-    const float now = fmaxf(m, wave_max(s));
-    const float base = now == -INFINITY ? 0.0f : now;
-    const float p = __expf(s - base), drop = __expf(m - base);
-    l = l * drop + wave_sum(p);
-    m = now;
-    for (int j = 0; j < 4; ++j) acc[j] *= drop;
-    for (int i = 0; i < 64 && t0 + i < hi; ++i) {
-      const float pi = __shfl(p, i, 64);
-      const int pg = __shfl(page, i, 64);
-      if (pg < 0) continue;
-      const int64_t row = cache_row(c, pg, head, t0 + i);
-      for (int j = 0; j < 4; ++j) {
-        const int d = lane + 64 * j;
-        if (d < c.dim)
-          acc[j] += pi * block_value(c.mx, c.v_scales[row * (c.dim / bs) + d / bs], gv) *
-                    e2m1_value((c.v_codes[row * (c.dim / 2) + d / 2] >> (4 * (d & 1))) & 15u);
-      }
-    }
-  }
-  for (int j = 0; j < 4; ++j) {
-    const int d = lane + 64 * j;
-    if (d >= c.dim) continue;
-    const int64_t i = ((int64_t)r * a.q_heads + h) * c.dim + d;
-    const float o = l > 0 ? acc[j] / l : 0.0f;
-    if (a.out_bf16) static_cast<uint16_t*>(a.out)[i] = (uint16_t)f32_to_bf16(o);
-    else static_cast<float*>(a.out)[i] = o;
-  }
-  if (a.lse != nullptr && lane == 0) a.lse[(int64_t)r * a.q_heads + h] = l > 0 ? m + logf(l) : -INFINITY;
+int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// Packed rows of a tile.
+int tile_rows(int64_t T, int64_t seqs, int group) { return T * group <= 16 * seqs ? 16 : 32; }
+
+UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads) {
+  UnitPlan p{};
+  p.group = q_heads / heads;
+  p.rows = tile_rows(T, seqs, p.group);
+  p.min_per = 4;
+  p.target = (4 * fp4impl::num_cus() + heads - 1) / heads;
+  p.max_slots = (int)(T * p.group / p.rows + seqs);
+  p.max_parts = 2 * p.target + p.target / 8 + 8;
+  return p;
+}
+
+size_t tiles_bytes(const UnitPlan& p) { return (size_t)(p.max_slots + 1) * sizeof(TileParts); }
+
+template <int DP, bool MX, bool QBF, bool SPLIT>
+void launch(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool q_vec, bool out_vec, hipStream_t stream) {
+  const dim3 grid = fp4impl::grid_of(((int64_t)p.max_slots + p.target + fp4impl::kSpareUnits) * c.heads);
+  if (p.rows == 16) k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
+  else k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
+}
+
+template <int DP>
+void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool q_vec, bool out_vec, hipStream_t stream) {
+  const bool split = !a.q_bf16 || !a.out_bf16;
+  auto go = [&](auto mx) {
+    if (!a.q_bf16) launch<DP, mx.value, false, true>(c, a, p, q_vec, out_vec, stream);
+    else if (split) launch<DP, mx.value, true, true>(c, a, p, q_vec, out_vec, stream);
+    else launch<DP, mx.value, true, false>(c, a, p, q_vec, out_vec, stream);
+  };
+  if (c.mx) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 }  // namespace
 
 namespace fp4impl {
 
-size_t kv_attention_workspace_bytes(int64_t, int64_t, int, int, int) { return 16; }
+size_t kv_attention_workspace_bytes(int64_t T, int64_t seqs, int q_heads, int heads, int dim) {
+  const UnitPlan p = plan_of(T, seqs, q_heads, heads);
+  return tiles_bytes(p) + (size_t)p.max_parts * heads * p.rows * (padded_dim(dim) + 2) * 4;
+}
 
-hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& p, hipStream_t stream) {
-  k_attend<<<grid_of((int64_t)c.rows * p.q_heads), 64, 0, stream>>>(c, p);
+hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStream_t stream) {
+  UnitPlan p = plan_of(c.rows, c.seqs, a.q_heads, c.heads);
+  p.causal = a.causal;
+  p.window = a.window;
+  p.tiles = a.workspace;
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + tiles_bytes(p));
+  auto multiple = [](const void* x, int64_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };
+  const bool q_vec = multiple(a.q, 16) && a.q_stride * (a.q_bf16 ? 2 : 4) % 16 == 0;
+  const bool out_vec = multiple(a.out, a.out_bf16 ? 8 : 16);
+  const int dp = padded_dim(c.dim);
+  if (dp == 64) launch_dp<64>(c, a, p, q_vec, out_vec, stream);
+  else if (dp == 128) launch_dp<128>(c, a, p, q_vec, out_vec, stream);
+  else launch_dp<256>(c, a, p, q_vec, out_vec, stream);
+  k_join_parts<<<grid_of((int64_t)p.max_slots * c.heads), 256, 0, stream>>>(c, a, p, dp, out_vec);
   return hipGetLastError();
 }
 
