@@ -7,6 +7,7 @@
 #include "grid.h"
 #include "kv_attention.h"
 #include "kv_attention_few.h"
+#include "kv_attention_tiles.h"
 
 using namespace fp4dev;
 using fp4impl::AttendProblem;
@@ -16,49 +17,82 @@ using fp4impl::UnitPlan;
 
 namespace {
 
-// One workgroup per tile and head: rows of tiles cut into parts, 16 threads a row.
-__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, int dp, bool out_vec) {
-  const int slot = workgroup() / c.heads, head = workgroup() % c.heads;
+// Joins the parts of four rows of a tile that was cut.  Wave w finds the weights of row w's parts;
+// then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
+// sums meet in LDS.
+template <int DP>
+__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, bool out_vec) {
+  constexpr int kChunk = 256, kPer = DP / 64;
+  typedef float fv __attribute__((ext_vector_type(kPer)));
+  __shared__ float weight[4][kChunk], total[4];
+  __shared__ __align__(16) float sums[4][4][DP];
   const TileParts* tiles = static_cast<const TileParts*>(p.tiles);
+  const int groups = p.rows / 4, at = workgroup() / groups, q0 = 4 * (workgroup() % groups);
+  const int slot = at / c.heads, head = at % c.heads;
   const int slots = tiles[p.max_slots].begin;
   if (slot >= slots || slots > p.max_slots) return;
   const TileParts t = tiles[slot];
-  if (t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts) return;
-  const int c16 = threadIdx.x & 15;
-  for (int q = threadIdx.x >> 4; q < t.rows; q += 16) {
-    const int rho = t.first_row + q, i = rho / p.group;
-    const int64_t at = (int64_t)(t.begin + i) * a.q_heads + head * p.group + (rho - i * p.group);
-    float top = -INFINITY, total = 0;
-    for (int k = 0; k < t.count; ++k) top = fmaxf(top, part_of(p, c.heads, head, t.part0 + k, dp)[2 * q]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    f32x4 sum[4] = {};
-    for (int k = 0; k < t.count; ++k) {
-      const float* left = part_of(p, c.heads, head, t.part0 + k, dp);
-      const float w = __builtin_amdgcn_exp2f(left[2 * q] - base);
-      total += left[2 * q + 1] * w;
+  if (t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts || q0 >= t.rows) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float* const first = part_of(p, c.heads, head, t.part0, DP);
+  const int64_t stride = part_of(p, c.heads, head, t.part0 + 1, DP) - first;
+  float top = -INFINITY;
+  for (int k = lane; k < t.count; k += 64) top = fmaxf(top, first[k * stride + 2 * (q0 + wave)]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * (c16 + 16 * j) < c.dim) sum[j] += *reinterpret_cast<const f32x4*>(left + 2 * p.rows + q * dp + 4 * (c16 + 16 * j)) * w;
+  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float l = 0;
+  fv sum[4] = {};
+  for (int k0 = 0; k0 < t.count; k0 += kChunk) {
+    const int n = min(kChunk, t.count - k0);
+    __syncthreads();
+    for (int k = lane; k < n; k += 64) {
+      const float* left = first + (k0 + k) * stride + 2 * (q0 + wave);
+      const float w = __builtin_amdgcn_exp2f(left[0] - base);
+      weight[wave][k] = w;
+      l += left[1] * w;
     }
-    const float inverse = total > 0 ? 1.0f / total : 0.0f;
+    __syncthreads();
+    const float* const from = first + k0 * stride + 2 * p.rows + q0 * DP + lane * kPer;
+#pragma unroll 4
+    for (int k = wave; k < n; k += 4) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (4 * (c16 + 16 * j) < c.dim) store4(a.out, a.out_bf16, out_vec, at * c.dim + 4 * (c16 + 16 * j), sum[j] * inverse);
-    if (c16 == 0 && a.lse != nullptr) a.lse[at] = row_lse(top, total);
+      for (int r = 0; r < 4; ++r) sum[r] += *reinterpret_cast<const fv*>(from + k * stride + r * DP) * weight[r][k];
+    }
   }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+  if (lane == 0) total[wave] = l;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) *reinterpret_cast<fv*>(&sums[wave][r][lane * kPer]) = sum[r];
+  __syncthreads();
+  const int q = q0 + wave, rho = t.first_row + q, i = rho / p.group;
+  if (q >= t.rows) return;
+  const int64_t row = (int64_t)(t.begin + i) * a.q_heads + head * p.group + (rho - i * p.group);
+  const float inverse = total[wave] > 0 ? 1.0f / total[wave] : 0.0f;
+  if (4 * lane < c.dim) {
+    f32x4 v{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][wave][4 * lane]);
+    store4(a.out, a.out_bf16, out_vec, row * c.dim + 4 * lane, v * inverse);
+  }
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = row_lse(top, total[wave]);
 }
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Packed rows of a tile.
-int tile_rows(int64_t T, int64_t seqs, int group) { return T * group <= 16 * seqs ? 16 : 32; }
+int tile_rows(int64_t T, int64_t seqs, int group) {
+  const int64_t rows = T * group;
+  return rows <= 16 * seqs ? 16 : rows <= 32 * seqs ? 32 : 128;
+}
 
 UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads) {
   UnitPlan p{};
   p.group = q_heads / heads;
   p.rows = tile_rows(T, seqs, p.group);
-  p.min_per = 4;
-  p.target = (4 * fp4impl::num_cus() + heads - 1) / heads;
+  p.min_per = p.rows == 128 ? 8 : 4;
+  p.target = ((p.rows == 128 ? 2 : 4) * fp4impl::num_cus() + heads - 1) / heads;
   p.max_slots = (int)(T * p.group / p.rows + seqs);
   p.max_parts = 2 * p.target + p.target / 8 + 8;
   return p;
@@ -70,7 +104,8 @@ template <int DP, bool MX, bool QBF, bool SPLIT>
 void launch(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool q_vec, bool out_vec, hipStream_t stream) {
   const dim3 grid = fp4impl::grid_of(((int64_t)p.max_slots + p.target + fp4impl::kSpareUnits) * c.heads);
   if (p.rows == 16) k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
-  else k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
+  else if (p.rows == 32) k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
+  else k_attend_tiles<DP, MX, QBF, SPLIT><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
 }
 
 template <int DP>
@@ -83,6 +118,7 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool
   };
   if (c.mx) go(std::true_type{});
   else go(std::false_type{});
+  k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * (p.rows / 4)), 256, 0, stream>>>(c, a, p, out_vec);
 }
 
 }  // namespace
@@ -107,7 +143,6 @@ hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStre
   if (dp == 64) launch_dp<64>(c, a, p, q_vec, out_vec, stream);
   else if (dp == 128) launch_dp<128>(c, a, p, q_vec, out_vec, stream);
   else launch_dp<256>(c, a, p, q_vec, out_vec, stream);
-  k_join_parts<<<grid_of((int64_t)p.max_slots * c.heads), 256, 0, stream>>>(c, a, p, dp, out_vec);
   return hipGetLastError();
 }
 
