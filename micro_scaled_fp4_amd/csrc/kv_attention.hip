@@ -27,56 +27,60 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
   __shared__ float weight[4][kChunk], total[4];
   __shared__ __align__(16) float sums[4][4][DP];
   const TileParts* tiles = static_cast<const TileParts*>(p.tiles);
-  const int groups = p.rows / 4, at = workgroup() / groups, q0 = 4 * (workgroup() % groups);
+  const int at = workgroup() >> 2;              // four workgroups a tile
   const int slot = at / c.heads, head = at % c.heads;
   const int slots = tiles[p.max_slots].begin;
   if (slot >= slots || slots > p.max_slots) return;
   const TileParts t = tiles[slot];
-  if (t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts || q0 >= t.rows) return;
+  if (t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float* const first = part_of(p, c.heads, head, t.part0, DP);
   const int64_t stride = part_of(p, c.heads, head, t.part0 + 1, DP) - first;
-  float top = -INFINITY;
-  for (int k = lane; k < t.count; k += 64) top = fmaxf(top, first[k * stride + 2 * (q0 + wave)]);
+  for (int q0 = 4 * (workgroup() & 3); q0 < t.rows; q0 += 16) {
+    float top = -INFINITY;
+    for (int k = lane; k < t.count; k += 64) top = fmaxf(top, first[k * stride + 2 * (q0 + wave)]);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  const float base = top == -INFINITY ? 0.0f : top;
-  float l = 0;
-  fv sum[4] = {};
-  for (int k0 = 0; k0 < t.count; k0 += kChunk) {
-    const int n = min(kChunk, t.count - k0);
-    __syncthreads();
-    for (int k = lane; k < n; k += 64) {
-      const float* left = first + (k0 + k) * stride + 2 * (q0 + wave);
-      const float w = __builtin_amdgcn_exp2f(left[0] - base);
-      weight[wave][k] = w;
-      l += left[1] * w;
-    }
-    __syncthreads();
-    const float* const from = first + k0 * stride + 2 * p.rows + q0 * DP + lane * kPer;
+    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float l = 0;
+    fv sum[4] = {};
+    for (int k0 = 0; k0 < t.count; k0 += kChunk) {
+      const int n = min(kChunk, t.count - k0);
+      __syncthreads();
+      for (int k = lane; k < n; k += 64) {
+        const float* left = first + (k0 + k) * stride + 2 * (q0 + wave);
+        const float w = __builtin_amdgcn_exp2f(left[0] - base);
+        weight[wave][k] = w;
+        l += left[1] * w;
+      }
+      __syncthreads();
+      const float* const from = first + k0 * stride + 2 * p.rows + q0 * DP + lane * kPer;
 #pragma unroll 4
-    for (int k = wave; k < n; k += 4) {
+      for (int k = wave; k < n; k += 4) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sum[r] += *reinterpret_cast<const fv*>(from + k * stride + r * DP) * weight[r][k];
+        for (int r = 0; r < 4; ++r) sum[r] += *reinterpret_cast<const fv*>(from + k * stride + r * DP) * weight[r][k];
+      }
     }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+    if (lane == 0) total[wave] = l;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *reinterpret_cast<fv*>(&sums[wave][r][lane * kPer]) = sum[r];
+    __syncthreads();
+    const int q = q0 + wave, rho = t.first_row + q, i = rho / p.group;
+    if (q < t.rows) {
+      const int64_t row = (int64_t)(t.begin + i) * a.q_heads + head * p.group + (rho - i * p.group);
+      const float inverse = total[wave] > 0 ? 1.0f / total[wave] : 0.0f;
+      if (4 * lane < c.dim) {
+        f32x4 v{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][wave][4 * lane]);
+        store4(a.out, a.out_bf16, out_vec, row * c.dim + 4 * lane, v * inverse);
+      }
+      if (lane == 0 && a.lse != nullptr) a.lse[row] = row_lse(top, total[wave]);
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
-  if (lane == 0) total[wave] = l;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) *reinterpret_cast<fv*>(&sums[wave][r][lane * kPer]) = sum[r];
-  __syncthreads();
-  const int q = q0 + wave, rho = t.first_row + q, i = rho / p.group;
-  if (q >= t.rows) return;
-  const int64_t row = (int64_t)(t.begin + i) * a.q_heads + head * p.group + (rho - i * p.group);
-  const float inverse = total[wave] > 0 ? 1.0f / total[wave] : 0.0f;
-  if (4 * lane < c.dim) {
-    f32x4 v{0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][wave][4 * lane]);
-    store4(a.out, a.out_bf16, out_vec, row * c.dim + 4 * lane, v * inverse);
-  }
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = row_lse(top, total[wave]);
 }
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -92,7 +96,7 @@ UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads) {
   p.group = q_heads / heads;
   p.rows = tile_rows(T, seqs, p.group);
   p.min_per = p.rows == 128 ? 8 : 4;
-  p.target = ((p.rows == 128 ? 2 : 4) * fp4impl::num_cus() + heads - 1) / heads;
+  p.target = (4 * fp4impl::num_cus() + heads - 1) / heads;
   p.max_slots = (int)(T * p.group / p.rows + seqs);
   p.max_parts = 2 * p.target + p.target / 8 + 8;
   return p;
@@ -118,7 +122,7 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool
   };
   if (c.mx) go(std::true_type{});
   else go(std::false_type{});
-  k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * (p.rows / 4)), 256, 0, stream>>>(c, a, p, out_vec);
+  k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * 4), 256, 0, stream>>>(c, a, p, out_vec);
 }
 
 }  // namespace

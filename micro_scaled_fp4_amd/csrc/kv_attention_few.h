@@ -109,17 +109,19 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
 
   const QuarterRow<DP, MX> k_at(r16, quad, c.dim), v_at(lane >> 2, lane & 3, c.dim);
   RawStep<DP> next;
+  int t0 = sp.t0 + 64 * wave;
+  PageWalk walk(c, u.b, t0);
   auto load = [&](int t0) {
+    walk.reach(t0);
     next.holes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + 16 * i;
       int n = min(max(sp.t1 - t, 0), 16);
-      int page = n > 0 ? page_of(c, u.b, t) : 0;
+      int page = walk.at(t);
       if (page < 0) {
-        next.holes |= 1 << i;
-        n = 0;
-        page = 0;
+        next.holes |= 1 << i;    // (past the last position: masked anyway)
+        n = page = 0;
       }
       const int64_t row = cache_row(c, page, head, t);
       const int codes = c.dim / 2, scales = c.dim / (MX ? 32 : 16);
@@ -129,7 +131,6 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
                            v_at, next.v[i], next.vs[i]);
     }
   };
-  int t0 = sp.t0 + 64 * wave;
   if (t0 < sp.t1) load(t0);
 
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);

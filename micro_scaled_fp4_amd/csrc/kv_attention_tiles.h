@@ -42,16 +42,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   const QuarterRow<DP, MX> at(lane >> 2, lane & 3, c.dim);
   uint32_t kw[kDwords], vw[kDwords], ks[kScales], vs[kScales], ks2[kScales], vs2[kScales];
   int holes = 0, holes_next = 0;                // of 16 positions each
-  auto page_at = [&](int t, int& n) {
-    n = min(max(sp.t1 - t, 0), 16);
-    int page = n > 0 ? page_of(c, u.b, t) : 0;
-    if (page < 0) n = page = 0;
-    return page;
-  };
+  PageWalk walk(c, u.b, sp.t0), walk2 = walk;   // along the codes, and one step ahead along the scales
   auto load = [&](int t0, bool codes) {
     const int t = t0 + 16 * wave;
-    int n;
-    const int page = page_at(t, n);
+    int n = min(max(sp.t1 - t, 0), 16);
+    (codes ? walk : walk2).reach(t0);
+    int page = (codes ? walk : walk2).at(t);
+    if (page < 0) n = page = 0;
     const int64_t row = cache_row(c, page, head, t);
     const int cb = c.dim / 2, sb = c.dim / (MX ? 32 : 16);
     if (codes) {
@@ -81,11 +78,11 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
       }
     }
   };
+  // of the step whose codes were loaded last (past the last position: masked anyway)
   auto holes_at = [&](int t0) {
     int h = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (t0 + 16 * i < sp.t1 && page_of(c, u.b, t0 + 16 * i) < 0) h |= 1 << i;
+    for (int i = 0; i < 4; ++i) h |= walk.at(t0 + 16 * i) < 0 ? 1 << i : 0;
     return h;
   };
   // MX: this wave's largest scale bytes of the step whose scales are in ks2, vs2
@@ -174,6 +171,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   dequantize(0);
   holes = holes_at(sp.t0);
   load(sp.t0 + 64, true);
+  holes_next = holes_at(sp.t0 + 64);
   note_tops(1);
   __syncthreads();
 
@@ -190,10 +188,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     const int k_ref = k_ref_next, v_top = v_ref_next;
     const bool more = t0 + 64 < sp.t1;
     scales_arrive();
-    if (more) {
-      load(t0 + 128, false);
-      holes_next = holes_at(t0 + 64);
-    }
+    if (more) load(t0 + 128, false);
     // a wave whose rows all end before this step only takes part in what the workgroup shares
     if (__any(t0 <= row.last && t0 + 63 >= row.first)) {
       const uint8_t* const kt = buffer[now].k;
@@ -269,6 +264,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
       dequantize(now ^ 1);
       load(t0 + 128, true);
       holes = holes_next;
+      holes_next = holes_at(t0 + 128);
     }
     // the step after the next one's references, for the end of the next step
     note_tops(now);

@@ -59,6 +59,19 @@ __device__ __forceinline__ int scan_lanes(int v) {
   return v;
 }
 
+// The sum over all lanes, the same in all.
+__device__ __forceinline__ float sum_lanes(float v) {
+  auto moved = [&](int x) { return __uint_as_float((uint32_t)x); };
+  auto bits = [&]() { return (int)__float_as_uint(v); };
+  v += moved(__builtin_amdgcn_update_dpp(0, bits(), 0x111, 0xf, 0xf, false));
+  v += moved(__builtin_amdgcn_update_dpp(0, bits(), 0x112, 0xf, 0xf, false));
+  v += moved(__builtin_amdgcn_update_dpp(0, bits(), 0x114, 0xf, 0xf, false));
+  v += moved(__builtin_amdgcn_update_dpp(0, bits(), 0x118, 0xf, 0xf, false));
+  v += moved(__builtin_amdgcn_update_dpp(0, bits(), 0x142, 0xa, 0xf, false));
+  v += moved(__builtin_amdgcn_update_dpp(0, bits(), 0x143, 0xc, 0xf, false));
+  return moved(__builtin_amdgcn_readlane(bits(), 63));
+}
+
 struct Unit {
   int b, begin, n, length;       // the sequence: its first row, rows, positions
   int tile, slot;                // its row tile, and that among all sequences' tiles
@@ -96,11 +109,8 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
     work += (float)s.tiles * (float)s.steps;
     all += (float)s.tiles;
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    work += __shfl_xor(work, off, 64);
-    all += __shfl_xor(all, off, 64);
-  }
+  work = sum_lanes(work);
+  all = sum_lanes(all);
   const float share = ceilf(work / (float)p.target);
   Unit r{};
   r.per = __builtin_amdgcn_readfirstlane(max(p.min_per, (int)fminf(share, 1.0e9f)));
@@ -137,6 +147,7 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
       r.slot = slot + r.tile;
       r.part = left - k * count;
       r.count = count;
+      r.per = __builtin_amdgcn_readfirstlane((s.steps + count - 1) / count);   // parts of equal length
       r.part0 = part0 + r.tile * count;
       return r;
     }
@@ -147,6 +158,39 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
   r.any = false;
   return r;
 }
+
+// The page table of a sequence as a wave walks along it: lane i holds entry base + i (-1: a hole
+// or past the table), and the next 64 entries are on their way, so that no page number is waited
+// for.
+struct PageWalk {
+  const int32_t* table;
+  int max_pages, num_pages, shift, base, now, next;
+
+  __device__ __forceinline__ int entries(int from) const {
+    const int i = from + (int)(threadIdx.x & 63);
+    const int p = i < max_pages ? table[i] : -1;
+    return p >= 0 && p < num_pages ? p : -1;
+  }
+  // from position t on
+  __device__ __forceinline__ PageWalk(const KvCache& c, int b, int t)
+      : table(c.pages + b * c.max_pages), max_pages((int)c.max_pages), num_pages((int)c.num_pages),
+        shift(c.page_shift), base(t >> c.page_shift) {
+    now = entries(base);
+    next = entries(base + 64);
+  }
+  // Makes at() valid for the 64 positions from t on (t is the same in all lanes and does not decrease).
+  __device__ __forceinline__ void reach(int t) {
+    while ((t >> shift) - base >= 64) {
+      base += 64;
+      now = next;
+      next = entries(base + 64);
+    }
+  }
+  __device__ __forceinline__ int at(int t) const {
+    const int i = (t >> shift) - base;
+    return i < 64 ? __builtin_amdgcn_readlane(now, i) : __builtin_amdgcn_readlane(next, i - 64);
+  }
+};
 
 // Positions of a unit: [t0, t1), t0 a multiple of 64 (positions before `lo` are masked).
 struct Span {
