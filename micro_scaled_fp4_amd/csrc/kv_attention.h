@@ -6,7 +6,9 @@
 // the weights leave the first product's accumulators in the order of positions in which the
 // second takes them, if V's rows are picked in that order too.  Softmax in base 2 with a running
 // maximum m and sum l:
-//   x = c s,  c = |scale| log2(e) (factors of q's and k's scaling),  P = 2^(x - m + 15).
+//   x = c s,  c = |scale| log2(e) (factors of q's and k's scaling),  P = 2^(x - m + 11),
+// where m follows the maximum only when it has grown by more than 4, so that sums are seldom
+// rescaled; P is at most 2^15 then.
 //
 // Why fp16.  A value of the cache is E2M1 x its block scale.  NVFP4: E2M1 x E4M3 has at most 6
 // significant bits and lies in [2^-10, 2688], exact in fp16; the tensor scale joins c and the
@@ -15,7 +17,7 @@
 // of q is scaled by a power of two to a maximum in [2^14, 2^15): bf16 values are exact then
 // (down to 2^-29 of the maximum), float32 ones are taken as two fp16 parts (22 bits).  P is
 // rounded to fp16, half a step being 2^-12 of a weight, against 2^-8 of the bf16 output; its
-// factor 2^15 keeps weights down to 2^-29 of the largest at full precision, which many small
+// factor 2^11 keeps weights down to 2^-25 of the largest at full precision, which many small
 // weights next to one large need.  With float32 operands P is two fp16 parts as well.
 #pragma once
 
@@ -35,7 +37,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kWeightBits = 15.0f;            // P is 2^15 at the maximum
+constexpr float kWeightBits = 11.0f;            // P is 2^11 at m
+constexpr float kGrowth = 4.0f;                 // a maximum within m + kGrowth leaves m as it is
 
 // The larger of v in lanes l and l ^ 32, or l and l ^ 16.
 __device__ __forceinline__ float max_over_halves(float v) {
@@ -182,6 +185,9 @@ __device__ __forceinline__ void store4(void* out, bool bf16, bool vec, int64_t i
 __device__ __forceinline__ float* part_of(const UnitPlan& p, int heads, int head, int part, int dp) {
   return p.parts + ((int64_t)part * heads + head) * p.rows * (dp + 2);
 }
+
+// The reference of a row's weights after a step whose largest exponent is `top`.
+__device__ __forceinline__ float next_max(float m, float top) { return top > m + kGrowth ? top : m; }
 
 // lse of a row with running maximum m and sum l.
 __device__ __forceinline__ float row_lse(float m, float l) {

@@ -1,5 +1,6 @@
 // Attention over a paged key/value cache in FP4 (include/fp4.h, kv_cache_attention): the
 // choice of kernel, and the kernel that joins the parts of long contexts.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp4_device.h"
@@ -91,12 +92,22 @@ int tile_rows(int64_t T, int64_t seqs, int group) {
   return rows <= 16 * seqs ? 16 : rows <= 32 * seqs ? 32 : 128;
 }
 
-UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads) {
+// Workgroups of k_attend_few that a compute unit holds, by their registers (a wave of each on each
+// SIMD).  Tiles of 128 rows take more parts than are resident: their rows' spans differ.
+int resident(int rows, int dp, bool split) {
+  if (rows == 128) return 4;
+  if (rows == 16) return dp == 64 ? (split ? 3 : 4) : dp == 128 ? (split ? 2 : 3) : 1;
+  return dp == 64 ? (split ? 2 : 3) : 1;
+}
+
+// resident: workgroups on a compute unit.
+UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int resident) {
   UnitPlan p{};
   p.group = q_heads / heads;
   p.rows = tile_rows(T, seqs, p.group);
   p.min_per = p.rows == 128 ? 8 : 4;
-  p.target = (4 * fp4impl::num_cus() + heads - 1) / heads;
+  p.fit = p.rows < 128;
+  p.target = std::max(1, resident * fp4impl::num_cus() / heads);
   p.max_slots = (int)(T * p.group / p.rows + seqs);
   p.max_parts = 2 * p.target + p.target / 8 + 8;
   return p;
@@ -130,12 +141,14 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool
 namespace fp4impl {
 
 size_t kv_attention_workspace_bytes(int64_t T, int64_t seqs, int q_heads, int heads, int dim) {
-  const UnitPlan p = plan_of(T, seqs, q_heads, heads);
+  const UnitPlan p = plan_of(T, seqs, q_heads, heads, kMostResident);
   return tiles_bytes(p) + (size_t)p.max_parts * heads * p.rows * (padded_dim(dim) + 2) * 4;
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStream_t stream) {
-  UnitPlan p = plan_of(c.rows, c.seqs, a.q_heads, c.heads);
+  const int dp = padded_dim(c.dim);
+  const bool split = !a.q_bf16 || !a.out_bf16;
+  UnitPlan p = plan_of(c.rows, c.seqs, a.q_heads, c.heads, resident(tile_rows(c.rows, c.seqs, a.q_heads / c.heads), dp, split));
   p.causal = a.causal;
   p.window = a.window;
   p.tiles = a.workspace;
@@ -143,7 +156,6 @@ hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStre
   auto multiple = [](const void* x, int64_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };
   const bool q_vec = multiple(a.q, 16) && a.q_stride * (a.q_bf16 ? 2 : 4) % 16 == 0;
   const bool out_vec = multiple(a.out, a.out_bf16 ? 8 : 16);
-  const int dp = padded_dim(c.dim);
   if (dp == 64) launch_dp<64>(c, a, p, q_vec, out_vec, stream);
   else if (dp == 128) launch_dp<128>(c, a, p, q_vec, out_vec, stream);
   else launch_dp<256>(c, a, p, q_vec, out_vec, stream);

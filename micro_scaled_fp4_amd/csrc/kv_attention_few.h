@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
         for (int e = 0; e < 4; ++e) top = fmaxf(top, s[g][i][e]);
       top = max_over_halves(max_over_rows(top));
       const float was = m[g];
-      m[g] = fmaxf(was, top * cf);
+      m[g] = next_max(was, top * cf);
       const float base = m[g] == -INFINITY ? 0.0f : m[g];
       const float drop = __builtin_amdgcn_exp2f(was - base);
       float sum = 0;
@@ -240,12 +240,13 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
           ph[g][i >> 1][4 * (i & 1) + e] = h;
           if constexpr (SPLIT) pl[g][i >> 1][4 * (i & 1) + e] = (_Float16)(w - (float)h);
         }
-      l[g] = l[g] * drop + sum;
       const float keep = MX ? __builtin_amdgcn_ldexpf(drop, v_ref - v_top) : drop;
       if (__any(keep != 1.0f)) {
+        l[g] *= drop;
 #pragma unroll
         for (int d = 0; d < kGranules; ++d) acc[g][d] *= keep;
       }
+      l[g] += sum;
     }
     v_ref = v_top;
     // outputs: O^T[channel][row r16] += V^T P^T, 32 positions at a time

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
       top = max_over_halves(top);
       const float was = m;
-      m = fmaxf(was, top * cf);
+      m = next_max(was, top * cf);
       const float base = m == -INFINITY ? 0.0f : m;
       const float drop = __builtin_amdgcn_exp2f(was - base);
       f16x8 ph[4], pl[SPLIT ? 4 : 1];
@@ -239,12 +239,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
           ph[2 * b + (e >> 3)][e & 7] = h;
           if constexpr (SPLIT) pl[2 * b + (e >> 3)][e & 7] = (_Float16)(w - (float)h);
         }
-      l = l * drop + sum;
       const float keep = MX ? __builtin_amdgcn_ldexpf(drop, v_ref - v_top) : drop;
       if (__any(keep != 1.0f)) {
+        l *= drop;
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d) acc[d] *= keep;
       }
+      l += sum;
       v_ref = v_top;
       // O^T += V^T P^T: 16 positions at a time, in the order 4 half + 0 .. 3, 8 + 4 half + 0 .. 3
 #pragma unroll

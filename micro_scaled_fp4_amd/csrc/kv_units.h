@@ -23,6 +23,7 @@ struct UnitPlan {
   int group;
   int min_per;                   // least steps of a part
   int target;                    // parts per key/value head that fill the card
+  bool fit;                      // no more than those, for kernels whose workgroups are all resident
   int max_slots, max_parts;      // most tiles, and most parts of cut tiles (per head)
   bool causal;
   int window;
@@ -39,6 +40,8 @@ struct TileParts {
 // Units past the tiles and parts that the layout can give (the total of the steps is a sum of
 // float32 values).
 constexpr int kSpareUnits = 8;
+// The most workgroups on a compute unit that any of the kernels reaches.
+constexpr int kMostResident = 4;
 
 }  // namespace fp4impl
 
@@ -99,7 +102,7 @@ __device__ __forceinline__ SeqSize seq_size(const KvCache& c, const UnitPlan& p,
 }
 
 // Unit u of this head, for one wave (all 64 lanes call; the result is the same in all).  Each
-// lane takes a run of sequences; two scans over the lanes give the totals and u's lane.
+// lane takes a run of sequences; sums and scans over the lanes give the totals and u's lane.
 __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int u) {
   const int lane = threadIdx.x & 63, run = (c.seqs + 63) >> 6;
   const int b0 = min(lane * run, c.seqs), b1 = min(b0 + run, c.seqs);
@@ -111,12 +114,28 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
   }
   work = sum_lanes(work);
   all = sum_lanes(all);
-  const float share = ceilf(work / (float)p.target);
   Unit r{};
-  r.per = __builtin_amdgcn_readfirstlane(max(p.min_per, (int)fminf(share, 1.0e9f)));
   // offsets that decrease can give more tiles than there are rows: nothing is done then
   r.slots = 0x7fffffff;
-  if (__builtin_amdgcn_readfirstlane(!(all <= 1.01f * (float)p.max_slots))) return r;
+  if (!(all <= 1.01f * (float)p.max_slots)) return r;
+  const float share = ceilf(work / (float)p.target);
+  r.per = max(p.min_per, (int)fminf(share, 1.0e9f));
+  if (p.fit && 2.0f * all < (float)p.target) {
+    // the shortest parts that are no more than `target`: each tile's last part is shorter than the
+    // others, so share gives up to a part more for each tile, and work / (target - all) never does
+    int lo = r.per, hi = max(p.min_per, (int)ceilf(work / ((float)p.target - all)));
+    for (int i = 0; i < 4 && lo < hi; ++i) {
+      const int mid = (lo + hi) >> 1;
+      float units = 0;
+      for (int b = b0; b < b1; ++b) {
+        const SeqSize s = seq_size(c, p, b);
+        units += (float)(s.tiles * ((s.steps + mid - 1) / mid));
+      }
+      if (sum_lanes(units) <= (float)p.target) hi = mid;
+      else lo = mid + 1;
+    }
+    r.per = hi;
+  }
   int units = 0, parts = 0, tiles = 0;
   for (int b = b0; b < b1; ++b) {
     const SeqSize s = seq_size(c, p, b);

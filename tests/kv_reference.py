@@ -111,7 +111,9 @@ def attention(case, store, q, scale, causal=True, window=0, f32=False):
     included: 2 A 2^-24).  Sums over L weights, joined in parts: (L + 64) 2^-24.  Weights as fp16
     2^-11 (half a step 2^-12, and the same for l's), or, from float32 operands, in two fp16 parts:
     2^-21, and q in two fp16 parts: 2^-22 A per score.  All of them multiply sum p |v|.  Weights
-    below 2^-29 of the largest lose digits: 2^-40 of the largest |v| per position."""
+    are stored as P = 2^11 w 2^d at the least, w relative to the largest and d >= 0: where P is below
+    2^-14 fp16's steps are 2^-24 and half a step 2^-25 is 2^-36 of the largest weight, so 2^-36 of
+    the largest |v| per position."""
     T, Hq, D = q.shape
     G = Hq // case.H
     out, lse = np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan)
@@ -144,7 +146,7 @@ def attention(case, store, q, scale, causal=True, window=0, f32=False):
                     rel += 2.0 ** -21 + 4 * 2.0 ** -22 * A
                 else:
                     rel += 2.0 ** -11
-                tol[r, h] = rel * (w @ np.abs(vh)) + n * 2.0 ** -40 * np.abs(vh).max()
+                tol[r, h] = rel * (w @ np.abs(vh)) + n * 2.0 ** -36 * np.abs(vh).max()
                 ltol[r, h] = (2 * (D + 16) * 2.0 ** -24 + (2.0 ** -22 if f32 else 0)) * A + 2.0 ** -20 + \
                     (n + 64) * 2.0 ** -24 + 2.0 ** -22 * abs(lse[r, h])
     return out, lse, tol, ltol
