@@ -92,32 +92,37 @@ int tile_rows(int64_t T, int64_t seqs, int group) {
   return rows <= 16 * seqs ? 16 : rows <= 32 * seqs ? 32 : 128;
 }
 
-// Workgroups of k_attend_few that a compute unit holds, by their registers (a wave of each on each
-// SIMD).  Tiles of 128 rows take more parts than are resident: their rows' spans differ.
+// Workgroups that a compute unit holds, by their registers and LDS (a wave of each on each SIMD).
 int resident(int rows, int dp, bool split) {
-  if (rows == 128) return 4;
+  if (rows == 128) return dp == 256 ? 1 : 2;
   if (rows == 16) return dp == 64 ? (split ? 3 : 4) : dp == 128 ? (split ? 2 : 3) : 1;
   return dp == 64 ? (split ? 2 : 3) : 1;
 }
 
-// resident: workgroups on a compute unit.
-UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int resident) {
+UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool split) {
   UnitPlan p{};
   p.group = q_heads / heads;
   p.rows = tile_rows(T, seqs, p.group);
   p.min_per = p.rows == 128 ? 8 : 4;
-  p.fit = p.rows < 128;
-  p.target = std::max(1, resident * fp4impl::num_cus() / heads);
+  p.target = std::max(1, resident(p.rows, dp, split) * fp4impl::num_cus() / heads);
+  p.rounds = p.rows == 128 ? 4 : 2;
   p.max_slots = (int)(T * p.group / p.rows + seqs);
-  p.max_parts = 2 * p.target + p.target / 8 + 8;
+  p.max_parts = std::max(p.rounds, 2) * p.target + p.target / 8 + 8;
   return p;
 }
 
 size_t tiles_bytes(const UnitPlan& p) { return (size_t)(p.max_slots + 1) * sizeof(TileParts); }
 
+// The most parts of a tile that the page table has positions for, and units of a head.
+int64_t most_parts(const KvCache& c, const UnitPlan& p) { return std::max((c.capacity / 64 + p.min_per) / p.min_per, 1); }
+int64_t most_units(const KvCache& c, const UnitPlan& p) {
+  return std::min(p.max_slots * most_parts(c, p),
+                  std::max((int64_t)p.max_slots + p.target, (int64_t)p.rounds * p.target) + fp4impl::kSpareUnits);
+}
+
 template <int DP, bool MX, bool QBF, bool SPLIT>
 void launch(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool q_vec, bool out_vec, hipStream_t stream) {
-  const dim3 grid = fp4impl::grid_of(((int64_t)p.max_slots + p.target + fp4impl::kSpareUnits) * c.heads);
+  const dim3 grid = fp4impl::grid_of(most_units(c, p) * c.heads);
   if (p.rows == 16) k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
   else if (p.rows == 32) k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
   else k_attend_tiles<DP, MX, QBF, SPLIT><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
@@ -133,7 +138,7 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool
   };
   if (c.mx) go(std::true_type{});
   else go(std::false_type{});
-  k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * 4), 256, 0, stream>>>(c, a, p, out_vec);
+  if (most_parts(c, p) > 1) k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * 4), 256, 0, stream>>>(c, a, p, out_vec);
 }
 
 }  // namespace
@@ -141,14 +146,19 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool
 namespace fp4impl {
 
 size_t kv_attention_workspace_bytes(int64_t T, int64_t seqs, int q_heads, int heads, int dim) {
-  const UnitPlan p = plan_of(T, seqs, q_heads, heads, kMostResident);
-  return tiles_bytes(p) + (size_t)p.max_parts * heads * p.rows * (padded_dim(dim) + 2) * 4;
+  // (the most that any types of q and out take)
+  const int dp = padded_dim(dim);
+  size_t most = 0;
+  for (bool split : {false, true}) {
+    const UnitPlan p = plan_of(T, seqs, q_heads, heads, dp, split);
+    most = std::max(most, tiles_bytes(p) + (size_t)p.max_parts * heads * p.rows * (dp + 2) * 4);
+  }
+  return most;
 }
 
 hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStream_t stream) {
   const int dp = padded_dim(c.dim);
-  const bool split = !a.q_bf16 || !a.out_bf16;
-  UnitPlan p = plan_of(c.rows, c.seqs, a.q_heads, c.heads, resident(tile_rows(c.rows, c.seqs, a.q_heads / c.heads), dp, split));
+  UnitPlan p = plan_of(c.rows, c.seqs, a.q_heads, c.heads, dp, !a.q_bf16 || !a.out_bf16);
   p.causal = a.causal;
   p.window = a.window;
   p.tiles = a.workspace;

@@ -83,13 +83,18 @@ __device__ __forceinline__ void wave_lds_fence() {
 template <int DP>
 __device__ __forceinline__ int v_granule(int t, int g) { return DP == 64 ? g ^ ((t >> 1) & 3) : g ^ (t & 7); }
 
-// Four positions of a channel: lane i of each 16 points at row t (+ i / 4) and gets channel i of
-// granule g.
+// Where a lane points for a transposed read of granule 0 of rows t .. t + 3 (t a multiple of 4):
+// lane i of each 16 at row t + i / 4.  Granule g is at this ^ (32 g), and 8 rows further on the
+// same lane's place is 8 rows further on.
 template <int DP>
-__device__ __forceinline__ s16x4 read_v4(const uint8_t* tile, int t, int g) {
+__device__ __forceinline__ int v_address(int t) {
   const int i = threadIdx.x & 15, row = t + (i >> 2);
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (__attribute__((address_space(3))) s16x4*)(tile + row * (2 * DP) + 32 * v_granule<DP>(row, g) + 8 * (i & 3)));
+  return row * (2 * DP) + 32 * v_granule<DP>(row, 0) + 8 * (i & 3);
+}
+
+// Four positions of a channel: lane i of each 16 gets channel i of the granule.
+__device__ __forceinline__ s16x4 read_v4(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
 template <int DP, bool MX, bool QBF, bool SPLIT, int R>
@@ -113,16 +118,13 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
   PageWalk walk(c, u.b, t0);
   auto load = [&](int t0) {
     walk.reach(t0);
-    next.holes = 0;
+    next.holes = walk.holes_at(t0);              // (past the last position: masked anyway)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + 16 * i;
       int n = min(max(sp.t1 - t, 0), 16);
       int page = walk.at(t);
-      if (page < 0) {
-        next.holes |= 1 << i;    // (past the last position: masked anyway)
-        n = page = 0;
-      }
+      if (page < 0) n = page = 0;
       const int64_t row = cache_row(c, page, head, t);
       const int codes = c.dim / 2, scales = c.dim / (MX ? 32 : 16);
       load_quarter<DP, MX>(uniform_rsrc(c.k_codes + row * codes, n * codes), uniform_rsrc(c.k_scales + row * scales, n * scales),
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
   }
   int v_ref = 0;
   uint8_t* mine = tile[wave];
+  const int v_at0 = v_address<DP>(4 * quad);
 
   for (; t0 < sp.t1; t0 += 256) {
     const RawStep<DP> now = next;
@@ -265,7 +268,8 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
       wave_lds_fence();
 #pragma unroll
       for (int d = 0; d < kGranules; ++d) {
-        const s16x4 x = read_v4<DP>(mine, 4 * quad, d), y = read_v4<DP>(mine, 16 + 4 * quad, d);
+        const uint8_t* const from = mine + (v_at0 ^ (32 * d));
+        const s16x4 x = read_v4(from), y = read_v4(from + 16 * 2 * DP);
         const f16x8 v8 = __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
         for (int g = 0; g < R; ++g) {

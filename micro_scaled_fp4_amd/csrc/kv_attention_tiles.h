@@ -2,10 +2,11 @@
 //
 // Each of the four waves holds 32 rows (a row is lane % 32 of the 32x32x16 MFMAs).  A step of 64
 // positions is dequantized once for the workgroup into LDS as fp16 (wave w: positions 16 w ..
-// 16 w + 15), double-buffered: while a step is computed the next one's codes, already in
-// registers, wait; they are dequantized into the other buffer at the step's end, behind which
-// stands the loop's only barrier.
+// 16 w + 15), into two buffers in turn: step n + 1's while step n is computed; one barrier ends a
+// step.  Codes are loaded two steps ahead.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_attention.h"
 #include "kv_attention_few.h"
@@ -17,17 +18,13 @@ namespace fp4dev {
 template <int DP>
 __device__ __forceinline__ int k_chunk(int t, int chunk) { return DP == 64 ? chunk ^ ((t >> 1) & 7) : chunk ^ (t & 15); }
 
-template <int DP>
-struct StepBuffer {
-  uint8_t k[64 * DP * 2], v[64 * DP * 2];
-};
-
 template <int DP, bool MX, bool QBF, bool SPLIT>
 __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     k_attend_tiles(KvCache c, AttendProblem a, UnitPlan p, bool q_vec, bool out_vec) {
   constexpr int kDwords = DP / 32, kScales = DP == 256 ? 2 : 1, kSteps = DP / 16, kBlocks = DP / 32;
-  __shared__ __align__(16) StepBuffer<DP> buffer[2];
-  __shared__ int tops[16];                      // MX: [2][4 waves][keys, values]
+  // (objects of their own, so that the compiler sees which accesses can change places)
+  __shared__ __align__(16) uint8_t k_even[64 * DP * 2], k_odd[64 * DP * 2], v_even[64 * DP * 2], v_odd[64 * DP * 2];
+  __shared__ int tops[4][4][2];                 // MX: [round][wave][keys, values]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
   const int unit = workgroup() / c.heads, head = workgroup() % c.heads;
@@ -38,98 +35,71 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   if (!u.any || !has_room(p, u)) return;
   const Span sp = span_of(p, u, rows);
 
-  // codes of the step after this one, scales of the one after that
+  // This wave's 16 positions of each step, and where they are in the cache.
   const QuarterRow<DP, MX> at(lane >> 2, lane & 3, c.dim);
-  uint32_t kw[kDwords], vw[kDwords], ks[kScales], vs[kScales], ks2[kScales], vs2[kScales];
-  int holes = 0, holes_next = 0;                // of 16 positions each
-  PageWalk walk(c, u.b, sp.t0), walk2 = walk;   // along the codes, and one step ahead along the scales
-  auto load = [&](int t0, bool codes) {
-    const int t = t0 + 16 * wave;
+  const int code_row = c.dim / 2, scale_row = c.dim / (MX ? 32 : 16);
+  struct Raw {
+    uint32_t kw[kDwords], vw[kDwords], ks[kScales], vs[kScales];
+  };
+  PageWalk walk(c, u.b, sp.t0);
+  uint32_t holes = 0;                           // in a step: four bits of 16 positions each, of it and the next two
+  int ahead = sp.t0;                            // the next step to load
+  Raw near, far;                                // the next step, and the one after it
+  auto load = [&](Raw& raw) {
+    const int t = ahead + 16 * wave;
+    walk.reach(ahead);
     int n = min(max(sp.t1 - t, 0), 16);
-    (codes ? walk : walk2).reach(t0);
-    int page = (codes ? walk : walk2).at(t);
+    int page = walk.at(t);
     if (page < 0) n = page = 0;
     const int64_t row = cache_row(c, page, head, t);
-    const int cb = c.dim / 2, sb = c.dim / (MX ? 32 : 16);
-    if (codes) {
-      const __amdgpu_buffer_rsrc_t rk = uniform_rsrc(c.k_codes + row * cb, n * cb), rv = uniform_rsrc(c.v_codes + row * cb, n * cb);
-      if constexpr (DP == 64) {
-        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rk, at.code[0], 0, 0), y = __builtin_amdgcn_raw_buffer_load_b64(rv, at.code[0], 0, 0);
-        kw[0] = x[0], kw[1] = x[1], vw[0] = y[0], vw[1] = y[1];
-      } else {
-#pragma unroll
-        for (int j = 0; j < DP / 128; ++j) {
-          const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rk, at.code[j], 0, 0), y = __builtin_amdgcn_raw_buffer_load_b128(rv, at.code[j], 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) kw[4 * j + e] = x[e], vw[4 * j + e] = y[e];
-        }
-      }
-    } else {
-      const __amdgpu_buffer_rsrc_t rk = uniform_rsrc(c.k_scales + row * sb, n * sb), rv = uniform_rsrc(c.v_scales + row * sb, n * sb);
-#pragma unroll
-      for (int j = 0; j < kScales; ++j) {
-        if constexpr (MX || DP == 64) {
-          ks2[j] = __builtin_amdgcn_raw_buffer_load_b8(rk, at.scale[j], 0, 0);
-          vs2[j] = __builtin_amdgcn_raw_buffer_load_b8(rv, at.scale[j], 0, 0);
-        } else {
-          ks2[j] = __builtin_amdgcn_raw_buffer_load_b16(rk, at.scale[j], 0, 0);
-          vs2[j] = __builtin_amdgcn_raw_buffer_load_b16(rv, at.scale[j], 0, 0);
-        }
-      }
-    }
+    const int codes = n * code_row, scales = n * scale_row;
+    holes = holes >> 4 | walk.holes_at(ahead) << 8;   // (past the last position: masked anyway)
+    load_quarter<DP, MX>(uniform_rsrc(c.k_codes + row * code_row, codes), uniform_rsrc(c.k_scales + row * scale_row, scales), at,
+                         raw.kw, raw.ks);
+    load_quarter<DP, MX>(uniform_rsrc(c.v_codes + row * code_row, codes), uniform_rsrc(c.v_scales + row * scale_row, scales), at,
+                         raw.vw, raw.vs);
+    ahead += 64;
   };
-  // of the step whose codes were loaded last (past the last position: masked anyway)
-  auto holes_at = [&](int t0) {
-    int h = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h |= walk.at(t0 + 16 * i) < 0 ? 1 << i : 0;
-    return h;
-  };
-  // MX: this wave's largest scale bytes of the step whose scales are in ks2, vs2
-  auto note_tops = [&](int parity) {
+  // MX: this wave's largest scale bytes of a round, and all waves'
+  auto note_tops = [&](const Raw& raw, int round) {
     if constexpr (MX) {
-      int k = (int)ks2[0], v = (int)vs2[0];
-      if constexpr (kScales == 2) k = max(k, (int)ks2[1]), v = max(v, (int)vs2[1]);
+      int k = (int)raw.ks[0], v = (int)raw.vs[0];
+      if constexpr (kScales == 2) k = max(k, (int)raw.ks[1]), v = max(v, (int)raw.vs[1]);
       k = wave_max_lanes(k);
       v = wave_max_lanes(v);
       if (lane == 0) {
-        tops[(parity * 4 + wave) * 2] = k;
-        tops[(parity * 4 + wave) * 2 + 1] = v;
+        tops[round & 3][wave][0] = k;
+        tops[round & 3][wave][1] = v;
       }
     }
   };
-  int v_ref = 0, k_ref_next = 0, v_ref_next = 0;
-  auto take_tops = [&](int parity) {
+  int k_ref1 = 0, v_ref = 0, v_ref1 = 0;        // of the next step's keys; of the sums so far and the next step's values
+  auto take_tops = [&](int round) {
     if constexpr (MX) {
-      k_ref_next = 0;
+      int k = 0, v = v_ref1;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        k_ref_next = max(k_ref_next, tops[(parity * 4 + w) * 2]);
-        v_ref_next = max(v_ref_next, tops[(parity * 4 + w) * 2 + 1]);
+        k = max(k, tops[round & 3][w][0]);
+        v = max(v, tops[round & 3][w][1]);
       }
-      k_ref_next = __builtin_amdgcn_readfirstlane(k_ref_next);
-      v_ref_next = __builtin_amdgcn_readfirstlane(v_ref_next);
+      k_ref1 = __builtin_amdgcn_readfirstlane(k);
+      v_ref1 = __builtin_amdgcn_readfirstlane(v);
     }
   };
-  auto scales_arrive = [&]() {
-#pragma unroll
-    for (int j = 0; j < kScales; ++j) ks[j] = ks2[j], vs[j] = vs2[j];
-  };
-  auto dequantize = [&](int into) {
+  auto dequantize = [&](const Raw& raw, uint8_t* k_tile, uint8_t* v_tile) {
     const int t = 16 * wave + (lane >> 2);
-    uint8_t* const k = buffer[into].k + t * (2 * DP);
-    uint8_t* const v = buffer[into].v + t * (2 * DP);
+    uint8_t* const k = k_tile + t * (2 * DP);
+    uint8_t* const v = v_tile + t * (2 * DP);
 #pragma unroll
     for (int w = 0; w < kDwords; ++w) {
       const int chunk = (lane & 3) * kDwords + w;
-      *reinterpret_cast<f16x8*>(k + 16 * k_chunk<DP>(t, chunk)) = quarter8<DP, MX>(kw, ks, w, k_ref_next);
-      *reinterpret_cast<f16x8*>(v + 32 * v_granule<DP>(t, chunk >> 1) + 16 * (chunk & 1)) = quarter8<DP, MX>(vw, vs, w, v_ref_next);
+      *reinterpret_cast<f16x8*>(k + 16 * k_chunk<DP>(t, chunk)) = quarter8<DP, MX>(raw.kw, raw.ks, w, k_ref1);
+      *reinterpret_cast<f16x8*>(v + 32 * v_granule<DP>(t, chunk >> 1) + 16 * (chunk & 1)) = quarter8<DP, MX>(raw.vw, raw.vs, w, v_ref1);
     }
   };
 
-  // first step into buffer 0, its successor's codes and scales on their way
-  load(sp.t0, false);
-  load(sp.t0, true);
+  load(near);
+  load(far);
 
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
   const QueryRow row = query_row(u, p, head, u.tile * p.rows + 32 * wave + r32, rows_end, sp.t1);
@@ -163,16 +133,29 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     }
   }
 
-  note_tops(0);
-  scales_arrive();
-  load(sp.t0 + 64, false);
+  // scores of the step in a buffer: S^T[position][row r32]; register e of block b: position
+  // 32 b + 8 (e / 4) + 4 half + e % 4
+  const int k_place = r32 * (2 * DP) + 16 * k_chunk<DP>(r32, half);   // chunk 2 i + half: ^ (32 i)
+  auto scores = [&](const uint8_t* k_tile, f32x16 (&s)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[b][e] = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const f16x8 k8 = *reinterpret_cast<const f16x8*>(k_tile + 32 * b * (2 * DP) + (k_place ^ (32 * i)));
+        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, qh[i], s[b], 0, 0, 0);
+        if constexpr (SPLIT) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, ql[i], s[b], 0, 0, 0);
+      }
+  };
+
+  note_tops(near, 0);
+  note_tops(far, 1);
   __syncthreads();
   take_tops(0);
-  dequantize(0);
-  holes = holes_at(sp.t0);
-  load(sp.t0 + 64, true);
-  holes_next = holes_at(sp.t0 + 64);
-  note_tops(1);
+  dequantize(near, k_even, v_even);
   __syncthreads();
 
   f32x16 acc[kBlocks];
@@ -181,127 +164,108 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[d][e] = 0;
   float m = -INFINITY, l = 0;
-
-  int now = 0;
-  for (int t0 = sp.t0; t0 < sp.t1; t0 += 64, now ^= 1) {
-    // k_ref_next, v_ref_next: this step's references; the next step's scales are in ks2, vs2
-    const int k_ref = k_ref_next, v_top = v_ref_next;
-    const bool more = t0 + 64 < sp.t1;
-    scales_arrive();
-    if (more) load(t0 + 128, false);
-    // a wave whose rows all end before this step only takes part in what the workgroup shares
-    if (__any(t0 <= row.last && t0 + 63 >= row.first)) {
-      const uint8_t* const kt = buffer[now].k;
-      const uint8_t* const vt = buffer[now].v;
-      f32x16 s[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[b][e] = 0;
-        const int t = 32 * b + r32;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const f16x8 k8 = *reinterpret_cast<const f16x8*>(kt + t * (2 * DP) + 16 * k_chunk<DP>(t, 2 * i + half));
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, qh[i], s[b], 0, 0, 0);
-          if constexpr (SPLIT) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k8, ql[i], s[b], 0, 0, 0);
-        }
-      }
-      const float cf = MX ? fmaxf(__builtin_amdgcn_ldexpf(factor, k_ref - 140), 1e-37f) : factor;
-      // register e of block b: position 32 b + 8 (e / 4) + 4 half + e % 4
-      if (holes != 0 || __any(t0 + 63 > row.last || t0 < row.first)) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int o = 32 * b + 8 * (e >> 2) + 4 * half + (e & 3);
-            if (t0 + o > row.last || t0 + o < row.first || (holes >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
-          }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
-      top = max_over_halves(top);
-      const float was = m;
-      m = next_max(was, top * cf);
-      const float base = m == -INFINITY ? 0.0f : m;
-      const float drop = __builtin_amdgcn_exp2f(was - base);
-      f16x8 ph[4], pl[SPLIT ? 4 : 1];
-      float sum = 0;
+  const int v_at0 = v_address<DP>(4 * half) ^ (32 * ((lane >> 4) & 1));
+  int t0 = sp.t0, round = 2;
+  // Step t0; near: the step to dequantize, far: the one to load.
+  auto step = [&](auto odd, const Raw& near, Raw& far) {
+    uint8_t* const k_now = odd.value ? k_odd : k_even;
+    uint8_t* const k_next = odd.value ? k_even : k_odd;
+    uint8_t* const v_now = odd.value ? v_odd : v_even;
+    uint8_t* const v_next = odd.value ? v_even : v_odd;
+    load(far);
+    const int k_ref = k_ref1, v_top = v_ref1;
+    take_tops(round - 1);
+    f32x16 s[2];
+    scores(k_now, s);
+    const float cf = MX ? fmaxf(__builtin_amdgcn_ldexpf(factor, k_ref - 140), 1e-37f) : factor;
+    if ((holes & 15u) != 0 || __any(t0 + 63 > row.last || t0 < row.first)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], cf, kWeightBits - base));
-          sum += w;
-          const _Float16 h = (_Float16)w;
-          ph[2 * b + (e >> 3)][e & 7] = h;
-          if constexpr (SPLIT) pl[2 * b + (e >> 3)][e & 7] = (_Float16)(w - (float)h);
+          const int o = 32 * b + 8 * (e >> 2) + 4 * half + (e & 3);
+          if (t0 + o > row.last || t0 + o < row.first || (holes >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
         }
-      const float keep = MX ? __builtin_amdgcn_ldexpf(drop, v_ref - v_top) : drop;
-      if (__any(keep != 1.0f)) {
-        l *= drop;
+    }
+    float top = s[0][0];
 #pragma unroll
-        for (int d = 0; d < kBlocks; ++d) acc[d] *= keep;
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+    const float was = m;
+    m = next_max(was, max_over_halves(top) * cf);
+    const float base = m == -INFINITY ? 0.0f : m;
+    const float drop = __builtin_amdgcn_exp2f(was - base);
+    const float keep = MX ? __builtin_amdgcn_ldexpf(drop, v_ref - v_top) : drop;
+    if (__any(keep != 1.0f)) {
+      l *= drop;
+#pragma unroll
+      for (int d = 0; d < kBlocks; ++d) acc[d] *= keep;
+    }
+    v_ref = v_top;
+    f16x8 ph[4], pl[SPLIT ? 4 : 1];
+    float sum = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], cf, kWeightBits - base));
+        sum += w;
+        const _Float16 h = (_Float16)w;
+        ph[2 * b + (e >> 3)][e & 7] = h;
+        if constexpr (SPLIT) pl[2 * b + (e >> 3)][e & 7] = (_Float16)(w - (float)h);
       }
-      l += sum;
-      v_ref = v_top;
-      // O^T += V^T P^T: 16 positions at a time, in the order 4 half + 0 .. 3, 8 + 4 half + 0 .. 3
+    l += sum;
+    // O^T += V^T P^T: 16 positions at a time, in the order 4 half + 0 .. 3, 8 + 4 half + 0 .. 3
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int d = 0; d < kBlocks; ++d) {
-          const int g = 2 * d + ((lane >> 4) & 1);
-          const s16x4 x = read_v4<DP>(vt, 16 * i + 4 * half, g), y = read_v4<DP>(vt, 16 * i + 8 + 4 * half, g);
-          const f16x8 v8 = __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-          acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, ph[i], acc[d], 0, 0, 0);
-          if constexpr (SPLIT) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, pl[i], acc[d], 0, 0, 0);
-        }
+      for (int d = 0; d < kBlocks; ++d) {
+        const uint8_t* const from = v_now + 16 * i * (2 * DP) + (v_at0 ^ (64 * d));
+        const s16x4 x = read_v4(from), y = read_v4(from + 8 * 2 * DP);
+        const f16x8 v8 = __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, ph[i], acc[d], 0, 0, 0);
+        if constexpr (SPLIT) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v8, pl[i], acc[d], 0, 0, 0);
       }
     }
-    if (more) {
-      take_tops(now ^ 1);
-      dequantize(now ^ 1);
-      load(t0 + 128, true);
-      holes = holes_next;
-      holes_next = holes_at(t0 + 128);
-    }
-    // the step after the next one's references, for the end of the next step
-    note_tops(now);
+    dequantize(near, k_next, v_next);
+    note_tops(far, round);
+    t0 += 64;
+    ++round;
     __syncthreads();
+  };
+  while (t0 < sp.t1) {
+    step(std::integral_constant<int, 0>{}, far, near);
+    if (t0 >= sp.t1) break;
+    step(std::integral_constant<int, 1>{}, near, far);
   }
 
+  const float unit_of_v = MX ? __builtin_amdgcn_ldexpf(1.0f, v_ref - 140) : gv;
   // register e of block d: channel 32 d + 8 (e / 4) + 4 half + e % 4 of row r32
   l = sum_over_halves(l);
   if (row.h < 0) return;
-  const float unit_of_v = MX ? __builtin_amdgcn_ldexpf(1.0f, v_ref - 140) : gv;
-  if (u.count > 1) {
-    float* const left = part_of(p, c.heads, head, u.part0 + u.part, DP);
-    const int q = 32 * wave + r32;
-#pragma unroll
-    for (int d = 0; d < kBlocks; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (32 * d < c.dim)
-          *reinterpret_cast<f32x4*>(left + 2 * p.rows + q * DP + 32 * d + 8 * e + 4 * half) =
-              f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * unit_of_v;
-    if (half == 0) {
-      left[2 * q] = m;
-      left[2 * q + 1] = l;
-    }
-    return;
-  }
-  const float inverse = l > 0 ? 1.0f / l : 0.0f;
+  const int q = 32 * wave + r32;
+  float* const left = u.count > 1 ? part_of(p, c.heads, head, u.part0 + u.part, DP) : nullptr;
+  const float f = left != nullptr ? unit_of_v : l > 0 ? unit_of_v / l : 0.0f;
   const int64_t o = (row.r * a.q_heads + row.h) * c.dim;
 #pragma unroll
-  for (int d = 0; d < kBlocks; ++d)
+  for (int d = 0; d < kBlocks; ++d) {
+    if (32 * d >= c.dim) break;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (32 * d < c.dim)
-        store4(a.out, a.out_bf16, out_vec, o + 32 * d + 8 * e + 4 * half,
-               f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * unit_of_v * inverse);
-  if (half == 0 && a.lse != nullptr) a.lse[row.r * a.q_heads + row.h] = row_lse(m, l);
+    for (int e = 0; e < 4; ++e) {
+      const f32x4 v = f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * f;
+      const int channel = 32 * d + 8 * e + 4 * half;
+      if (left != nullptr) *reinterpret_cast<f32x4*>(left + 2 * p.rows + q * DP + channel) = v;
+      else store4(a.out, a.out_bf16, out_vec, o + channel, v);
+    }
+  }
+  if (half != 0) return;
+  if (left != nullptr) {
+    left[2 * q] = m;
+    left[2 * q + 1] = l;
+  } else if (a.lse != nullptr) {
+    a.lse[row.r * a.q_heads + row.h] = row_lse(m, l);
+  }
 }
 
 }  // namespace fp4dev

@@ -23,7 +23,7 @@ struct UnitPlan {
   int group;
   int min_per;                   // least steps of a part
   int target;                    // parts per key/value head that fill the card
-  bool fit;                      // no more than those, for kernels whose workgroups are all resident
+  int rounds;                    // at most that many such rounds are looked at
   int max_slots, max_parts;      // most tiles, and most parts of cut tiles (per head)
   bool causal;
   int window;
@@ -75,6 +75,18 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return moved(__builtin_amdgcn_readlane(bits(), 63));
 }
 
+__device__ __forceinline__ float max_lanes(float v) {   // v >= 0
+  auto at = [&](int x) { return __uint_as_float((uint32_t)x); };
+  auto bits = [&]() { return (int)__float_as_uint(v); };
+  v = fmaxf(v, at(__builtin_amdgcn_update_dpp(0, bits(), 0x111, 0xf, 0xf, false)));
+  v = fmaxf(v, at(__builtin_amdgcn_update_dpp(0, bits(), 0x112, 0xf, 0xf, false)));
+  v = fmaxf(v, at(__builtin_amdgcn_update_dpp(0, bits(), 0x114, 0xf, 0xf, false)));
+  v = fmaxf(v, at(__builtin_amdgcn_update_dpp(0, bits(), 0x118, 0xf, 0xf, false)));
+  v = fmaxf(v, at(__builtin_amdgcn_update_dpp(0, bits(), 0x142, 0xa, 0xf, false)));
+  v = fmaxf(v, at(__builtin_amdgcn_update_dpp(0, bits(), 0x143, 0xc, 0xf, false)));
+  return at(__builtin_amdgcn_readlane(bits(), 63));
+}
+
 struct Unit {
   int b, begin, n, length;       // the sequence: its first row, rows, positions
   int tile, slot;                // its row tile, and that among all sequences' tiles
@@ -106,44 +118,60 @@ __device__ __forceinline__ SeqSize seq_size(const KvCache& c, const UnitPlan& p,
 __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int u) {
   const int lane = threadIdx.x & 63, run = (c.seqs + 63) >> 6;
   const int b0 = min(lane * run, c.seqs), b1 = min(b0 + run, c.seqs);
-  float work = 0, all = 0;       // steps of all tiles, and tiles
-  for (int b = b0; b < b1; ++b) {
-    const SeqSize s = seq_size(c, p, b);
+  // (up to 64 sequences: one a lane, read once)
+  const SeqSize mine = b0 < b1 ? seq_size(c, p, b0) : SeqSize{0, 0, 0, 0, 1};
+  auto each = [&](auto f) {
+    f(mine);
+    for (int b = b0 + 1; b < b1; ++b) f(seq_size(c, p, b));
+  };
+  float work = 0, all = 0, longest = 0;         // steps of all tiles, tiles, the most steps of one
+  each([&](const SeqSize& s) {
     work += (float)s.tiles * (float)s.steps;
     all += (float)s.tiles;
-  }
+    longest = fmaxf(longest, s.tiles > 0 ? (float)s.steps : 0.0f);
+  });
   work = sum_lanes(work);
   all = sum_lanes(all);
   Unit r{};
   // offsets that decrease can give more tiles than there are rows: nothing is done then
   r.slots = 0x7fffffff;
   if (!(all <= 1.01f * (float)p.max_slots)) return r;
-  const float share = ceilf(work / (float)p.target);
-  r.per = max(p.min_per, (int)fminf(share, 1.0e9f));
-  if (p.fit && 2.0f * all < (float)p.target) {
-    // the shortest parts that are no more than `target`: each tile's last part is shorter than the
-    // others, so share gives up to a part more for each tile, and work / (target - all) never does
-    int lo = r.per, hi = max(p.min_per, (int)ceilf(work / ((float)p.target - all)));
-    for (int i = 0; i < 4 && lo < hi; ++i) {
-      const int mid = (lo + hi) >> 1;
-      float units = 0;
-      for (int b = b0; b < b1; ++b) {
-        const SeqSize s = seq_size(c, p, b);
-        units += (float)(s.tiles * ((s.steps + mid - 1) / mid));
+  const float target = (float)p.target;
+  r.per = max(p.min_per, (int)fminf(ceilf(work / target), 1.0e9f));
+  if (all < p.rounds * target && work > 0) {
+    // Parts of the same length run in rounds of `target`: the shortest length that needs no more
+    // than k rounds, for the k with the least time (kStart steps for a part's beginning and end).
+    constexpr float kStart = 4;
+    longest = max_lanes(longest);
+    float best = INFINITY;
+    for (int k = 1; k <= p.rounds; ++k) {
+      const float room = k * target;
+      if (all > room) continue;
+      const float least = fmaxf(ceilf(work / room), (float)p.min_per);
+      float lo = least, hi = fmaxf(lo, all < room ? fminf(longest, ceilf(work / (room - all))) : longest);
+      for (int i = 0; i < 6 && lo < hi; ++i) {
+        const float mid = floorf(0.5f * (lo + hi)), inverse = (1.0f + 0x1p-21f) / mid;   // never too few
+        float units = 0;
+        each([&](const SeqSize& s) { units += (float)s.tiles * ceilf((float)s.steps * inverse); });
+        if (sum_lanes(units) <= room) hi = mid;
+        else lo = mid + 1;
       }
-      if (sum_lanes(units) <= (float)p.target) hi = mid;
-      else lo = mid + 1;
+      const float time = k * (hi + kStart);
+      if (time < best) {
+        best = time;
+        r.per = (int)hi;
+      }
+      if (hi <= 1.125f * least + 1) break;      // a round more has nothing left to fill
     }
-    r.per = hi;
   }
+  r.per = __builtin_amdgcn_readfirstlane(r.per);
   int units = 0, parts = 0, tiles = 0;
-  for (int b = b0; b < b1; ++b) {
-    const SeqSize s = seq_size(c, p, b);
+  each([&](const SeqSize& s) {
     const int count = (s.steps + r.per - 1) / r.per;
     units += s.tiles * count;
     parts += count > 1 ? s.tiles * count : 0;
     tiles += s.tiles;
-  }
+  });
   const int units_to = scan_lanes(units), parts_to = scan_lanes(parts), tiles_to = scan_lanes(tiles);
   r.slots = __builtin_amdgcn_readlane(tiles_to, 63);
   r.any = u < __builtin_amdgcn_readlane(units_to, 63);
@@ -152,9 +180,16 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
   int left = u - __builtin_amdgcn_readlane(units_to - units, at);
   int part0 = __builtin_amdgcn_readlane(parts_to - parts, at), slot = __builtin_amdgcn_readlane(tiles_to - tiles, at);
   for (int b = at * run; b < c.seqs; ++b) {
-    const SeqSize s = seq_size(c, p, b);
-    const int count = __builtin_amdgcn_readfirstlane((s.steps + r.per - 1) / r.per);
+    SeqSize s;
+    if (b == at * run) {
+      s = {__builtin_amdgcn_readlane(mine.begin, at), __builtin_amdgcn_readlane(mine.n, at),
+           __builtin_amdgcn_readlane(mine.length, at), __builtin_amdgcn_readlane(mine.tiles, at),
+           __builtin_amdgcn_readlane(mine.steps, at)};
+    } else {
+      s = seq_size(c, p, b);
+    }
     const int tiles_b = __builtin_amdgcn_readfirstlane(s.tiles);
+    const int count = __builtin_amdgcn_readfirstlane((s.steps + r.per - 1) / r.per);
     if (left < tiles_b * count) {
       // later rows see more positions and start first
       const int k = left / count;
@@ -178,36 +213,46 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
   return r;
 }
 
-// The page table of a sequence as a wave walks along it: lane i holds entry base + i (-1: a hole
-// or past the table), and the next 64 entries are on their way, so that no page number is waited
-// for.
+// The page table of a sequence as a wave walks along it in steps of 64 positions: lane i holds
+// entry base + i (-1: a hole or past the table), and the next 64 entries are on their way, so that
+// no page number is waited for.  A step's entries (1, 2 or 4, and 64 is a multiple of them) are
+// among the 64.
 struct PageWalk {
   const int32_t* table;
   int max_pages, num_pages, shift, base, now, next;
+  uint64_t holes;                // of `now`
 
   __device__ __forceinline__ int entries(int from) const {
     const int i = from + (int)(threadIdx.x & 63);
     const int p = i < max_pages ? table[i] : -1;
     return p >= 0 && p < num_pages ? p : -1;
   }
-  // from position t on
+  // from step t on (a multiple of 64)
   __device__ __forceinline__ PageWalk(const KvCache& c, int b, int t)
       : table(c.pages + b * c.max_pages), max_pages((int)c.max_pages), num_pages((int)c.num_pages),
         shift(c.page_shift), base(t >> c.page_shift) {
     now = entries(base);
     next = entries(base + 64);
+    holes = __ballot(now < 0);
   }
-  // Makes at() valid for the 64 positions from t on (t is the same in all lanes and does not decrease).
+  // To step t, the same in all lanes, not before the last one.
   __device__ __forceinline__ void reach(int t) {
     while ((t >> shift) - base >= 64) {
       base += 64;
       now = next;
       next = entries(base + 64);
+      holes = __ballot(now < 0);
     }
   }
-  __device__ __forceinline__ int at(int t) const {
-    const int i = (t >> shift) - base;
-    return i < 64 ? __builtin_amdgcn_readlane(now, i) : __builtin_amdgcn_readlane(next, i - 64);
+  // The page of a position of the step reached.
+  __device__ __forceinline__ int at(int t) const { return __builtin_amdgcn_readlane(now, (t >> shift) - base); }
+  // Bit i: positions t + 16 i .. of the step t reached are in a hole.
+  __device__ __forceinline__ uint32_t holes_at(int t) const {
+    if (holes == 0) return 0;
+    uint32_t h = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h |= (uint32_t)(holes >> (((t + 16 * i) >> shift) - base) & 1) << i;
+    return h;
   }
 };
 
