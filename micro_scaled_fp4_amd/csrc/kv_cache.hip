@@ -20,6 +20,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+// From here on a wave reads four rows: 4096 waves fill the card, and a row's look-up of its sequence
+// and page is a chain of loads.
+constexpr int kManyRows = 16384;
 
 // N consecutive values from x + i.  VEC: x + i is 16-byte aligned.
 template <bool BF16, bool VEC, int N>
@@ -110,64 +113,105 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(KvCache c, const void* k,
 // Eight values of codes and their scale as fp4_dequantize gives them.
 template <bool MX>
 __device__ __forceinline__ void dequant8_f32(uint32_t codes, uint32_t byte, float s_global, float (&v)[8]) {
-  const float s = MX ? e8m0_value(byte) : s_global * e4m3_value(byte);
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const float s = MX ? e8m0_value(byte) : s_global * __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
+  const f32x2 p[4] = {
+      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1),
+      __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3)};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = s * e2m1_value((codes >> (4 * j)) & 15u);
-}
-
-template <bool MX, bool BF16, bool VEC>
-__device__ __forceinline__ void read_row(const KvCache& c, void* y, int64_t at, const uint8_t* codes,
-                                         const uint8_t* scales, float s_global, int page, int t) {
-  const int lane = threadIdx.x & 63, units = c.heads * c.dim >> 3, per_head = c.dim >> 3;
-  constexpr int kShift = MX ? 2 : 1;            // units of a scale
-  for (int u = lane; u < units; u += 64) {
-    const int head = u / per_head, part = u - head * per_head;
-    uint32_t w = 0, byte = 0;
-    if (page >= 0) {
-      const int64_t row = cache_row(c, page, head, t);
-      w = reinterpret_cast<const uint32_t*>(codes)[row * per_head + part];
-      byte = scales[row * (per_head >> kShift) + (part >> kShift)];
-    }
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (page >= 0) dequant8_f32<MX>(w, byte, s_global, v);
-    const int64_t i = at + (int64_t)u * 8;
-    if constexpr (BF16) {
-      uint16_t* p = static_cast<uint16_t*>(y) + i;
-      const u32x4 o{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]), bf16_pack2(v[6], v[7])};
-      if constexpr (VEC) {
-        *reinterpret_cast<u32x4*>(p) = o;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
-      }
-    } else {
-      float* p = static_cast<float*>(y) + i;
-      if constexpr (VEC) {
-        reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-        reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = v[j];
-      }
-    }
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = s * p[j][0];
+    v[2 * j + 1] = s * p[j][1];
   }
 }
 
-template <bool MX, bool BF16, bool VEC>
+// A wave's next row: output row r at position t (page < 0: zeros).
+struct ReadRow {
+  int page, t;
+};
+
+// The wave reads kRows rows; a lane takes units of 8 values (keys first, then values) of all of them.
+template <bool MX, bool BF16, bool VEC, int kRows>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int32_t* starts, void* k, void* v) {
-  const int r = (int)(workgroup() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
-  if (r >= c.rows) return;
-  const int b = seq_of_row(c, r);
-  if (b < 0) return;
-  const int begin = seq_begin(c, b), end = seq_end(c, b, begin);
-  if (r >= end) return;
-  const int length = seq_length(c, b);
-  const int64_t t = starts != nullptr ? (int64_t)starts[b] + (r - begin) : length - (end - r);
-  const int page = t >= 0 && t < length ? page_of(c, b, (int)t) : -1;
+  const int first = (int)(workgroup() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kRows;
+  if (first >= c.rows) return;
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
-  const int64_t at = (int64_t)r * c.heads * c.dim;
-  read_row<MX, BF16, VEC>(c, k, at, c.k_codes, c.k_scales, gk, page, (int)t);
-  read_row<MX, BF16, VEC>(c, v, at, c.v_codes, c.v_scales, gv, page, (int)t);
+  ReadRow rows[kRows];
+  int b = -1, begin = 0, end = 0, length = 0, start = 0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = first + i;
+    rows[i] = {-1, -1};
+    if (r >= c.rows) continue;
+    if (i == 0 || r >= end) {                   // the next sequence
+      b = seq_of_row(c, r);
+      if (b < 0) continue;
+      begin = seq_begin(c, b);
+      end = seq_end(c, b, begin);
+      length = seq_length(c, b);
+      start = starts != nullptr ? starts[b] : length - (end - begin);
+    }
+    if (r >= end) continue;
+    const int64_t t = (int64_t)start + (r - begin);
+    rows[i] = {t >= 0 && t < length ? page_of(c, b, (int)t) : -1, (int)(t >= 0 && t < length ? t : 0)};
+  }
+  const int lane = threadIdx.x & 63, units = c.heads * c.dim >> 3, per_head = c.dim >> 3;
+  constexpr int kShift = MX ? 2 : 1;            // units of a scale
+  constexpr int kUnits = kRows == 1 ? 4 : 2;    // of a lane at a time, for each row
+  for (int u0 = 0; u0 < 2 * units; u0 += 64 * kUnits) {
+    int head[kUnits], part[kUnits];
+    uint32_t w[kRows][kUnits], byte[kRows][kUnits];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      const int u = u0 + 64 * j + lane;
+      const bool value = u >= units;
+      const int x = value ? u - units : u;
+      head[j] = x / per_head;
+      part[j] = x - head[j] * per_head;
+      const uint32_t* const codes = reinterpret_cast<const uint32_t*>(value ? c.v_codes : c.k_codes) + part[j];
+      const uint8_t* const scales = (value ? c.v_scales : c.k_scales) + (part[j] >> kShift);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        w[i][j] = byte[i][j] = 0;
+        if (u < 2 * units && rows[i].page >= 0) {
+          const int64_t row = cache_row(c, rows[i].page, head[j], rows[i].t);
+          w[i][j] = codes[row * per_head];
+          byte[i][j] = scales[row * (per_head >> kShift)];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) {
+        const int u = u0 + 64 * j + lane;
+        if (u >= 2 * units || rows[i].t < 0) continue;   // (t < 0: no sequence's row)
+        const bool value = u >= units;
+        const int64_t o = (int64_t)(first + i) * c.heads * c.dim + (value ? u - units : u) * 8;
+        float x[8];
+        dequant8_f32<MX>(w[i][j], byte[i][j], value ? gv : gk, x);
+        if constexpr (BF16) {
+          uint16_t* const p = static_cast<uint16_t*>(value ? v : k) + o;
+          const u32x4 y{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]), bf16_pack2(x[6], x[7])};
+          if constexpr (VEC) {
+            __builtin_nontemporal_store(y, reinterpret_cast<u32x4*>(p));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
+          }
+        } else {
+          float* const p = static_cast<float*>(value ? v : k) + o;
+          if constexpr (VEC) {
+            __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4*>(p));
+            __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4*>(p) + 1);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = x[e];
+          }
+        }
+      }
+    }
+  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -198,8 +242,13 @@ hipError_t launch_kv_write(const KvCache& c, const void* k, int64_t k_stride, co
 hipError_t launch_kv_read(const KvCache& c, const int32_t* starts, void* k, void* v, bool bf16,
                           hipStream_t stream) {
   select3(c.mx, bf16, aligned16(k) && aligned16(v), [&](auto mx, auto bf, auto al) {
-    k_kv_read<mx.value, bf.value, al.value><<<grid_of((c.rows + kWaves - 1) / kWaves), kThreads, 0, stream>>>(
-        c, starts, k, v);
+    auto go = [&](auto rows) {
+      constexpr int kRows = rows.value;
+      k_kv_read<mx.value, bf.value, al.value, kRows>
+          <<<grid_of((c.rows + kRows * kWaves - 1) / (kRows * kWaves)), kThreads, 0, stream>>>(c, starts, k, v);
+    };
+    if (c.rows >= kManyRows) go(std::integral_constant<int, 4>{});
+    else go(std::integral_constant<int, 1>{});
   });
   return hipGetLastError();
 }
