@@ -112,32 +112,19 @@ __device__ __forceinline__ QueryRow query_row(const Unit& u, const UnitPlan& p, 
   return q;
 }
 
-// Eight consecutive values of a query row.  VEC: 16-byte aligned.
+// Eight consecutive values of a query row.  (Element alignment is enough for 16-byte accesses to global memory.)
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* q, int64_t i, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void* q, int64_t i, float (&v)[8]) {
   if constexpr (BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(q) + i;
-    if (vec) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+    u32x4 w;
+    __builtin_memcpy(&w, static_cast<const uint16_t*>(q) + i, 16);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16_lo(w[j]);
-        v[2 * j + 1] = bf16_hi(w[j]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(w[j]);
+      v[2 * j + 1] = bf16_hi(w[j]);
     }
   } else {
-    const float* p = static_cast<const float*>(q) + i;
-    if (vec) {
-      const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[j];
-    }
+    __builtin_memcpy(v, static_cast<const float*>(q) + i, 32);
   }
 }
 
@@ -159,24 +146,12 @@ __device__ __forceinline__ void to_f16(const float (&v)[8], f16x8& hi, f16x8& lo
 }
 
 // Four consecutive output values.
-__device__ __forceinline__ void store4(void* out, bool bf16, bool vec, int64_t i, f32x4 v) {
+__device__ __forceinline__ void store4(void* out, bool bf16, int64_t i, f32x4 v) {
   if (bf16) {
-    uint16_t* p = static_cast<uint16_t*>(out) + i;
     const u32x2 w{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])};
-    if (vec) {
-      *reinterpret_cast<u32x2*>(p) = w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-    }
+    __builtin_memcpy(static_cast<uint16_t*>(out) + i, &w, 8);
   } else {
-    float* p = static_cast<float*>(out) + i;
-    if (vec) {
-      *reinterpret_cast<f32x4*>(p) = v;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = v[j];
-    }
+    __builtin_memcpy(static_cast<float*>(out) + i, &v, 16);
   }
 }
 

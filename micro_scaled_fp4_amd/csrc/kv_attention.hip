@@ -22,7 +22,7 @@ namespace {
 // then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
 // sums meet in LDS.
 template <int DP>
-__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, bool out_vec) {
+__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p) {
   constexpr int kChunk = 256, kPer = DP / 64;
   typedef float fv __attribute__((ext_vector_type(kPer)));
   __shared__ float weight[4][kChunk], total[4];
@@ -30,10 +30,10 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
   const TileParts* tiles = static_cast<const TileParts*>(p.tiles);
   const int at = workgroup() >> 2;              // four workgroups a tile
   const int slot = at / c.heads, head = at % c.heads;
+  if (slot >= p.max_slots) return;
   const int slots = tiles[p.max_slots].begin;
-  if (slot >= slots || slots > p.max_slots) return;
   const TileParts t = tiles[slot];
-  if (t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts) return;
+  if (slot >= slots || slots > p.max_slots || t.count <= 1 || t.part0 < 0 || t.part0 + t.count > p.max_parts) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float* const first = part_of(p, c.heads, head, t.part0, DP);
   const int64_t stride = part_of(p, c.heads, head, t.part0 + 1, DP) - first;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
       }
       __syncthreads();
       const float* const from = first + k0 * stride + 2 * p.rows + q0 * DP + lane * kPer;
-#pragma unroll 4
+#pragma unroll 6
       for (int k = wave; k < n; k += 4) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum[r] += *reinterpret_cast<const fv*>(from + k * stride + r * DP) * weight[r][k];
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
         f32x4 v{0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][wave][4 * lane]);
-        store4(a.out, a.out_bf16, out_vec, row * c.dim + 4 * lane, v * inverse);
+        store4(a.out, a.out_bf16, row * c.dim + 4 * lane, v * inverse);
       }
       if (lane == 0 && a.lse != nullptr) a.lse[row] = row_lse(top, total[wave]);
     }
@@ -96,7 +96,7 @@ int tile_rows(int64_t T, int64_t seqs, int group) {
 int resident(int rows, int dp, bool split) {
   if (rows == 128) return dp == 256 ? 1 : 2;
   if (rows == 16) return dp == 64 ? (split ? 3 : 4) : dp == 128 ? (split ? 2 : 3) : 1;
-  return dp == 64 ? (split ? 2 : 3) : 1;
+  return dp == 64 ? (split ? 2 : 3) : dp == 128 && !split ? 2 : 1;
 }
 
 UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool split) {
@@ -121,24 +121,26 @@ int64_t most_units(const KvCache& c, const UnitPlan& p) {
 }
 
 template <int DP, bool MX, bool QBF, bool SPLIT>
-void launch(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool q_vec, bool out_vec, hipStream_t stream) {
+void launch(const KvCache& c, const AttendProblem& a, const UnitPlan& p, hipStream_t stream) {
   const dim3 grid = fp4impl::grid_of(most_units(c, p) * c.heads);
-  if (p.rows == 16) k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
-  else if (p.rows == 32) k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
-  else k_attend_tiles<DP, MX, QBF, SPLIT><<<grid, 256, 0, stream>>>(c, a, p, q_vec, out_vec);
+  if (p.rows == 16) k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p);
+  else if (p.rows == 32) k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p);
+  else k_attend_tiles<DP, MX, QBF, SPLIT><<<grid, 256, 0, stream>>>(c, a, p);
 }
 
 template <int DP>
-void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, bool q_vec, bool out_vec, hipStream_t stream) {
+void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, hipStream_t stream) {
   const bool split = !a.q_bf16 || !a.out_bf16;
   auto go = [&](auto mx) {
-    if (!a.q_bf16) launch<DP, mx.value, false, true>(c, a, p, q_vec, out_vec, stream);
-    else if (split) launch<DP, mx.value, true, true>(c, a, p, q_vec, out_vec, stream);
-    else launch<DP, mx.value, true, false>(c, a, p, q_vec, out_vec, stream);
+    if (!a.q_bf16) launch<DP, mx.value, false, true>(c, a, p, stream);
+    else if (split) launch<DP, mx.value, true, true>(c, a, p, stream);
+    else launch<DP, mx.value, true, false>(c, a, p, stream);
   };
   if (c.mx) go(std::true_type{});
   else go(std::false_type{});
-  if (most_parts(c, p) > 1) k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * 4), 256, 0, stream>>>(c, a, p, out_vec);
+  if (most_parts(c, p) <= 1) return;
+  const dim3 grid = fp4impl::grid_of((int64_t)p.max_slots * c.heads * 4);
+  k_join_parts<DP><<<grid, 256, 0, stream>>>(c, a, p);
 }
 
 }  // namespace
@@ -163,12 +165,9 @@ hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStre
   p.window = a.window;
   p.tiles = a.workspace;
   p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + tiles_bytes(p));
-  auto multiple = [](const void* x, int64_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };
-  const bool q_vec = multiple(a.q, 16) && a.q_stride * (a.q_bf16 ? 2 : 4) % 16 == 0;
-  const bool out_vec = multiple(a.out, a.out_bf16 ? 8 : 16);
-  if (dp == 64) launch_dp<64>(c, a, p, q_vec, out_vec, stream);
-  else if (dp == 128) launch_dp<128>(c, a, p, q_vec, out_vec, stream);
-  else launch_dp<256>(c, a, p, q_vec, out_vec, stream);
+  if (dp == 64) launch_dp<64>(c, a, p, stream);
+  else if (dp == 128) launch_dp<128>(c, a, p, stream);
+  else launch_dp<256>(c, a, p, stream);
   return hipGetLastError();
 }
 

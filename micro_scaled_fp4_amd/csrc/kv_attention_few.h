@@ -36,6 +36,7 @@ struct QuarterRow {
   }
 };
 
+// A lane's quarter row.
 template <int DP, bool MX>
 __device__ __forceinline__ void load_quarter(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales,
                                              const QuarterRow<DP, MX>& at, uint32_t (&w)[DP / 32],
@@ -98,14 +99,15 @@ __device__ __forceinline__ s16x4 read_v4(const uint8_t* p) {
 }
 
 template <int DP, bool MX, bool QBF, bool SPLIT, int R>
-__global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
-    k_attend_few(KvCache c, AttendProblem a, UnitPlan p, bool q_vec, bool out_vec) {
+__global__ void __launch_bounds__(256, DP == 256 || (R == 2 && DP == 128 && SPLIT) ? 1 : 2)
+    k_attend_few(KvCache c, AttendProblem a, UnitPlan p) {
   constexpr int kDwords = DP / 32, kGranules = DP / 16;
   __shared__ __align__(16) uint8_t tile[4][32 * DP * 2];
   __shared__ float stats[4][16][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quad = lane >> 4;
   const int unit = workgroup() / c.heads, head = workgroup() % c.heads;
+  const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
   const Unit u = unit_of(c, p, unit);
   const int rows_end = min((u.tile + 1) * p.rows, u.n * p.group);
   if (head == 0) note_tile(p, u, unit, rows_end - u.tile * p.rows);
@@ -119,23 +121,32 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
   auto load = [&](int t0) {
     walk.reach(t0);
     next.holes = walk.holes_at(t0);              // (past the last position: masked anyway)
+    const int codes = c.dim / 2, scales = c.dim / (MX ? 32 : 16);
+    // 16 positions at a time; pages of 64 and more positions hold the whole step
+    const bool whole = c.page_shift >= 6;
+    int64_t codes_at = 0, scales_at = 0;
+    int page = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + 16 * i;
-      int n = min(max(sp.t1 - t, 0), 16);
-      int page = walk.at(t);
-      if (page < 0) n = page = 0;
-      const int64_t row = cache_row(c, page, head, t);
-      const int codes = c.dim / 2, scales = c.dim / (MX ? 32 : 16);
-      load_quarter<DP, MX>(uniform_rsrc(c.k_codes + row * codes, n * codes), uniform_rsrc(c.k_scales + row * scales, n * scales),
-                           k_at, next.k[i], next.ks[i]);
-      load_quarter<DP, MX>(uniform_rsrc(c.v_codes + row * codes, n * codes), uniform_rsrc(c.v_scales + row * scales, n * scales),
-                           v_at, next.v[i], next.vs[i]);
+      if (i == 0 || !whole) {
+        page = walk.at(t);
+        const int64_t row = cache_row(c, max(page, 0), head, t);
+        codes_at = row * codes;
+        scales_at = row * scales;
+      } else {
+        codes_at += 16 * codes;
+        scales_at += 16 * scales;
+      }
+      const int n = page < 0 ? 0 : min(max(sp.t1 - t, 0), 16);
+      load_quarter<DP, MX>(uniform_rsrc(c.k_codes + codes_at, n * codes), uniform_rsrc(c.k_scales + scales_at, n * scales), k_at,
+                           next.k[i], next.ks[i]);
+      load_quarter<DP, MX>(uniform_rsrc(c.v_codes + codes_at, n * codes), uniform_rsrc(c.v_scales + scales_at, n * scales), v_at,
+                           next.v[i], next.vs[i]);
     }
   };
   if (t0 < sp.t1) load(t0);
 
-  const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
   f16x8 qh[R][kDwords], ql[R][SPLIT ? kDwords : 1];
   float factor[R];                              // c: scores -> base-2 exponents
   QueryRow row[R];
@@ -149,7 +160,7 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
       const int d = quad * (DP / 4) + 8 * i;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = 0;
-      if (row[g].h >= 0 && d < c.dim) load8<QBF>(a.q, row[g].r * a.q_stride + (int64_t)row[g].h * c.dim + d, q_vec, v[i]);
+      if (row[g].h >= 0 && d < c.dim) load8<QBF>(a.q, row[g].r * a.q_stride + (int64_t)row[g].h * c.dim + d, v[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = umax(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
     }
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(256, R* DP >= 256 ? 1 : 2)
 #pragma unroll
       for (int w = 0; w < 4; ++w) sumv += *reinterpret_cast<const f32x4*>(whole + (w * 16 + q) * DP + 4 * (chunk ^ q)) * part[w];
       if (left != nullptr) *reinterpret_cast<f32x4*>(left + 2 * p.rows + (16 * g + q) * DP + 4 * chunk) = sumv;
-      else store4(a.out, a.out_bf16, out_vec, o + 4 * chunk, sumv * inverse);
+      else store4(a.out, a.out_bf16, o + 4 * chunk, sumv * inverse);
     }
     if (c16 == 0) {
       if (left != nullptr) {

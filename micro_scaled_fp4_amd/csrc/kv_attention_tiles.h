@@ -20,7 +20,7 @@ __device__ __forceinline__ int k_chunk(int t, int chunk) { return DP == 64 ? chu
 
 template <int DP, bool MX, bool QBF, bool SPLIT>
 __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
-    k_attend_tiles(KvCache c, AttendProblem a, UnitPlan p, bool q_vec, bool out_vec) {
+    k_attend_tiles(KvCache c, AttendProblem a, UnitPlan p) {
   constexpr int kDwords = DP / 32, kScales = DP == 256 ? 2 : 1, kSteps = DP / 16, kBlocks = DP / 32;
   // (objects of their own, so that the compiler sees which accesses can change places)
   __shared__ __align__(16) uint8_t k_even[64 * DP * 2], k_odd[64 * DP * 2], v_even[64 * DP * 2], v_odd[64 * DP * 2];
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
       const int d = 16 * i + 8 * half;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = 0;
-      if (row.h >= 0 && d < c.dim) load8<QBF>(a.q, row.r * a.q_stride + (int64_t)row.h * c.dim + d, q_vec, v);
+      if (row.h >= 0 && d < c.dim) load8<QBF>(a.q, row.r * a.q_stride + (int64_t)row.h * c.dim + d, v);
     };
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
       const f32x4 v = f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * f;
       const int channel = 32 * d + 8 * e + 4 * half;
       if (left != nullptr) *reinterpret_cast<f32x4*>(left + 2 * p.rows + q * DP + channel) = v;
-      else store4(a.out, a.out_bf16, out_vec, o + channel, v);
+      else store4(a.out, a.out_bf16, o + channel, v);
     }
   }
   if (half != 0) return;

@@ -8,6 +8,8 @@
 //   Read: a lane dequantizes 8 values (one dword of codes) and stores 16 bytes of bf16.
 // Both are bound by HBM bytes (a row of 8 heads x 128 bf16 channels moves 4096 bytes one
 // way and 1152 the other).
+#include <type_traits>
+
 #include "fp4_device.h"
 #include "fp4_internal.h"
 #include "grid.h"
@@ -24,42 +26,25 @@ constexpr int kWaves = kThreads / 64;
 // and page is a chain of loads.
 constexpr int kManyRows = 16384;
 
-// N consecutive values from x + i.  VEC: x + i is 16-byte aligned.
-template <bool BF16, bool VEC, int N>
-__device__ __forceinline__ void load_values(const void* x, int64_t i, float (&v)[N]) {
+// Sixteen consecutive values from x + i.  (Element alignment is enough for 16-byte accesses to global memory.)
+template <bool BF16>
+__device__ __forceinline__ void load16(const void* x, int64_t i, float (&v)[16]) {
   if constexpr (BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(x) + i;
-    if constexpr (VEC) {
+    u32x4 w[2];
+    __builtin_memcpy(w, static_cast<const uint16_t*>(x) + i, 32);
 #pragma unroll
-      for (int j = 0; j < N / 8; ++j) {
-        const u32x4 w = reinterpret_cast<const u32x4*>(p)[j];
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[8 * j + 2 * e] = bf16_lo(w[e]);
-          v[8 * j + 2 * e + 1] = bf16_hi(w[e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        v[8 * j + 2 * e] = bf16_lo(w[j][e]);
+        v[8 * j + 2 * e + 1] = bf16_hi(w[j][e]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
-    }
   } else {
-    const float* p = static_cast<const float*>(x) + i;
-    if constexpr (VEC) {
-#pragma unroll
-      for (int j = 0; j < N / 4; ++j) {
-        const f32x4 w = reinterpret_cast<const f32x4*>(p)[j];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * j + e] = w[e];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = p[j];
-    }
+    __builtin_memcpy(v, static_cast<const float*>(x) + i, 64);
   }
 }
 
-template <bool MX, bool BF16, bool VEC>
+template <bool MX, bool BF16>
 __device__ __forceinline__ void write_row(const KvCache& c, const void* x, int64_t at, uint8_t* codes,
                                           uint8_t* scales, float s_global, int page, int t) {
   const int lane = threadIdx.x & 63, units = c.heads * c.dim >> 4, per_head = c.dim >> 4;
@@ -68,7 +53,7 @@ __device__ __forceinline__ void write_row(const KvCache& c, const void* x, int64
     if (u >= units) break;
     const int head = u / per_head, part = u - head * per_head;
     float v[16];
-    load_values<BF16, VEC>(x, at + (int64_t)u * 16, v);
+    load16<BF16>(x, at + (int64_t)u * 16, v);
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) m = umax(m, __float_as_uint(v[j]) & 0x7fffffffu);
@@ -93,7 +78,7 @@ __device__ __forceinline__ void write_row(const KvCache& c, const void* x, int64
   }
 }
 
-template <bool MX, bool BF16, bool VEC>
+template <bool MX, bool BF16>
 __global__ void __launch_bounds__(kThreads) k_kv_write(KvCache c, const void* k, int64_t k_stride, const void* v,
                                                        int64_t v_stride) {
   const int r = (int)(workgroup() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
@@ -106,8 +91,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_write(KvCache c, const void* k,
   const int page = page_of(c, b, t);
   if (page < 0) return;
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
-  write_row<MX, BF16, VEC>(c, k, r * k_stride, c.k_codes, c.k_scales, gk, page, t);
-  write_row<MX, BF16, VEC>(c, v, r * v_stride, c.v_codes, c.v_scales, gv, page, t);
+  write_row<MX, BF16>(c, k, r * k_stride, c.k_codes, c.k_scales, gk, page, t);
+  write_row<MX, BF16>(c, v, r * v_stride, c.v_codes, c.v_scales, gv, page, t);
 }
 
 // Eight values of codes and their scale as fp4_dequantize gives them.
@@ -131,7 +116,7 @@ struct ReadRow {
 };
 
 // The wave reads kRows rows; a lane takes units of 8 values (keys first, then values) of all of them.
-template <bool MX, bool BF16, bool VEC, int kRows>
+template <bool MX, bool BF16, int kRows>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int32_t* starts, void* k, void* v) {
   const int first = (int)(workgroup() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kRows;
   if (first >= c.rows) return;
@@ -191,37 +176,25 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int32_t* 
         float x[8];
         dequant8_f32<MX>(w[i][j], byte[i][j], value ? gv : gk, x);
         if constexpr (BF16) {
-          uint16_t* const p = static_cast<uint16_t*>(value ? v : k) + o;
+          typedef u32x4 any __attribute__((aligned(2)));
           const u32x4 y{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]), bf16_pack2(x[6], x[7])};
-          if constexpr (VEC) {
-            __builtin_nontemporal_store(y, reinterpret_cast<u32x4*>(p));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
-          }
+          __builtin_nontemporal_store(y, reinterpret_cast<any*>(static_cast<uint16_t*>(value ? v : k) + o));
         } else {
-          float* const p = static_cast<float*>(value ? v : k) + o;
-          if constexpr (VEC) {
-            __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4*>(p));
-            __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4*>(p) + 1);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = x[e];
-          }
+          typedef f32x4 any __attribute__((aligned(4)));
+          any* const p = reinterpret_cast<any*>(static_cast<float*>(value ? v : k) + o);
+          __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, p);
+          __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, p + 1);
         }
       }
     }
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// f(MX, BF16, VEC) with the three as compile-time constants.
+// f(MX, BF16) with the two as compile-time constants.
 template <typename F>
-void select3(bool a, bool b, bool c, F f) {
-  auto with = [&](auto x, auto y) { c ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
-  auto next = [&](auto x) { b ? with(x, std::true_type{}) : with(x, std::false_type{}); };
-  a ? next(std::true_type{}) : next(std::false_type{});
+void select2(bool a, bool b, F f) {
+  auto with = [&](auto x) { b ? f(x, std::true_type{}) : f(x, std::false_type{}); };
+  a ? with(std::true_type{}) : with(std::false_type{});
 }
 
 }  // namespace
@@ -230,10 +203,8 @@ namespace fp4impl {
 
 hipError_t launch_kv_write(const KvCache& c, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                            bool bf16, hipStream_t stream) {
-  const int64_t e = bf16 ? 2 : 4;
-  const bool vec = aligned16(k) && aligned16(v) && k_stride * e % 16 == 0 && v_stride * e % 16 == 0;
-  select3(c.mx, bf16, vec, [&](auto mx, auto bf, auto al) {
-    k_kv_write<mx.value, bf.value, al.value><<<grid_of((c.rows + kWaves - 1) / kWaves), kThreads, 0, stream>>>(
+  select2(c.mx, bf16, [&](auto mx, auto bf) {
+    k_kv_write<mx.value, bf.value><<<grid_of((c.rows + kWaves - 1) / kWaves), kThreads, 0, stream>>>(
         c, k, k_stride, v, v_stride);
   });
   return hipGetLastError();
@@ -241,10 +212,10 @@ hipError_t launch_kv_write(const KvCache& c, const void* k, int64_t k_stride, co
 
 hipError_t launch_kv_read(const KvCache& c, const int32_t* starts, void* k, void* v, bool bf16,
                           hipStream_t stream) {
-  select3(c.mx, bf16, aligned16(k) && aligned16(v), [&](auto mx, auto bf, auto al) {
+  select2(c.mx, bf16, [&](auto mx, auto bf) {
     auto go = [&](auto rows) {
       constexpr int kRows = rows.value;
-      k_kv_read<mx.value, bf.value, al.value, kRows>
+      k_kv_read<mx.value, bf.value, kRows>
           <<<grid_of((c.rows + kRows * kWaves - 1) / (kRows * kWaves)), kThreads, 0, stream>>>(c, starts, k, v);
     };
     if (c.rows >= kManyRows) go(std::integral_constant<int, 4>{});
