@@ -103,7 +103,7 @@ UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool s
   UnitPlan p{};
   p.group = q_heads / heads;
   p.rows = tile_rows(T, seqs, p.group);
-  p.min_per = p.rows == 128 ? 8 : 4;
+  p.min_per = 8;
   p.target = std::max(1, resident(p.rows, dp, split) * fp4impl::num_cus() / heads);
   p.rounds = p.rows == 128 ? 4 : 2;
   p.max_slots = (int)(T * p.group / p.rows + seqs);
