@@ -86,23 +86,31 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Packed rows of a tile.
-int tile_rows(int64_t T, int64_t seqs, int group) {
+// Packed rows of a tile, by the mean of the sequences' rows.  16 sequences of 8192 positions, 8 heads, us:
+//   rows per head        16    32    64   128
+//   D 128, bf16: 16      41    60   110   184
+//                32      48    52    80   132
+//               128      87    90    98   114
+//   D 128, f32:  16      46    73   123   230   (32: 73, 78, 125, 235; 128: 121, 122, 134, 165)
+//   D 256, bf16: 16      87   139   259   499   (32: 280, 285, 469, 861; 128: 262, 269, 277, 295)
+// (float32 and 256 channels leave a SIMD one wave of the 32-row kernel).
+int tile_rows(int64_t T, int64_t seqs, int group, int dp, bool split) {
   const int64_t rows = T * group;
-  return rows <= 16 * seqs ? 16 : rows <= 32 * seqs ? 32 : 128;
+  if (rows > 64 * seqs) return 128;
+  return rows <= 16 * seqs || dp == 256 || split ? 16 : 32;
 }
 
 // Workgroups that a compute unit holds, by their registers and LDS (a wave of each on each SIMD).
 int resident(int rows, int dp, bool split) {
   if (rows == 128) return dp == 256 ? 1 : 2;
-  if (rows == 16) return dp == 64 ? (split ? 3 : 4) : dp == 128 ? (split ? 2 : 3) : 1;
-  return dp == 64 ? (split ? 2 : 3) : dp == 128 && !split ? 2 : 1;
+  if (rows == 32) return dp == 64 ? 3 : 2;
+  return dp == 64 ? (split ? 3 : 4) : dp == 128 ? (split ? 2 : 3) : 1;
 }
 
 UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool split) {
   UnitPlan p{};
   p.group = q_heads / heads;
-  p.rows = tile_rows(T, seqs, p.group);
+  p.rows = tile_rows(T, seqs, p.group, dp, split);
   p.min_per = 8;
   p.target = std::max(1, resident(p.rows, dp, split) * fp4impl::num_cus() / heads);
   p.rounds = p.rows == 128 ? 4 : 2;
@@ -123,9 +131,17 @@ int64_t most_units(const KvCache& c, const UnitPlan& p) {
 template <int DP, bool MX, bool QBF, bool SPLIT>
 void launch(const KvCache& c, const AttendProblem& a, const UnitPlan& p, hipStream_t stream) {
   const dim3 grid = fp4impl::grid_of(most_units(c, p) * c.heads);
-  if (p.rows == 16) k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p);
-  else if (p.rows == 32) k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p);
-  else k_attend_tiles<DP, MX, QBF, SPLIT><<<grid, 256, 0, stream>>>(c, a, p);
+  if (p.rows == 16) {
+    k_attend_few<DP, MX, QBF, SPLIT, 1><<<grid, 256, 0, stream>>>(c, a, p);
+    return;
+  }
+  if constexpr (DP < 256 && !SPLIT) {
+    if (p.rows == 32) {
+      k_attend_few<DP, MX, QBF, SPLIT, 2><<<grid, 256, 0, stream>>>(c, a, p);
+      return;
+    }
+  }
+  k_attend_tiles<DP, MX, QBF, SPLIT><<<grid, 256, 0, stream>>>(c, a, p);
 }
 
 template <int DP>

@@ -99,7 +99,7 @@ __device__ __forceinline__ s16x4 read_v4(const uint8_t* p) {
 }
 
 template <int DP, bool MX, bool QBF, bool SPLIT, int R>
-__global__ void __launch_bounds__(256, DP == 256 || (R == 2 && DP == 128 && SPLIT) ? 1 : 2)
+__global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     k_attend_few(KvCache c, AttendProblem a, UnitPlan p) {
   constexpr int kDwords = DP / 32, kGranules = DP / 16;
   __shared__ __align__(16) uint8_t tile[4][32 * DP * 2];
