@@ -109,8 +109,12 @@ __device__ __forceinline__ QueryRow query_row(const Unit& u, const UnitPlan& p, 
   const int pos = u.length - u.n + i;
   q.first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
   q.last = p.causal ? min(pos, t1 - 1) : t1 - 1;
+  if (q.last < q.first) q.first = q.last = 0x7f000000;   // no position is there
   return q;
 }
+
+// Whether a row does not see position t.
+__device__ __forceinline__ bool hidden(const QueryRow& q, int t) { return (uint32_t)(t - q.first) > (uint32_t)(q.last - q.first); }
 
 // Eight consecutive values of a query row.  (Element alignment is enough for 16-byte accesses to global memory.)
 template <bool BF16>

@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int t = t0 + 16 * i + 4 * quad + e;
-            if (t > row[g].last || t < row[g].first || (now.holes >> i & 1)) s[g][i][e] = -INFINITY;
+            const bool hide = hidden(row[g], t0 + 16 * i + 4 * quad + e) | (now.holes >> i & 1);
+            s[g][i][e] = hide ? -INFINITY : s[g][i][e];
           }
       }
       float top = s[g][0][0];

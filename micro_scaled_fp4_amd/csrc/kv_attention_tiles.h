@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int o = 32 * b + 8 * (e >> 2) + 4 * half + (e & 3);
-          if (t0 + o > row.last || t0 + o < row.first || (holes >> (2 * b + (e >> 3)) & 1)) s[b][e] = -INFINITY;
+          const bool hide = hidden(row, t0 + 32 * b + 8 * (e >> 2) + 4 * half + (e & 3)) | (holes >> (2 * b + (e >> 3)) & 1);
+          s[b][e] = hide ? -INFINITY : s[b][e];
         }
     }
     float top = s[0][0];
