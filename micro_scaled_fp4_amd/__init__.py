@@ -828,7 +828,7 @@ class KVCache:
 
 def _call_on(dev: torch.device, fn, *args) -> int:
     """fn(*args, the device's current stream) with dev as the current device."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         return fn(*args, _stream(dev))
     with torch.cuda.device(dev):
         return fn(*args, _stream(dev))
@@ -836,26 +836,30 @@ def _call_on(dev: torch.device, fn, *args) -> int:
 
 def _sequences(cache: KVCache, offsets: torch.Tensor, lengths: torch.Tensor, pages: torch.Tensor):
     """(B, offsets, lengths, pages, max_pages) of a cache call, checked."""
-    B = lengths.numel()
-    if pages.dim() != 2:
-        raise ValueError("pages must be [B, max_pages]")
-    if offsets.device != cache.device or lengths.device != cache.device or pages.device != cache.device:
-        raise ValueError(f"offsets, lengths and pages must be on {cache.device}")
-    offsets = _typed(offsets, torch.int32, (B + 1,), "offsets")
-    lengths = _typed(lengths, torch.int32, (B,), "lengths")
-    pages = _typed(pages, torch.int32, (B, pages.shape[1]), "pages")
-    return B, offsets, lengths, pages, pages.shape[1]
+    B, shape, dev = lengths.numel(), pages.shape, cache.device
+    if len(shape) != 2 or shape[0] != B or lengths.dim() != 1 or offsets.shape != (B + 1,):
+        raise ValueError("offsets, lengths and pages must be [B + 1], [B] and [B, max_pages], not "
+                         f"{tuple(offsets.shape)}, {tuple(lengths.shape)} and {tuple(shape)}")
+    for t in (offsets, lengths, pages):
+        if t.dtype != torch.int32:
+            raise TypeError("offsets, lengths and pages must be torch.int32")
+        if t.device != dev:
+            raise ValueError(f"offsets, lengths and pages must be on {dev}")
+    return B, offsets.contiguous(), lengths.contiguous(), pages.contiguous(), shape[1]
 
 
 def _head_rows(t: torch.Tensor, heads: Optional[int], dim: int, dev, name: str):
     """t [T, heads, dim] with contiguous heads (copied where they are not) and its token stride."""
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [T, {heads or 'num_q_heads'}, {dim}], not {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {heads or 'num_q_heads'}, {dim}], not {tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+    token, head, channel = t.stride()
+    if channel != 1 or (head != dim and shape[1] > 1):
         t = t.contiguous()
-    return t, t.stride(0)
+        token = t.stride(0)
+    return t, token
 
 
 def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
@@ -919,8 +923,11 @@ def kv_cache_attention(cache: KVCache, q: torch.Tensor, offsets: torch.Tensor, l
         raise ValueError(f"out must be contiguous {tuple(q.shape)} on {dev}")
     lse = torch.empty(T, heads, dtype=torch.float32, device=dev) if return_lse else None
     lib = load_library()
-    need = lib.kv_cache_attention_workspace_bytes(cache._address, T, B, heads)
-    workspace = _workspace(workspace, need, dev)
+    if workspace is None:
+        need = lib.kv_cache_attention_workspace_bytes(cache._address, T, B, heads)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
     _check(_call_on(dev, lib.kv_cache_attention, cache._address, _ptr(q), qs, _dtype_code(q.dtype), T, heads, B,
                     _ptr(offsets), _ptr(lengths), _ptr(pages), wide,
                     cache.head_dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window),

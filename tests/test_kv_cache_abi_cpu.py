@@ -108,3 +108,29 @@ def test_binding_refuses_host_tensors():
         m.KVCache(7, z, s, z, s)
     with pytest.raises(ValueError):
         m.KVCache(m.FP4_MXFP4, z[0], s, z, s)
+
+
+def test_binding_checks_before_the_library():
+    """Shapes and types of the sequences' tensors and of rows (host tensors standing in: the first check that
+    looks at the device comes after them)."""
+    class Stub:
+        device, num_heads, head_dim = torch.device("cpu"), 2, 64
+
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    assert m._sequences(Stub, i(4), i(3), i(3, 5))[0::4] == (3, 5)
+    for bad in ((i(3), i(3), i(3, 5)), (i(4), i(3), i(2, 5)), (i(4), i(3), i(15)), (i(4), i(3, 1), i(3, 5)), (i(4, 1), i(3), i(3, 5))):
+        with pytest.raises(ValueError):
+            m._sequences(Stub, *bad)
+    for bad in ((i(4).long(), i(3), i(3, 5)), (i(4), i(3).float(), i(3, 5)), (i(4), i(3), i(3, 5).to(torch.int16))):
+        with pytest.raises(TypeError):
+            m._sequences(Stub, *bad)
+    rows = torch.zeros(5, 9, 64)
+    t, stride = m._head_rows(rows[:, 2:4], 2, 64, Stub.device, "k")
+    assert t.data_ptr() == rows[:, 2:4].data_ptr() and stride == 9 * 64
+    t, stride = m._head_rows(torch.zeros(2, 5, 64).transpose(0, 1), 2, 64, Stub.device, "k")
+    assert t.is_contiguous() and stride == 128
+    t, stride = m._head_rows(torch.zeros(1, 2, 64).expand(5, 2, 64), 2, 64, Stub.device, "k")
+    assert stride == 0
+    for bad in (torch.zeros(5, 128), torch.zeros(5, 3, 64), torch.zeros(5, 2, 32)):
+        with pytest.raises(ValueError):
+            m._head_rows(bad, 2, 64, Stub.device, "k")
