@@ -190,8 +190,18 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   const int v_at0 = v_address<DP>(4 * quad);
 
   for (; t0 < sp.t1; t0 += 256) {
-    const RawStep<DP> now = next;
+    RawStep<DP> now = next;
     if (t0 + 256 < sp.t1) load(t0 + 256);
+    if (t0 < sp.lo) {
+      // what no row sees may be anything, a NaN or the largest scale too: scale bytes of 0 make it 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < RawStep<DP>::kScales; ++j) {
+          now.ks[i][j] = t0 + 16 * i + r16 < sp.lo ? 0 : now.ks[i][j];
+          now.vs[i][j] = t0 + 16 * i + (lane >> 2) < sp.lo ? 0 : now.vs[i][j];
+        }
+    }
     int k_ref = 0, v_top = 0;
     if constexpr (MX) {
 #pragma unroll

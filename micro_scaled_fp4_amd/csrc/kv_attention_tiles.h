@@ -53,10 +53,14 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     if (page < 0) n = page = 0;
     const int64_t row = cache_row(c, page, head, t);
     const int codes = n * code_row, scales = n * scale_row;
+    // what no row sees may be anything, a NaN or the largest scale too: scale bytes of 0 make it 0
+    QuarterRow<DP, MX> seen = at;
+#pragma unroll
+    for (int j = 0; j < kScales; ++j) seen.scale[j] = t + (lane >> 2) < sp.lo ? kOutOfRange : at.scale[j];
     holes = holes >> 4 | walk.holes_at(ahead) << 8;   // (past the last position: masked anyway)
-    load_quarter<DP, MX>(uniform_rsrc(c.k_codes + row * code_row, codes), uniform_rsrc(c.k_scales + row * scale_row, scales), at,
+    load_quarter<DP, MX>(uniform_rsrc(c.k_codes + row * code_row, codes), uniform_rsrc(c.k_scales + row * scale_row, scales), seen,
                          raw.kw, raw.ks);
-    load_quarter<DP, MX>(uniform_rsrc(c.v_codes + row * code_row, codes), uniform_rsrc(c.v_scales + row * scale_row, scales), at,
+    load_quarter<DP, MX>(uniform_rsrc(c.v_codes + row * code_row, codes), uniform_rsrc(c.v_scales + row * scale_row, scales), seen,
                          raw.vw, raw.vs);
     ahead += 64;
   };

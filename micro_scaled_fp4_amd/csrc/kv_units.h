@@ -256,19 +256,20 @@ struct PageWalk {
   }
 };
 
-// Positions of a unit: [t0, t1), t0 a multiple of 64 (positions before `lo` are masked).
+// Positions of a unit: [t0, t1), t0 a multiple of 64 unless the unit is empty.  Positions before lo
+// are seen by no row of the tile.
 struct Span {
-  int t0, t1;
+  int t0, t1, lo;
 };
 
 __device__ __forceinline__ Span span_of(const UnitPlan& p, const Unit& u, int rows) {
   const int first = u.length - u.n + u.tile * p.rows / p.group;
   const int last = u.length - u.n + (u.tile * p.rows + rows - 1) / p.group;
-  const int hi = p.causal ? min(u.length, last + 1) : u.length;
+  const int hi = p.causal ? max(0, min(u.length, last + 1)) : u.length;   // (rows may sit before position 0)
   const int lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
   const int64_t t0 = (lo & ~63) + (int64_t)u.part * u.per * 64;
   const int64_t t1 = u.part == u.count - 1 ? hi : min((int64_t)hi, t0 + (int64_t)u.per * 64);
-  return {(int)min(t0, (int64_t)hi), (int)t1};
+  return {(int)min(t0, (int64_t)hi), (int)t1, lo};
 }
 
 }  // namespace fp4dev

@@ -176,3 +176,41 @@ def test_many_sequences():
     case = ref.Case(ref.MX, 1, 32, 16, seqs, seed=82, spare_rows=5)
     q, q64 = queries(case, 2, torch.bfloat16)
     check(case, case.full_store(), q, q64)
+
+
+@pytest.mark.parametrize("fmt", [ref.NV, ref.MX])
+@pytest.mark.parametrize("seqs", [[(400, 1), (170, 1)], [(300, 4), (65, 3)], [(500, 130), (90, 90)]], ids=["decode", "drafts", "prompts"])
+def test_positions_before_every_window_may_hold_anything(fmt, seqs):
+    """A window has left pages behind whose table entries still stand: their bytes are NaN and the largest scales."""
+    announce(f"kv attention garbage before the window fmt {fmt} {seqs}")
+    for D, page, window in ((128, 16, 20), (64, 64, 33), (256, 16, 64)):
+        case = ref.Case(fmt, 2, D, page, seqs, seed=window)
+        store = case.full_store()
+        for junk in (0xff, 0x7f, 0xfe):
+            mine = [t.copy() for t in store]
+            for b, (length, n) in enumerate(seqs):
+                for t in range(max(0, length - n - window + 1)):
+                    for a in mine:
+                        a[case.pages[b, t // page], :, t % page] = junk
+            for dtype in (torch.bfloat16, torch.float32):
+                q, q64 = queries(case, 4, dtype)
+                got = fp4.kv_cache_attention(gpu_cache(case, mine), q, *tables(case), window=window)
+                want = fp4.kv_cache_attention(gpu_cache(case, store), q, *tables(case), window=window)
+                assert torch.equal(got, want)
+        check(case, store, q, q64, window=window)
+
+
+@pytest.mark.parametrize("fmt", [ref.NV, ref.MX])
+def test_far_more_rows_than_positions(fmt):
+    """Whole row tiles before position 0, in the first sequence and a later one."""
+    announce(f"kv attention rows before position 0 fmt {fmt}")
+    case = ref.Case(fmt, 1, 64, 16, [(20, 300), (0, 200), (33, 1), (5, 140)], seed=9)
+    store = case.full_store()
+    for dtype in (torch.bfloat16, torch.float32):
+        q, q64 = queries(case, 2, dtype)
+        check(case, store, q, q64)
+        check(case, store, q, q64, window=4)
+    # and on the kernels for few rows
+    case = ref.Case(fmt, 1, 64, 16, [(2, 30)] + [(40, 1)] * 9, seed=10)
+    q, q64 = queries(case, 4, torch.bfloat16)
+    check(case, case.full_store(), q, q64)
