@@ -7,6 +7,14 @@
 // LDS as fp16, 32 positions at a time, private to the wave, and come back transposed
 // (ds_read_b64_tr_b16), four positions of one channel to a lane.  The next step's bytes are
 // loaded while this one is computed.
+//
+// Bound by HBM bytes where contexts are long: 1000000 positions, 8 heads x 128, 4 query heads
+// each: 228 us NVFP4, 216 us MXFP4 with the join of the parts (5.06 and 5.05 TB/s), 64 sequences of
+// 16384: 252 us (4.8 TB/s).  R = 2 is bound by vector instructions, half of them for its two
+// softmaxes: 80 packed rows of 8 heads x 128 over 16 sequences of 5750 positions 36 us (2.7 TB/s).
+// Short contexts pay the chain of a part: 2.6 us until its unit is known, 1.9 the first loads, 2.0 a
+// step, 0.8 the join of the waves (1000 positions: 11 us in all).  Unrolling over two steps
+// needs more registers than two waves a SIMD leave (32 sequences, 51 -> 61 us).
 #pragma once
 
 #include "kv_attention.h"

@@ -4,6 +4,15 @@
 // positions is dequantized once for the workgroup into LDS as fp16 (wave w: positions 16 w ..
 // 16 w + 15), into two buffers in turn: step n + 1's while step n is computed; one barrier ends a
 // step.  Codes are loaded two steps ahead.
+//
+// Bound by the matrix and the vector instructions together: of a step at 128 channels a wave
+// issues 32 MFMAs (about 1040 cycles) and 265 vector instructions (about 1300: half for the
+// softmax, a quarter for its share of the dequantizing), and the two waves of a SIMD hardly overlap
+// them (the cycles of both add up to 98% of the time).  A causal prompt of 16384, 32 / 8 heads x
+// 128: 2230 us NVFP4 (985 TFLOP/s), 2200 us MXFP4 (1000); 64 channels 693, 256 channels 571 TFLOP/s
+// (sums and q fill 192 registers: one wave a SIMD).  At the same prompt, 64 rows a wave at one wave a
+// SIMD reached 722 TFLOP/s, eight waves over 256 rows 970, the next step's scores beside this
+// step's weights 930, raised wave priorities 2% less.
 #pragma once
 
 #include <type_traits>

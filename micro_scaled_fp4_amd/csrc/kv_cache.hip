@@ -5,9 +5,13 @@
 // page once, then its lanes take the row's values in order.
 //   Write: a lane quantizes 16 values, an NVFP4 block; two lanes share an MXFP4 block and
 //   its maximum.  The steps are those of nvfp4_quantize and mxfp4_quantize, bit for bit.
-//   Read: a lane dequantizes 8 values (one dword of codes) and stores 16 bytes of bf16.
+//   Read: a lane dequantizes 8 values (one dword of codes) and stores 16 bytes of bf16, past
+//   the caches: what is read back is larger than they are.
 // Both are bound by HBM bytes (a row of 8 heads x 128 bf16 channels moves 4096 bytes one
-// way and 1152 the other).
+// way and 1152 or 1088 the other).  Measured at that row: written, 32 rows 4.3 us (the chain of
+// loads that finds a row's page), 16384 rows 18.5 us (4.6 TB/s); read, 32 rows 4.0 us, 4096 rows
+// 7.0, 16384 rows 15 and 65536 rows 54 (6.3 TB/s).  Four rows a wave read no faster (8.1 us at
+// 1024 rows, 54 at 65536).
 #include <type_traits>
 
 #include "fp4_device.h"
@@ -22,9 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-// From here on a wave reads four rows: 4096 waves fill the card, and a row's look-up of its sequence
-// and page is a chain of loads.
-constexpr int kManyRows = 16384;
 
 // Sixteen consecutive values from x + i.  (Element alignment is enough for 16-byte accesses to global memory.)
 template <bool BF16>
@@ -110,81 +111,55 @@ __device__ __forceinline__ void dequant8_f32(uint32_t codes, uint32_t byte, floa
   }
 }
 
-// A wave's next row: output row r at position t (page < 0: zeros).
-struct ReadRow {
-  int page, t;
-};
-
-// The wave reads kRows rows; a lane takes units of 8 values (keys first, then values) of all of them.
-template <bool MX, bool BF16, int kRows>
+// A lane takes units of 8 values of the wave's row, keys first, then values; kUnits at a time, so that
+// their loads are on their way together.
+template <bool MX, bool BF16>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvCache c, const int32_t* starts, void* k, void* v) {
-  const int first = (int)(workgroup() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kRows;
-  if (first >= c.rows) return;
+  const int r = (int)(workgroup() * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  if (r >= c.rows) return;
+  const int b = seq_of_row(c, r);
+  if (b < 0) return;
+  const int begin = seq_begin(c, b), end = seq_end(c, b, begin);
+  if (r >= end) return;
+  const int length = seq_length(c, b);
+  const int64_t at = (int64_t)(starts != nullptr ? starts[b] : length - (end - begin)) + (r - begin);
+  const int t = at >= 0 && at < length ? (int)at : 0;
+  const int page = at >= 0 && at < length ? page_of(c, b, t) : -1;     // (-1: zeros)
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
-  ReadRow rows[kRows];
-  int b = -1, begin = 0, end = 0, length = 0, start = 0;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = first + i;
-    rows[i] = {-1, -1};
-    if (r >= c.rows) continue;
-    if (i == 0 || r >= end) {                   // the next sequence
-      b = seq_of_row(c, r);
-      if (b < 0) continue;
-      begin = seq_begin(c, b);
-      end = seq_end(c, b, begin);
-      length = seq_length(c, b);
-      start = starts != nullptr ? starts[b] : length - (end - begin);
-    }
-    if (r >= end) continue;
-    const int64_t t = (int64_t)start + (r - begin);
-    rows[i] = {t >= 0 && t < length ? page_of(c, b, (int)t) : -1, (int)(t >= 0 && t < length ? t : 0)};
-  }
   const int lane = threadIdx.x & 63, units = c.heads * c.dim >> 3, per_head = c.dim >> 3;
   constexpr int kShift = MX ? 2 : 1;            // units of a scale
-  constexpr int kUnits = kRows == 1 ? 4 : 2;    // of a lane at a time, for each row
+  constexpr int kUnits = 4;
   for (int u0 = 0; u0 < 2 * units; u0 += 64 * kUnits) {
-    int head[kUnits], part[kUnits];
-    uint32_t w[kRows][kUnits], byte[kRows][kUnits];
+    uint32_t w[kUnits], byte[kUnits];
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) {
       const int u = u0 + 64 * j + lane;
       const bool value = u >= units;
-      const int x = value ? u - units : u;
-      head[j] = x / per_head;
-      part[j] = x - head[j] * per_head;
-      const uint32_t* const codes = reinterpret_cast<const uint32_t*>(value ? c.v_codes : c.k_codes) + part[j];
-      const uint8_t* const scales = (value ? c.v_scales : c.k_scales) + (part[j] >> kShift);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        w[i][j] = byte[i][j] = 0;
-        if (u < 2 * units && rows[i].page >= 0) {
-          const int64_t row = cache_row(c, rows[i].page, head[j], rows[i].t);
-          w[i][j] = codes[row * per_head];
-          byte[i][j] = scales[row * (per_head >> kShift)];
-        }
+      const int x = value ? u - units : u, head = x / per_head, part = x - head * per_head;
+      w[j] = byte[j] = 0;
+      if (u < 2 * units && page >= 0) {
+        const int64_t row = cache_row(c, page, head, t);
+        w[j] = reinterpret_cast<const uint32_t*>(value ? c.v_codes : c.k_codes)[row * per_head + part];
+        byte[j] = (value ? c.v_scales : c.k_scales)[row * (per_head >> kShift) + (part >> kShift)];
       }
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int u = u0 + 64 * j + lane;
-        if (u >= 2 * units || rows[i].t < 0) continue;   // (t < 0: no sequence's row)
-        const bool value = u >= units;
-        const int64_t o = (int64_t)(first + i) * c.heads * c.dim + (value ? u - units : u) * 8;
-        float x[8];
-        dequant8_f32<MX>(w[i][j], byte[i][j], value ? gv : gk, x);
-        if constexpr (BF16) {
-          typedef u32x4 any __attribute__((aligned(2)));
-          const u32x4 y{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]), bf16_pack2(x[6], x[7])};
-          __builtin_nontemporal_store(y, reinterpret_cast<any*>(static_cast<uint16_t*>(value ? v : k) + o));
-        } else {
-          typedef f32x4 any __attribute__((aligned(4)));
-          any* const p = reinterpret_cast<any*>(static_cast<float*>(value ? v : k) + o);
-          __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, p);
-          __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, p + 1);
-        }
+    for (int j = 0; j < kUnits; ++j) {
+      const int u = u0 + 64 * j + lane;
+      if (u >= 2 * units) continue;
+      const bool value = u >= units;
+      const int64_t o = (int64_t)r * c.heads * c.dim + (value ? u - units : u) * 8;
+      float x[8];
+      dequant8_f32<MX>(w[j], byte[j], value ? gv : gk, x);
+      if constexpr (BF16) {
+        typedef u32x4 any __attribute__((aligned(2)));
+        const u32x4 y{bf16_pack2(x[0], x[1]), bf16_pack2(x[2], x[3]), bf16_pack2(x[4], x[5]), bf16_pack2(x[6], x[7])};
+        __builtin_nontemporal_store(y, reinterpret_cast<any*>(static_cast<uint16_t*>(value ? v : k) + o));
+      } else {
+        typedef f32x4 any __attribute__((aligned(4)));
+        any* const p = reinterpret_cast<any*>(static_cast<float*>(value ? v : k) + o);
+        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, p);
+        __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, p + 1);
       }
     }
   }
@@ -213,13 +188,7 @@ hipError_t launch_kv_write(const KvCache& c, const void* k, int64_t k_stride, co
 hipError_t launch_kv_read(const KvCache& c, const int32_t* starts, void* k, void* v, bool bf16,
                           hipStream_t stream) {
   select2(c.mx, bf16, [&](auto mx, auto bf) {
-    auto go = [&](auto rows) {
-      constexpr int kRows = rows.value;
-      k_kv_read<mx.value, bf.value, kRows>
-          <<<grid_of((c.rows + kRows * kWaves - 1) / (kRows * kWaves)), kThreads, 0, stream>>>(c, starts, k, v);
-    };
-    if (c.rows >= kManyRows) go(std::integral_constant<int, 4>{});
-    else go(std::integral_constant<int, 1>{});
+    k_kv_read<mx.value, bf.value><<<grid_of((c.rows + kWaves - 1) / kWaves), kThreads, 0, stream>>>(c, starts, k, v);
   });
   return hipGetLastError();
 }

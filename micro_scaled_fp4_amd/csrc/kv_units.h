@@ -4,8 +4,8 @@
 // The query rows of a sequence and key/value head are packed as rho = row * group + (query
 // head within the group), so that all heads of a group share what is read; kRows of them make a
 // row tile.  A tile's positions are cut into parts of `per` steps (of 64 positions), `per`
-// being the same for all sequences: the total of all tiles' steps over the number of parts that
-// fill the card.  So long sequences are cut into many parts and short ones into one, whatever
+// being the same for all sequences: the length that makes whole rounds of resident workgroups
+// fastest (unit_of).  So long sequences are cut into many parts and short ones into one, whatever
 // the batch holds, and the host needs to know no length.  A tile of one part writes its output;
 // the parts of a cut one leave theirs in the workspace, and k_join_parts joins them.
 #pragma once
@@ -23,7 +23,7 @@ struct UnitPlan {
   int group;
   int min_per;                   // least steps of a part
   int target;                    // parts per key/value head that fill the card
-  int rounds;                    // at most that many such rounds are looked at
+  int rounds;                    // at most that many rounds of such parts are looked at
   int max_slots, max_parts;      // most tiles, and most parts of cut tiles (per head)
   bool causal;
   int window;
@@ -40,8 +40,6 @@ struct TileParts {
 // Units past the tiles and parts that the layout can give (the total of the steps is a sum of
 // float32 values).
 constexpr int kSpareUnits = 8;
-// The most workgroups on a compute unit that any of the kernels reaches.
-constexpr int kMostResident = 4;
 
 }  // namespace fp4impl
 
