@@ -139,6 +139,9 @@ __device__ __forceinline__ void row_factors(float top, float& f, float& inverse)
   inverse = __uint_as_float((uint32_t)(e - 14) << 23);
 }
 
+// A row's factor c, kept from 0 and infinity, whose products with -inf (a masked position) and 0 are NaN.
+__device__ __forceinline__ float in_range(float c) { return fminf(fmaxf(c, 1e-37f), 3e38f); }
+
 // Two fp16 parts of eight float32 values (hi + lo, 22 bits); lo is left out where !SPLIT.
 template <bool SPLIT>
 __device__ __forceinline__ void to_f16(const float (&v)[8], f16x8& hi, f16x8& lo) {

@@ -87,6 +87,74 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
   }
 }
 
+// Lays more than kLaneSeqs sequences out, for unit_of: one workgroup, each thread a run of them.  Bound by
+// its launch and chains of loads; with it one token each of 65, 128, 256, 512 and 4096 sequences of 1000
+// positions (8 heads x 128) takes 39, 49, 80, 151 and 1027 us, laid out by every wave for itself 34, 48,
+// 88, 208 and 5704.
+constexpr int kLayOutThreads = 1024, kLayOutWaves = kLayOutThreads / 64;
+__global__ void __launch_bounds__(kLayOutThreads) k_lay_out(KvCache c, UnitPlan p) {
+  __shared__ float sums[kLayOutWaves];
+  __shared__ int scans[3][kLayOutWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int run = (c.seqs + kLayOutThreads - 1) / kLayOutThreads;
+  const int b0 = min((int)threadIdx.x * run, c.seqs), b1 = min(b0 + run, c.seqs);
+  const SeqSize mine = b0 < b1 ? seq_size(c, p, b0) : SeqSize{0, 0, 0, 0, 1};
+  auto each = [&](auto f) {
+    if (b0 < b1) f(b0, mine);
+    for (int b = b0 + 1; b < b1; ++b) f(b, seq_size(c, p, b));
+  };
+  // over all threads, the same in all
+  auto joined = [&](float v, auto f) {
+    __syncthreads();
+    if (lane == 0) sums[wave] = v;
+    __syncthreads();
+    float r = sums[0];
+    for (int w = 1; w < kLayOutWaves; ++w) r = f(r, sums[w]);
+    return r;
+  };
+  auto sum = [&](float v) { return joined(sum_lanes(v), [](float x, float y) { return x + y; }); };
+  Totals all{0, 0, 0};
+  each([&](int, const SeqSize& s) {
+    all.work += (float)s.tiles * (float)s.steps;
+    all.tiles += (float)s.tiles;
+    all.longest = fmaxf(all.longest, s.tiles > 0 ? (float)s.steps : 0.0f);
+  });
+  all = {sum(all.work), sum(all.tiles), joined(max_lanes(all.longest), [](float x, float y) { return fmaxf(x, y); })};
+  if (!fits(p, all)) {
+    if (threadIdx.x == 0) p.layout[c.seqs] = {0, 0, fp4impl::kNoLayout, 1};
+    return;
+  }
+  const int per = part_steps(p, all, [&](float inverse) {
+    float units = 0;
+    each([&](int, const SeqSize& s) { units += (float)s.tiles * ceilf((float)s.steps * inverse); });
+    return sum(units);
+  });
+  int own[3] = {0, 0, 0}, to[3];
+  auto add = [&](const SeqSize& s) {
+    const int count = parts_of(s.steps, per);
+    own[0] += s.tiles * count;
+    own[1] += count > 1 ? s.tiles * count : 0;
+    own[2] += s.tiles;
+  };
+  each([&](int, const SeqSize& s) { add(s); });
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    to[i] = scan_lanes(own[i]);
+    if (lane == 63) scans[i][wave] = to[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    for (int w = 0; w < wave; ++w) to[i] += scans[i][w];
+    own[i] = to[i] - own[i];                    // before this thread's first
+  }
+  if (threadIdx.x == kLayOutThreads - 1) p.layout[c.seqs] = {to[0], to[1], to[2], per};
+  each([&](int b, const SeqSize& s) {
+    p.layout[b] = {own[0], own[1], own[2], 0};
+    add(s);
+  });
+}
+
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Packed rows of a tile, by the mean of the sequences' rows.  16 sequences of 8192 positions, 8 heads, us:
@@ -129,6 +197,8 @@ UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool s
 }
 
 size_t tiles_bytes(const UnitPlan& p) { return (size_t)(p.max_slots + 1) * sizeof(TileParts); }
+
+size_t layout_bytes(int64_t seqs) { return seqs > fp4impl::kLaneSeqs ? (size_t)(seqs + 1) * sizeof(int4) : 0; }
 
 // The most parts of a tile that the page table has positions for, and units of a head.
 int64_t most_parts(const KvCache& c, const UnitPlan& p) { return std::max((c.capacity / 64 + p.min_per) / p.min_per, 1); }
@@ -178,7 +248,7 @@ size_t kv_attention_workspace_bytes(int64_t T, int64_t seqs, int q_heads, int he
   size_t most = 0;
   for (bool split : {false, true}) {
     const UnitPlan p = plan_of(T, seqs, q_heads, heads, dp, split);
-    most = std::max(most, tiles_bytes(p) + (size_t)p.max_parts * heads * p.rows * (dp + 2) * 4);
+    most = std::max(most, tiles_bytes(p) + layout_bytes(seqs) + (size_t)p.max_parts * heads * p.rows * (dp + 2) * 4);
   }
   return most;
 }
@@ -189,7 +259,13 @@ hipError_t launch_kv_attention(const KvCache& c, const AttendProblem& a, hipStre
   p.causal = a.causal;
   p.window = a.window;
   p.tiles = a.workspace;
-  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + tiles_bytes(p));
+  p.layout = reinterpret_cast<int4*>(static_cast<char*>(a.workspace) + tiles_bytes(p));
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + tiles_bytes(p) + layout_bytes(c.seqs));
+  if (c.seqs > kLaneSeqs) {
+    k_lay_out<<<1, kLayOutThreads, 0, stream>>>(c, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (dp == 64) launch_dp<64>(c, a, p, stream);
   else if (dp == 128) launch_dp<128>(c, a, p, stream);
   else launch_dp<256>(c, a, p, stream);

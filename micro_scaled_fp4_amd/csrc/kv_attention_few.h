@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     }
     float f, inverse;
     row_factors(max_over_halves(max_over_rows(__uint_as_float(top))), f, inverse);
-    factor[g] = fmaxf(fabsf(a.scale) * kLog2e * inverse * gk, 1e-37f);
+    factor[g] = in_range(fabsf(a.scale) * kLog2e * inverse * gk);
     if (a.scale < 0) f = -f;
 #pragma unroll
     for (int i = 0; i < kDwords; ++i) {
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     f16x8 ph[R][2], pl[R][SPLIT ? 2 : 1];
 #pragma unroll
     for (int g = 0; g < R; ++g) {
-      const float cf = MX ? fmaxf(__builtin_amdgcn_ldexpf(factor[g], k_ref - 140), 1e-37f) : factor[g];
+      const float cf = MX ? in_range(__builtin_amdgcn_ldexpf(factor[g], k_ref - 140)) : factor[g];
       if (now.holes != 0 || __any(t0 + 63 > row[g].last || t0 < row[g].first)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     }
     float f, inverse;
     row_factors(max_over_halves(__uint_as_float(top)), f, inverse);
-    factor = fmaxf(fabsf(a.scale) * kLog2e * inverse * gk, 1e-37f);
+    factor = in_range(fabsf(a.scale) * kLog2e * inverse * gk);
     if (a.scale < 0) f = -f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     take_tops(round - 1);
     f32x16 s[2];
     scores(k_now, s);
-    const float cf = MX ? fmaxf(__builtin_amdgcn_ldexpf(factor, k_ref - 140), 1e-37f) : factor;
+    const float cf = MX ? in_range(__builtin_amdgcn_ldexpf(factor, k_ref - 140)) : factor;
     if ((holes & 15u) != 0 || __any(t0 + 63 > row.last || t0 < row.first)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)

@@ -29,21 +29,26 @@ __device__ __forceinline__ int64_t cache_row(const fp4impl::KvCache& c, int page
   return (((int64_t)page * c.heads + head) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
 }
 
-// The sequence of row r (the same in all 64 lanes, which all call): the last b with
-// offsets[b] <= r, or -1.  64 probes a round, so one round up to 64 sequences.
-__device__ __forceinline__ int seq_of_row(const fp4impl::KvCache& c, int r) {
+// The last i < n with at(i) <= x for ascending at(i), or -1; the same in all 64 lanes, which all
+// call.  64 probes a round, so one round up to 64.
+template <typename At>
+__device__ __forceinline__ int last_at_most(int n, int x, At at) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, n = c.seqs;
+  int lo = 0;
   while (true) {
     const int step = (n + 63) >> 6;
-    const int i = lo + lane * step;
-    const bool at = lane * step < n && c.offsets[i] <= r;
-    const int hits = __popcll(__ballot(at));
+    const bool reached = lane * step < n && at(lo + lane * step) <= x;
+    const int hits = __popcll(__ballot(reached));
     if (hits == 0) return -1;
     lo += (hits - 1) * step;
     n = min(step, n - (hits - 1) * step);
     if (step == 1) return lo;
   }
+}
+
+// The sequence of row r: the last b with offsets[b] <= r, or -1.
+__device__ __forceinline__ int seq_of_row(const fp4impl::KvCache& c, int r) {
+  return last_at_most(c.seqs, r, [&](int b) { return c.offsets[b]; });
 }
 
 }  // namespace fp4dev

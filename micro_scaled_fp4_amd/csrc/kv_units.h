@@ -8,6 +8,9 @@
 // fastest (unit_of).  So long sequences are cut into many parts and short ones into one, whatever
 // the batch holds, and the host needs to know no length.  A tile of one part writes its output;
 // the parts of a cut one leave theirs in the workspace, and k_join_parts joins them.
+//
+// Up to 64 sequences every wave lays them out by itself, a lane for each (part of the 2.6 us until a
+// unit is known, and no launch); more are laid out once, by k_lay_out, and a wave searches that.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,8 +30,10 @@ struct UnitPlan {
   int max_slots, max_parts;      // most tiles, and most parts of cut tiles (per head)
   bool causal;
   int window;
-  // workspace: per tile (slot) a TileParts, then the parts' results
+  // workspace: per tile (slot) a TileParts, then the layout of more than kLaneSeqs sequences, then
+  // the parts' results
   void* tiles;
+  int4* layout;                  // [seqs + 1]: units, parts of cut tiles and tiles before each; the last: of all, and `per`
   float* parts;
 };
 
@@ -40,6 +45,10 @@ struct TileParts {
 // Units past the tiles and parts that the layout can give (the total of the steps is a sum of
 // float32 values).
 constexpr int kSpareUnits = 8;
+// Sequences that a wave lays out by itself.
+constexpr int kLaneSeqs = 64;
+// `slots` where offsets decrease and give more tiles than there are rows: nothing is done then.
+constexpr int kNoLayout = 0x7fffffff;
 
 }  // namespace fp4impl
 
@@ -111,103 +120,98 @@ __device__ __forceinline__ SeqSize seq_size(const KvCache& c, const UnitPlan& p,
   return s;
 }
 
-// Unit u of this head, for one wave (all 64 lanes call; the result is the same in all).  Each
-// lane takes a run of sequences; sums and scans over the lanes give the totals and u's lane.
-__device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int u) {
-  const int lane = threadIdx.x & 63, run = (c.seqs + 63) >> 6;
-  const int b0 = min(lane * run, c.seqs), b1 = min(b0 + run, c.seqs);
-  // (up to 64 sequences: one a lane, read once)
-  const SeqSize mine = b0 < b1 ? seq_size(c, p, b0) : SeqSize{0, 0, 0, 0, 1};
-  auto each = [&](auto f) {
-    f(mine);
-    for (int b = b0 + 1; b < b1; ++b) f(seq_size(c, p, b));
-  };
-  float work = 0, all = 0, longest = 0;         // steps of all tiles, tiles, the most steps of one
-  each([&](const SeqSize& s) {
-    work += (float)s.tiles * (float)s.steps;
-    all += (float)s.tiles;
-    longest = fmaxf(longest, s.tiles > 0 ? (float)s.steps : 0.0f);
-  });
-  work = sum_lanes(work);
-  all = sum_lanes(all);
-  Unit r{};
-  // offsets that decrease can give more tiles than there are rows: nothing is done then
-  r.slots = 0x7fffffff;
-  if (!(all <= 1.01f * (float)p.max_slots)) return r;
+// The sequences' totals: steps of all tiles, tiles, and the most steps of a tile.
+struct Totals {
+  float work, tiles, longest;
+};
+
+// Whether the layout of so many tiles holds (false: offsets decrease).
+__device__ __forceinline__ bool fits(const UnitPlan& p, const Totals& all) { return all.tiles <= 1.01f * (float)p.max_slots; }
+
+// Steps of a part.  Parts of the same length run in rounds of `target`: the shortest length that
+// needs no more than k rounds, for the k with the least time (kStart steps for a part's beginning and
+// end).  units_at(inverse): all units of parts of 1 / inverse steps.
+template <typename UnitsAt>
+__device__ __forceinline__ int part_steps(const UnitPlan& p, const Totals& all, UnitsAt units_at) {
+  constexpr float kStart = 4;
   const float target = (float)p.target;
-  r.per = max(p.min_per, (int)fminf(ceilf(work / target), 1.0e9f));
-  if (all < p.rounds * target && work > 0) {
-    // Parts of the same length run in rounds of `target`: the shortest length that needs no more
-    // than k rounds, for the k with the least time (kStart steps for a part's beginning and end).
-    constexpr float kStart = 4;
-    longest = max_lanes(longest);
-    float best = INFINITY;
-    for (int k = 1; k <= p.rounds; ++k) {
-      const float room = k * target;
-      if (all > room) continue;
-      const float least = fmaxf(ceilf(work / room), (float)p.min_per);
-      float lo = least, hi = fmaxf(lo, all < room ? fminf(longest, ceilf(work / (room - all))) : longest);
-      for (int i = 0; i < 6 && lo < hi; ++i) {
-        const float mid = floorf(0.5f * (lo + hi)), inverse = (1.0f + 0x1p-21f) / mid;   // never too few
-        float units = 0;
-        each([&](const SeqSize& s) { units += (float)s.tiles * ceilf((float)s.steps * inverse); });
-        if (sum_lanes(units) <= room) hi = mid;
-        else lo = mid + 1;
-      }
-      const float time = k * (hi + kStart);
-      if (time < best) {
-        best = time;
-        r.per = (int)hi;
-      }
-      if (hi <= 1.125f * least + 1) break;      // a round more has nothing left to fill
+  int per = max(p.min_per, (int)fminf(ceilf(all.work / target), 1.0e9f));
+  if (!(all.tiles < p.rounds * target && all.work > 0)) return per;
+  float best = INFINITY;
+  for (int k = 1; k <= p.rounds; ++k) {
+    const float room = k * target;
+    if (all.tiles > room) continue;
+    const float least = fmaxf(ceilf(all.work / room), (float)p.min_per);
+    float lo = least, hi = fmaxf(lo, all.tiles < room ? fminf(all.longest, ceilf(all.work / (room - all.tiles))) : all.longest);
+    for (int i = 0; i < 6 && lo < hi; ++i) {
+      const float mid = floorf(0.5f * (lo + hi));
+      if (units_at((1.0f + 0x1p-21f) / mid) <= room) hi = mid;   // (never too few)
+      else lo = mid + 1;
     }
+    const float time = k * (hi + kStart);
+    if (time < best) {
+      best = time;
+      per = (int)hi;
+    }
+    if (hi <= 1.125f * least + 1) break;      // a round more has nothing left to fill
   }
-  r.per = __builtin_amdgcn_readfirstlane(r.per);
-  int units = 0, parts = 0, tiles = 0;
-  each([&](const SeqSize& s) {
-    const int count = (s.steps + r.per - 1) / r.per;
-    units += s.tiles * count;
-    parts += count > 1 ? s.tiles * count : 0;
-    tiles += s.tiles;
-  });
-  const int units_to = scan_lanes(units), parts_to = scan_lanes(parts), tiles_to = scan_lanes(tiles);
-  r.slots = __builtin_amdgcn_readlane(tiles_to, 63);
-  r.any = u < __builtin_amdgcn_readlane(units_to, 63);
-  if (!r.any) return r;
-  const int at = __builtin_amdgcn_readfirstlane((int)__ffsll((unsigned long long)__ballot(units_to > u)) - 1);
-  int left = u - __builtin_amdgcn_readlane(units_to - units, at);
-  int part0 = __builtin_amdgcn_readlane(parts_to - parts, at), slot = __builtin_amdgcn_readlane(tiles_to - tiles, at);
-  for (int b = at * run; b < c.seqs; ++b) {
-    SeqSize s;
-    if (b == at * run) {
-      s = {__builtin_amdgcn_readlane(mine.begin, at), __builtin_amdgcn_readlane(mine.n, at),
-           __builtin_amdgcn_readlane(mine.length, at), __builtin_amdgcn_readlane(mine.tiles, at),
-           __builtin_amdgcn_readlane(mine.steps, at)};
-    } else {
-      s = seq_size(c, p, b);
-    }
-    const int tiles_b = __builtin_amdgcn_readfirstlane(s.tiles);
-    const int count = __builtin_amdgcn_readfirstlane((s.steps + r.per - 1) / r.per);
-    if (left < tiles_b * count) {
-      // later rows see more positions and start first
-      const int k = left / count;
-      r.b = b;
-      r.begin = __builtin_amdgcn_readfirstlane(s.begin);
-      r.n = __builtin_amdgcn_readfirstlane(s.n);
-      r.length = __builtin_amdgcn_readfirstlane(s.length);
-      r.tile = tiles_b - 1 - k;
-      r.slot = slot + r.tile;
-      r.part = left - k * count;
-      r.count = count;
-      r.per = __builtin_amdgcn_readfirstlane((s.steps + count - 1) / count);   // parts of equal length
-      r.part0 = part0 + r.tile * count;
-      return r;
-    }
-    left -= tiles_b * count;
-    part0 += count > 1 ? tiles_b * count : 0;
-    slot += tiles_b;
+  return per;
+}
+
+__device__ __forceinline__ int parts_of(int steps, int per) { return (steps + per - 1) / per; }
+
+// Unit u of this head, for one wave (all 64 lanes call; the result is the same in all).
+__device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int u) {
+  const int lane = threadIdx.x & 63;
+  Unit r{};
+  r.slots = fp4impl::kNoLayout;
+  SeqSize s;
+  int left, part0, slot;         // u among the sequence's units; parts and tiles before the sequence
+  if (c.seqs <= fp4impl::kLaneSeqs) {
+    const SeqSize mine = lane < c.seqs ? seq_size(c, p, lane) : SeqSize{0, 0, 0, 0, 1};
+    const float tiles = (float)mine.tiles, steps = (float)mine.steps;
+    const Totals all{sum_lanes(tiles * steps), sum_lanes(tiles), max_lanes(mine.tiles > 0 ? steps : 0.0f)};
+    if (!fits(p, all)) return r;
+    r.per = __builtin_amdgcn_readfirstlane(
+        part_steps(p, all, [&](float inverse) { return sum_lanes(tiles * ceilf(steps * inverse)); }));
+    const int count = parts_of(mine.steps, r.per), units = mine.tiles * count, parts = count > 1 ? units : 0;
+    const int units_to = scan_lanes(units), parts_to = scan_lanes(parts), tiles_to = scan_lanes(mine.tiles);
+    r.slots = __builtin_amdgcn_readlane(tiles_to, 63);
+    r.any = u < __builtin_amdgcn_readlane(units_to, 63);
+    if (!r.any) return r;
+    r.b = __builtin_amdgcn_readfirstlane((int)__ffsll((unsigned long long)__ballot(units_to > u)) - 1);
+    s = {__builtin_amdgcn_readlane(mine.begin, r.b), __builtin_amdgcn_readlane(mine.n, r.b),
+         __builtin_amdgcn_readlane(mine.length, r.b), __builtin_amdgcn_readlane(mine.tiles, r.b),
+         __builtin_amdgcn_readlane(mine.steps, r.b)};
+    left = u - __builtin_amdgcn_readlane(units_to - units, r.b);
+    part0 = __builtin_amdgcn_readlane(parts_to - parts, r.b);
+    slot = __builtin_amdgcn_readlane(tiles_to - mine.tiles, r.b);
+  } else {
+    const int4 all = p.layout[c.seqs];
+    r.per = __builtin_amdgcn_readfirstlane(all.w);
+    r.slots = __builtin_amdgcn_readfirstlane(all.z);
+    r.any = u < __builtin_amdgcn_readfirstlane(all.x);
+    if (!r.any) return r;
+    r.b = __builtin_amdgcn_readfirstlane(last_at_most(c.seqs, u, [&](int b) { return p.layout[b].x; }));
+    const int4 before = p.layout[r.b];
+    left = u - __builtin_amdgcn_readfirstlane(before.x);
+    part0 = __builtin_amdgcn_readfirstlane(before.y);
+    slot = __builtin_amdgcn_readfirstlane(before.z);
+    const SeqSize mine = seq_size(c, p, r.b);
+    s = {__builtin_amdgcn_readfirstlane(mine.begin), __builtin_amdgcn_readfirstlane(mine.n),
+         __builtin_amdgcn_readfirstlane(mine.length), __builtin_amdgcn_readfirstlane(mine.tiles),
+         __builtin_amdgcn_readfirstlane(mine.steps)};
   }
-  r.any = false;
+  const int count = __builtin_amdgcn_readfirstlane(parts_of(s.steps, r.per)), k = left / count;
+  r.begin = s.begin;
+  r.n = s.n;
+  r.length = s.length;
+  r.tile = s.tiles - 1 - k;                     // later rows see more positions and start first
+  r.slot = slot + r.tile;
+  r.part = left - k * count;
+  r.count = count;
+  r.per = __builtin_amdgcn_readfirstlane(parts_of(s.steps, count));   // parts of equal length
+  r.part0 = part0 + r.tile * count;
   return r;
 }
 

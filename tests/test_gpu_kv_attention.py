@@ -214,3 +214,53 @@ def test_far_more_rows_than_positions(fmt):
     case = ref.Case(fmt, 1, 64, 16, [(2, 30)] + [(40, 1)] * 9, seed=10)
     q, q64 = queries(case, 4, torch.bfloat16)
     check(case, case.full_store(), q, q64)
+
+
+@pytest.mark.parametrize("fmt", [ref.NV, ref.MX])
+@pytest.mark.parametrize("B,most_rows,long", [(64, 1, 5000), (65, 1, 5000), (65, 80, 700), (130, 3, 2100), (1030, 1, 3000),
+                                             (2500, 2, 400)])
+def test_more_sequences_than_lanes(fmt, B, most_rows, long):
+    """Around and past the sequences that a wave lays out by itself: short ones, empty ones, one long one that is cut."""
+    announce(f"kv attention of {B} sequences, up to {most_rows} rows, one of {long}, fmt {fmt}")
+    rng = np.random.default_rng(B + most_rows)
+    seqs = [(int(rng.integers(0, 30)), int(rng.integers(most_rows // 3, most_rows + 1))) for _ in range(B)]
+    seqs[B // 2] = (long, most_rows)
+    seqs[0], seqs[B - 1] = (0, 1), (9, 0)
+    case = ref.Case(fmt, 1, 32, 16, seqs, seed=B, spare_rows=3)
+    store = case.full_store()
+    q, q64 = queries(case, 2, torch.bfloat16)
+    check(case, store, q, q64)
+    if B == 130:
+        check(case, store, q, q64, window=50)
+        check(case, store, q, q64, causal=False)
+
+
+def test_layout_of_many_sequences_in_a_graph():
+    announce("kv attention of 300 sequences, captured, replayed with other lengths")
+    case = ref.Case(ref.NV, 2, 64, 16, [(90, 1)] * 300, seed=5)
+    cache = gpu_cache(case, case.full_store())
+    q, _ = queries(case, 8, torch.bfloat16)
+    offsets, lengths, pages = tables(case)
+    fp4.kv_cache_attention(cache, q, offsets, lengths, pages)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = fp4.kv_cache_attention(cache, q, offsets, lengths, pages, return_lse=True)
+    rng = np.random.default_rng(6)
+    for _ in range(4):
+        lengths.copy_(i32(rng.integers(0, 91, 300)))
+        graph.replay()
+        want, wlse = fp4.kv_cache_attention(cache, q, offsets, lengths, pages, return_lse=True)
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("fmt", [ref.NV, ref.MX])
+def test_largest_factors_with_scores_of_zero(fmt):
+    """|scale| and q so large that their product is past float32, keys of 0: the mean of the values."""
+    announce(f"kv attention of scores of zero fmt {fmt}")
+    case = ref.Case(fmt, 1, 64, 16, [(70, 1), (100, 40)], seed=3, k_std=0.0)
+    store = case.full_store()
+    for dtype in (torch.bfloat16, torch.float32):
+        for group in (1, 4):
+            q = torch.full((case.T, group, 64), 2.0 ** 120, dtype=dtype, device=DEV)
+            check(case, store, q, q.double().cpu().numpy(), scale=2.0 ** 120)
