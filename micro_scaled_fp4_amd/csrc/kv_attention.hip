@@ -21,17 +21,17 @@ namespace {
 // Joins the parts of four rows of a tile that was cut.  Wave w finds the weights of row w's parts;
 // then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
 // sums meet in LDS.  The order of the parts is fixed, so the same call gives the same bits.
-// Bound by its launch and two chains of loads for few parts (4 us), by bytes for many (113 MB of
+// Bound by its launch and two chains of loads for few parts (4 us), by the bytes of many (113 MB of
 // parts read and 17 written in 41 us: 3.2 TB/s); holding all of a part's loads in registers halves the
 // waves (5 -> 12 us for 256 tiles of 4 parts).
 template <int DP>
-__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p) {
+__global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, int groups) {
   constexpr int kChunk = 256, kPer = DP / 64;
   typedef float fv __attribute__((ext_vector_type(kPer)));
   __shared__ float weight[4][kChunk], total[4];
   __shared__ __align__(16) float sums[4][4][DP];
   const TileParts* tiles = static_cast<const TileParts*>(p.tiles);
-  const int at = workgroup() >> 2;              // four workgroups a tile
+  const int at = workgroup() / groups, group = workgroup() % groups;     // `groups` workgroups a tile
   const int slot = at / c.heads, head = at % c.heads;
   if (slot >= p.max_slots) return;
   const int slots = tiles[p.max_slots].begin;
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float* const first = part_of(p, c.heads, head, t.part0, DP);
   const int64_t stride = part_of(p, c.heads, head, t.part0 + 1, DP) - first;
-  for (int q0 = 4 * (workgroup() & 3); q0 < t.rows; q0 += 16) {
+  for (int q0 = 4 * group; q0 < t.rows; q0 += 4 * groups) {
     float top = -INFINITY;
     for (int k = lane; k < t.count; k += 64) top = fmaxf(top, first[k * stride + 2 * (q0 + wave)]);
 #pragma unroll
@@ -114,8 +114,10 @@ __global__ void __launch_bounds__(kLayOutThreads) k_lay_out(KvCache c, UnitPlan 
   };
   auto sum = [&](float v) { return joined(sum_lanes(v), [](float x, float y) { return x + y; }); };
   Totals all{0, 0, 0};
+  float seen = 0;
   each([&](int, const SeqSize& s) {
     all.work += (float)s.tiles * (float)s.steps;
+    seen += seen_steps(p, s);
     all.tiles += (float)s.tiles;
     all.longest = fmaxf(all.longest, s.tiles > 0 ? (float)s.steps : 0.0f);
   });
@@ -124,9 +126,10 @@ __global__ void __launch_bounds__(kLayOutThreads) k_lay_out(KvCache c, UnitPlan 
     if (threadIdx.x == 0) p.layout[c.seqs] = {0, 0, fp4impl::kNoLayout, 1};
     return;
   }
-  const int per = part_steps(p, all, [&](float inverse) {
+  const float whole = p.turn > 1 ? whole_time(p, all) : whole_time(p, all, sum(seen));
+  const int per = part_steps(p, all, whole, [&](float inverse) {
     float units = 0;
-    each([&](int, const SeqSize& s) { units += (float)s.tiles * ceilf((float)s.steps * inverse); });
+    each([&](int, const SeqSize& s) { units += (float)s.tiles * parts_at((float)s.steps, inverse); });
     return sum(units);
   });
   int own[3] = {0, 0, 0}, to[3];
@@ -175,23 +178,29 @@ int tile_rows(int64_t T, int64_t seqs, int group, int dp, bool split) {
 int resident(int rows, int dp, bool split) {
   if (rows == 128) return dp == 256 ? 1 : 2;
   if (rows == 32) return dp == 64 ? 3 : 2;
-  return dp == 64 ? (split ? 3 : 4) : dp == 128 ? (split ? 2 : 3) : 1;
+  return dp == 64 ? 4 : dp == 128 ? (split ? 2 : 3) : 1;
 }
 
 UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool split) {
   UnitPlan p{};
   p.group = q_heads / heads;
   p.rows = tile_rows(T, seqs, p.group, dp, split);
-  // Parts of at least 8 steps (us of a call at 4, 8, 16; one token, 32 / 8 heads x 128, replayed): 300
-  // positions 11.1, 9.6, 9.6; 1000 11.3, 13.3, 13.8; 4096 12.3, 13.3, 16.9; 32 sequences of 1000
-  // 22.1, 19.5, 18.4; of 4096 38.6 each.
-  p.min_per = 8;
   p.target = std::max(1, resident(p.rows, dp, split) * fp4impl::num_cus() / heads);
-  // Few rows: 1, 2 or 3 rounds give 173, 165, 173 us for 128 sequences of 1000 to 16000 positions, 43, 41,
-  // 43 for 32 of 4096.  Prompts: whole tiles are long, and cutting them into up to 4 rounds levels a
-  // batch of unequal ones.
-  p.rounds = p.rows == 128 ? 4 : 2;
   p.max_slots = (int)(T * p.group / p.rows + seqs);
+  // Few rows: parts of 4 steps, one for each wave (one token, 32 / 8 heads x 128, replayed: 1000 positions 11.2
+  // us against 13.4 with parts of 8; 4096 12.2, 13.6; 16384, 64 parts of 4 or 32 of 8, 16.4, 14.6), joining
+  // them for 9 steps' time (32 sequences of 1000, not cut, 18.5 us; cut by a cost of 5 20.1; 1000 positions
+  // left whole by a cost of 14 15.0).  Where few tiles can be cut evenly one round is enough, and no
+  // workgroups wait for nothing; else 2 (1, 2, 3 rounds: 128 sequences of 1000 to 16000 173, 165, 173 us).
+  // Tiles of 128 rows: a round's parts are 34 MB to write and read, 14 steps' time (a prompt of 1024 whole
+  // 37 us, in two parts 54).  Up to 4 rounds level batches like two chunks over 16384 and 32768
+  // positions (uncut 520 steps, in 3 rounds 3 x 132).
+  const bool few = p.rows < 128;
+  p.min_per = few ? 4 : 8;
+  p.whole = 8;
+  p.turn = few ? 4 : 1;
+  p.join = few ? 9 : 14;
+  p.rounds = few ? (4 * p.max_slots <= p.target ? 1 : 2) : 4;
   p.max_parts = std::max(p.rounds, 2) * p.target + p.target / 8 + 8;
   return p;
 }
@@ -201,7 +210,10 @@ size_t tiles_bytes(const UnitPlan& p) { return (size_t)(p.max_slots + 1) * sizeo
 size_t layout_bytes(int64_t seqs) { return seqs > fp4impl::kLaneSeqs ? (size_t)(seqs + 1) * sizeof(int4) : 0; }
 
 // The most parts of a tile that the page table has positions for, and units of a head.
-int64_t most_parts(const KvCache& c, const UnitPlan& p) { return std::max((c.capacity / 64 + p.min_per) / p.min_per, 1); }
+int64_t most_parts(const KvCache& c, const UnitPlan& p) {
+  const int steps = (c.capacity + 63) / 64;
+  return steps <= p.whole ? 1 : (steps + p.min_per - 1) / p.min_per;
+}
 int64_t most_units(const KvCache& c, const UnitPlan& p) {
   return std::min(p.max_slots * most_parts(c, p),
                   std::max((int64_t)p.max_slots + p.target, (int64_t)p.rounds * p.target) + fp4impl::kSpareUnits);
@@ -234,8 +246,10 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, hipS
   if (c.mx) go(std::true_type{});
   else go(std::false_type{});
   if (most_parts(c, p) <= 1) return;
-  const dim3 grid = fp4impl::grid_of((int64_t)p.max_slots * c.heads * 4);
-  k_join_parts<DP><<<grid, 256, 0, stream>>>(c, a, p);
+  // (80 rows of 8 heads over 16 sequences: 6.0 us with 8 workgroups a tile of 32 rows, 7.3 with 4; tiles
+  // of 128 rows are bound by the parts' bytes: 264 of them in 2 parts 20 us with 4, 23 with 16)
+  const int groups = p.rows < 128 ? p.rows / 4 : 4;
+  k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * groups), 256, 0, stream>>>(c, a, p, groups);
 }
 
 }  // namespace

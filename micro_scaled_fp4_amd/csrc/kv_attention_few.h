@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   const int r16 = lane & 15, quad = lane >> 4;
   const int unit = workgroup() / c.heads, head = workgroup() % c.heads;
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
-  const Unit u = unit_of(c, p, unit);
+  const Unit u = unit_of<true>(c, p, unit);
   const int rows_end = min((u.tile + 1) * p.rows, u.n * p.group);
   if (head == 0) note_tile(p, u, unit, rows_end - u.tile * p.rows);
   if (!u.any || !has_room(p, u)) return;

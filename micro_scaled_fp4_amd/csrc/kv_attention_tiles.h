@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
   const int unit = workgroup() / c.heads, head = workgroup() % c.heads;
-  const Unit u = unit_of(c, p, unit);
+  const Unit u = unit_of<false>(c, p, unit);
   const int rows_end = min((u.tile + 1) * p.rows, u.n * p.group);
   const int rows = rows_end - u.tile * p.rows;
   if (head == 0) note_tile(p, u, unit, rows);

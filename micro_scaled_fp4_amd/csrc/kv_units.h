@@ -25,6 +25,9 @@ struct UnitPlan {
   int rows;                      // query rows of a tile (packed)
   int group;
   int min_per;                   // least steps of a part
+  int whole;                     // tiles of up to so many steps are never cut, if no tile has more
+  int turn;                      // steps that a workgroup takes at a time
+  int join;                      // what joining parts costs, in steps (tiles of 128 rows: for each round)
   int target;                    // parts per key/value head that fill the card
   int rounds;                    // at most that many rounds of such parts are looked at
   int max_slots, max_parts;      // most tiles, and most parts of cut tiles (per head)
@@ -128,39 +131,73 @@ struct Totals {
 // Whether the layout of so many tiles holds (false: offsets decrease).
 __device__ __forceinline__ bool fits(const UnitPlan& p, const Totals& all) { return all.tiles <= 1.01f * (float)p.max_slots; }
 
-// Steps of a part.  Parts of the same length run in rounds of `target`: the shortest length that
-// needs no more than k rounds, for the k with the least time (kStart steps for a part's beginning and
-// end).  units_at(inverse): all units of parts of 1 / inverse steps.
+// Parts of 1 / inverse steps each that `steps` steps make, inverse being 2^-21 too large: as many up to
+// 2^20 steps, never too few beyond.
+__device__ __forceinline__ float parts_at(float steps, float inverse) { return ceilf((steps - 0.5f) * inverse); }
+
+constexpr float kStart = 4;      // a part's beginning and end, in steps
+
+// Steps of all tiles of a sequence, about, as far as causal rows see: the first tile sees `least`, each
+// further one as many positions more as it has rows, up to s.steps.
+__device__ __forceinline__ float seen_steps(const UnitPlan& p, const SeqSize& s) {
+  const float tiles = (float)s.tiles, steps = (float)s.steps;
+  if (!p.causal) return tiles * steps;
+  const float rows = fmaxf((float)(p.rows / p.group), 1.0f);
+  const float least = fminf(fmaxf(((float)(s.length - s.n) + rows) * (1.0f / 64), 1.0f), steps);
+  return tiles * steps - 0.5f * (steps - least) * fminf(tiles, (steps - least) * 64 / rows);
+}
+
+// Time of all tiles without parts, in steps: whole rounds of the longest where tiles are alike.  Causal
+// tiles of a prompt are not: longest first, they fill each other's gaps, and the mean load of a workgroup
+// counts.  `seen` steps (the sum of seen_steps) say how far they differ.
+__device__ __forceinline__ float whole_time(const UnitPlan& p, const Totals& all) {
+  return ceilf(all.tiles / (float)p.target) * (all.longest + kStart);
+}
+__device__ __forceinline__ float whole_time(const UnitPlan& p, const Totals& all, float seen) {
+  const float alike = fmaxf(2 * seen / all.work - 1, 0.0f);
+  return alike * whole_time(p, all) +
+         (1 - alike) * fmaxf(all.longest + kStart, (seen + all.tiles * kStart) / (float)p.target);
+}
+
+// Steps of a part: a multiple of p.turn.  Parts of the same length run in rounds of `target`: the
+// shortest length that needs no more than k rounds, for the k with the least time, or no parts at all
+// (`whole`, whole_time).  Time in steps: kStart for a part, p.join for joining.  units_at(inverse): all
+// units of parts of 1 / inverse steps.
 template <typename UnitsAt>
-__device__ __forceinline__ int part_steps(const UnitPlan& p, const Totals& all, UnitsAt units_at) {
-  constexpr float kStart = 4;
-  const float target = (float)p.target;
-  int per = max(p.min_per, (int)fminf(ceilf(all.work / target), 1.0e9f));
-  if (!(all.tiles < p.rounds * target && all.work > 0)) return per;
-  float best = INFINITY;
+__device__ __forceinline__ int part_steps(const UnitPlan& p, const Totals& all, float whole, UnitsAt units_at) {
+  const float target = (float)p.target, turn = (float)p.turn;
+  if (!(all.tiles < p.rounds * target && all.longest > (float)p.whole)) return max(p.whole, (int)fminf(ceilf(all.work / target), 1.0e9f));
+  // (more than 32 parts of a tile: twice as long ones, since each is a step of the join's)
+  const float shortest = (float)(all.longest > 32.0f * (float)p.min_per ? p.whole : p.min_per);
+  float best = whole;
+  float per = all.longest;
   for (int k = 1; k <= p.rounds; ++k) {
     const float room = k * target;
     if (all.tiles > room) continue;
-    const float least = fmaxf(ceilf(all.work / room), (float)p.min_per);
-    float lo = least, hi = fmaxf(lo, all.tiles < room ? fminf(all.longest, ceilf(all.work / (room - all.tiles))) : all.longest);
+    const float least = fmaxf(ceilf(all.work / room), shortest);
+    // in turns
+    float lo = ceilf(least / turn);
+    float hi = fmaxf(lo, ceilf((all.tiles < room ? fminf(all.longest, ceilf(all.work / (room - all.tiles))) : all.longest) / turn));
     for (int i = 0; i < 6 && lo < hi; ++i) {
       const float mid = floorf(0.5f * (lo + hi));
-      if (units_at((1.0f + 0x1p-21f) / mid) <= room) hi = mid;   // (never too few)
+      if (units_at((1.0f + 0x1p-21f) / (mid * turn)) <= room) hi = mid;
       else lo = mid + 1;
     }
-    const float time = k * (hi + kStart);
+    const float time = k * (hi * turn + kStart) + (p.turn > 1 ? p.join : k * p.join);
     if (time < best) {
       best = time;
-      per = (int)hi;
+      per = hi * turn;
     }
-    if (hi <= 1.125f * least + 1) break;      // a round more has nothing left to fill
+    if (hi * turn <= 1.125f * least + 1) break;   // a round more has nothing left to fill
   }
-  return per;
+  return max((int)per, p.min_per);
 }
 
 __device__ __forceinline__ int parts_of(int steps, int per) { return (steps + per - 1) / per; }
 
-// Unit u of this head, for one wave (all 64 lanes call; the result is the same in all).
+// Unit u of this head, for one wave (all 64 lanes call; the result is the same in all).  ALIKE: a
+// sequence's tiles see the same steps, but for one or two (few rows).
+template <bool ALIKE>
 __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int u) {
   const int lane = threadIdx.x & 63;
   Unit r{};
@@ -172,8 +209,11 @@ __device__ __forceinline__ Unit unit_of(const KvCache& c, const UnitPlan& p, int
     const float tiles = (float)mine.tiles, steps = (float)mine.steps;
     const Totals all{sum_lanes(tiles * steps), sum_lanes(tiles), max_lanes(mine.tiles > 0 ? steps : 0.0f)};
     if (!fits(p, all)) return r;
+    float whole;
+    if constexpr (ALIKE) whole = whole_time(p, all);
+    else whole = whole_time(p, all, sum_lanes(seen_steps(p, mine)));
     r.per = __builtin_amdgcn_readfirstlane(
-        part_steps(p, all, [&](float inverse) { return sum_lanes(tiles * ceilf(steps * inverse)); }));
+        part_steps(p, all, whole, [&](float inverse) { return sum_lanes(tiles * parts_at(steps, inverse)); }));
     const int count = parts_of(mine.steps, r.per), units = mine.tiles * count, parts = count > 1 ? units : 0;
     const int units_to = scan_lanes(units), parts_to = scan_lanes(parts), tiles_to = scan_lanes(mine.tiles);
     r.slots = __builtin_amdgcn_readlane(tiles_to, 63);
