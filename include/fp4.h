@@ -566,7 +566,7 @@ fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows,
  * contents).  Offsets outside [0, T] and lengths outside [0, max_pages * page_size] are
  * clamped, so no memory outside the arrays is touched; offsets that decrease leave the
  * outputs unspecified.  0 <= B <= FP4_KV_MAX_SEQS, 0 <= T <= FP4_KV_MAX_ROWS, max_pages *
- * page_size <= 2^30, B * max_pages < 2^40, else FP4_ERR_SHAPE.
+ * page_size <= 2^30, else FP4_ERR_SHAPE.
  */
 #define FP4_KV_MAX_HEADS 1024
 #define FP4_KV_MAX_SEQS (1LL << 16)

@@ -162,11 +162,11 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Packed rows of a tile, by the mean of the sequences' rows.  16 sequences of 8192 positions, 8 heads, us:
 //   rows per head        16    32    64   128
-//   D 128, bf16: 16      41    60   110   184
-//                32      48    52    80   132
-//               128      87    90    98   114
-//   D 128, f32:  16      46    73   123   230   (32: 73, 78, 125, 235; 128: 121, 122, 134, 165)
-//   D 256, bf16: 16      87   139   259   499   (32: 280, 285, 469, 861; 128: 262, 269, 277, 295)
+//   D 128, bf16: 16      41    59   107   182
+//                32      48    51    81   134
+//               128      87    90    96   113
+//   D 128, f32:  16      46    73   125   231   (128: 128, 131, 142, 170)
+//   D 256, bf16: 16      88   140   261   503   (128: 269, 275, 284, 302; a 32-row kernel: 280, 285, 469, 861)
 // (float32 and 256 channels leave a SIMD one wave of the 32-row kernel).
 int tile_rows(int64_t T, int64_t seqs, int group, int dp, bool split) {
   const int64_t rows = T * group;
