@@ -162,8 +162,12 @@ __device__ __forceinline__ void store4(void* out, bool bf16, int64_t i, f32x4 v)
   }
 }
 
-// A part's results in the workspace: for each of its rows m and l, then the outputs [rows][DP]
-// as sums of P v, in the values' own unit.
+// 1 / l, by which a row's sums of P v are multiplied before the values' own unit is: P is up to 2^15, so the
+// sums times the unit, or the unit / l, may leave float32's range where the result does not.  0 where l is.
+__device__ __forceinline__ float inverse_of(float l) { return l > 0 ? 1.0f / l : 0.0f; }
+
+// A part's results in the workspace: for each of its rows m and l, then the outputs [rows][DP] of
+// its positions alone.
 __device__ __forceinline__ float* part_of(const UnitPlan& p, int heads, int head, int part, int dp) {
   return p.parts + ((int64_t)part * heads + head) * p.rows * (dp + 2);
 }

@@ -18,8 +18,8 @@ using fp4impl::UnitPlan;
 
 namespace {
 
-// Joins the parts of four rows of a tile that was cut.  Wave w finds the weights of row w's parts;
-// then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
+// Joins the parts of four rows of a tile that was cut: the mean of their outputs by their shares of the
+// row's sum.  Wave w finds the shares of row w's parts; then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
 // sums meet in LDS.  The order of the parts is fixed, so the same call gives the same bits.
 // Bound by its launch and two chains of loads for few parts (4 us), by the bytes of many (113 MB of
 // parts read and 17 written in 41 us: 3.2 TB/s); holding all of a part's loads in registers halves the
@@ -28,7 +28,7 @@ template <int DP>
 __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, int groups) {
   constexpr int kChunk = 256, kPer = DP / 64;
   typedef float fv __attribute__((ext_vector_type(kPer)));
-  __shared__ float weight[4][kChunk], total[4];
+  __shared__ float weight[4][kChunk];
   __shared__ __align__(16) float sums[4][4][DP];
   const TileParts* tiles = static_cast<const TileParts*>(p.tiles);
   const int at = workgroup() / groups, group = workgroup() % groups;     // `groups` workgroups a tile
@@ -41,21 +41,30 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
   const float* const first = part_of(p, c.heads, head, t.part0, DP);
   const int64_t stride = part_of(p, c.heads, head, t.part0 + 1, DP) - first;
   for (int q0 = 4 * group; q0 < t.rows; q0 += 4 * groups) {
-    float top = -INFINITY;
-    for (int k = lane; k < t.count; k += 64) top = fmaxf(top, first[k * stride + 2 * (q0 + wave)]);
+    // the row's maximum and sum, and of these each part's share
+    const float* const stats = first + 2 * (q0 + wave);
+    float mine = -INFINITY, l = 0;
+    for (int k = lane; k < t.count; k += 64) {
+      const float m = stats[k * stride], was = mine;
+      mine = fmaxf(was, m);
+      const float base = mine == -INFINITY ? 0.0f : mine;
+      l = l * __builtin_amdgcn_exp2f(was - base) + stats[k * stride + 1] * __builtin_amdgcn_exp2f(m - base);
+    }
+    float top = mine;
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
     const float base = top == -INFINITY ? 0.0f : top;
-    float l = 0;
+    l *= __builtin_amdgcn_exp2f(mine - base);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+    const float inverse = inverse_of(l);
     fv sum[4] = {};
     for (int k0 = 0; k0 < t.count; k0 += kChunk) {
       const int n = min(kChunk, t.count - k0);
       __syncthreads();
       for (int k = lane; k < n; k += 64) {
-        const float* left = first + (k0 + k) * stride + 2 * (q0 + wave);
-        const float w = __builtin_amdgcn_exp2f(left[0] - base);
-        weight[wave][k] = w;
-        l += left[1] * w;
+        const float* const left = stats + (k0 + k) * stride;
+        weight[wave][k] = left[1] * __builtin_amdgcn_exp2f(left[0] - base) * inverse;
       }
       __syncthreads();
       const float* const from = first + k0 * stride + 2 * p.rows + q0 * DP + lane * kPer;
@@ -66,22 +75,18 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
       }
     }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
-    if (lane == 0) total[wave] = l;
-#pragma unroll
     for (int r = 0; r < 4; ++r) *reinterpret_cast<fv*>(&sums[wave][r][lane * kPer]) = sum[r];
     __syncthreads();
     const int q = q0 + wave, rho = t.first_row + q, i = rho / p.group;
     if (q < t.rows) {
       const int64_t row = (int64_t)(t.begin + i) * a.q_heads + head * p.group + (rho - i * p.group);
-      const float inverse = total[wave] > 0 ? 1.0f / total[wave] : 0.0f;
       if (4 * lane < c.dim) {
         f32x4 v{0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][wave][4 * lane]);
-        store4(a.out, a.out_bf16, row * c.dim + 4 * lane, v * inverse);
+        store4(a.out, a.out_bf16, row * c.dim + 4 * lane, v);
       }
-      if (lane == 0 && a.lse != nullptr) a.lse[row] = row_lse(top, total[wave]);
+      if (lane == 0 && a.lse != nullptr) a.lse[row] = row_lse(top, l);
     }
     __syncthreads();
   }

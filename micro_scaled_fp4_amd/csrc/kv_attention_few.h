@@ -317,10 +317,11 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     __syncthreads();
     const float sum = sum_over_halves(sum_over_rows(l[g]));
     const float unit_of_v = MX ? __builtin_amdgcn_ldexpf(1.0f, v_ref - 140) : gv;
+    const float inverse = inverse_of(sum);
     float* const whole = reinterpret_cast<float*>(&tile[0][0]);        // [wave][16 rows][DP]
 #pragma unroll
     for (int d = 0; d < kGranules; ++d)
-      *reinterpret_cast<f32x4*>(whole + (wave * 16 + r16) * DP + 4 * ((4 * d + quad) ^ r16)) = acc[g][d] * unit_of_v;
+      *reinterpret_cast<f32x4*>(whole + (wave * 16 + r16) * DP + 4 * ((4 * d + quad) ^ r16)) = acc[g][d] * inverse * unit_of_v;
     if (quad == 0) {
       stats[wave][r16][0] = m[g];
       stats[wave][r16][1] = sum;
@@ -333,11 +334,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     for (int w = 0; w < 4; ++w) top = fmaxf(top, stats[w][q][0]);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      part[w] = __builtin_amdgcn_exp2f(stats[w][q][0] - (top == -INFINITY ? 0.0f : top));
-      total += stats[w][q][1] * part[w];
+      part[w] = stats[w][q][1] * __builtin_amdgcn_exp2f(stats[w][q][0] - (top == -INFINITY ? 0.0f : top));
+      total += part[w];
     }
+    const float of_total = inverse_of(total);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) part[w] *= of_total;
     float* const left = u.count > 1 ? part_of(p, c.heads, head, u.part0 + u.part, DP) : nullptr;
-    const float inverse = total > 0 ? 1.0f / total : 0.0f;
     const int64_t o = (out.r * a.q_heads + out.h) * c.dim;
 #pragma unroll
     for (int j = 0; j < DP / 64; ++j) {
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
 #pragma unroll
       for (int w = 0; w < 4; ++w) sumv += *reinterpret_cast<const f32x4*>(whole + (w * 16 + q) * DP + 4 * (chunk ^ q)) * part[w];
       if (left != nullptr) *reinterpret_cast<f32x4*>(left + 2 * p.rows + (16 * g + q) * DP + 4 * chunk) = sumv;
-      else store4(a.out, a.out_bf16, o + 4 * chunk, sumv * inverse);
+      else store4(a.out, a.out_bf16, o + 4 * chunk, sumv);
     }
     if (c16 == 0) {
       if (left != nullptr) {

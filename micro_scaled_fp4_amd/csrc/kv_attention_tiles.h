@@ -259,14 +259,14 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   if (row.h < 0) return;
   const int q = 32 * wave + r32;
   float* const left = u.count > 1 ? part_of(p, c.heads, head, u.part0 + u.part, DP) : nullptr;
-  const float f = left != nullptr ? unit_of_v : l > 0 ? unit_of_v / l : 0.0f;
+  const float inverse = inverse_of(l);
   const int64_t o = (row.r * a.q_heads + row.h) * c.dim;
 #pragma unroll
   for (int d = 0; d < kBlocks; ++d) {
     if (32 * d >= c.dim) break;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const f32x4 v = f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * f;
+      const f32x4 v = f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * inverse * unit_of_v;
       const int channel = 32 * d + 8 * e + 4 * half;
       if (left != nullptr) *reinterpret_cast<f32x4*>(left + 2 * p.rows + q * DP + channel) = v;
       else store4(a.out, a.out_bf16, o + channel, v);
