@@ -232,7 +232,9 @@ struct AttendProblem {
   int64_t q_stride;
   bool q_bf16, out_bf16;
   int q_heads;
-  float scale;
+  bool negative;                 // scale < 0
+  float mantissa;                // |scale| log2(e) = mantissa 2^exponent, mantissa in [0.72, 1.45) or 0
+  int exponent;
   bool causal;
   int window;                    // 0: none
   void* out;

@@ -24,6 +24,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fp4_device.h"
 #include "fp4_internal.h"
 #include "kv_units.h"
@@ -36,7 +38,7 @@ using fp4impl::AttendProblem;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightBits = 11.0f;            // P is 2^11 at m
 constexpr float kGrowth = 4.0f;                 // a maximum within m + kGrowth leaves m as it is
 
@@ -132,15 +134,29 @@ __device__ __forceinline__ void load8(const void* q, int64_t i, float (&v)[8]) {
   }
 }
 
-// The power of two that brings a row of maximum `top` into [2^14, 2^15), and its inverse.
-__device__ __forceinline__ void row_factors(float top, float& f, float& inverse) {
+// The power of two that brings a row of maximum `top` into [2^14, 2^15), and the exponent of its inverse.
+__device__ __forceinline__ void row_factors(float top, float& f, int& inverse) {
   const int e = max((int)(__float_as_uint(top) >> 23), 15);
   f = __uint_as_float((uint32_t)(268 - e) << 23);
-  inverse = __uint_as_float((uint32_t)(e - 14) << 23);
+  inverse = e - 141;
 }
 
-// A row's factor c, kept from 0 and infinity, whose products with -inf (a masked position) and 0 are NaN.
-__device__ __forceinline__ float in_range(float c) { return fminf(fmaxf(c, 1e-37f), 3e38f); }
+// A row's factor c is |scale| log2(e) (mantissa 2^exponent in AttendProblem) x q's factor's inverse x the keys' (NVFP4: their
+// tensor scale; MXFP4: a step's reference).  Products of some of them may leave float32's range where c does
+// not, so it is put together from exponents and rounded once.
+
+// What a lane keeps of its row's c: c itself, or (MXFP4, where the keys' reference joins in each step) an exponent.
+template <bool MX>
+using RowScale = std::conditional_t<MX, int, float>;
+
+// c = mantissa 2^exponent, kept from 0 and infinity, whose products with -inf (a masked position) and 0 are
+// NaN.  (Scores are sums of fp16 products, below 2^40: c of 1e-37 makes them 0.)
+__device__ __forceinline__ float row_factor(float mantissa, int exponent) {
+  return fminf(fmaxf(__builtin_amdgcn_ldexpf(mantissa, exponent), 1e-37f), 3e38f);
+}
+__device__ __forceinline__ float row_factor_nv(const AttendProblem& a, int inverse, float gk) {
+  return row_factor(a.mantissa * __builtin_amdgcn_frexp_mantf(gk), a.exponent + inverse + __builtin_amdgcn_frexp_expf(gk));
+}
 
 // Two fp16 parts of eight float32 values (hi + lo, 22 bits); lo is left out where !SPLIT.
 template <bool SPLIT>

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   if (t0 < sp.t1) load(t0);
 
   f16x8 qh[R][kDwords], ql[R][SPLIT ? kDwords : 1];
-  float factor[R];                              // c: scores -> base-2 exponents
+  RowScale<MX> factor[R];                       // c: scores -> base-2 exponents (MX: its exponent but for the keys')
   QueryRow row[R];
 #pragma unroll
   for (int g = 0; g < R; ++g) {
@@ -172,10 +172,12 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = umax(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
     }
-    float f, inverse;
+    float f;
+    int inverse;
     row_factors(max_over_halves(max_over_rows(__uint_as_float(top))), f, inverse);
-    factor[g] = in_range(fabsf(a.scale) * kLog2e * inverse * gk);
-    if (a.scale < 0) f = -f;
+    if constexpr (MX) factor[g] = a.exponent + inverse - 140;
+    else factor[g] = row_factor_nv(a, inverse, gk);
+    if (a.negative) f = -f;
 #pragma unroll
     for (int i = 0; i < kDwords; ++i) {
 #pragma unroll
@@ -241,7 +243,9 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     f16x8 ph[R][2], pl[R][SPLIT ? 2 : 1];
 #pragma unroll
     for (int g = 0; g < R; ++g) {
-      const float cf = MX ? in_range(__builtin_amdgcn_ldexpf(factor[g], k_ref - 140)) : factor[g];
+      float cf;
+      if constexpr (MX) cf = row_factor(a.mantissa, factor[g] + k_ref);
+      else cf = factor[g];
       if (now.holes != 0 || __any(t0 + 63 > row[g].last || t0 < row[g].first)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
   const float gk = MX ? 1.0f : nv_global_scale(*c.k_amax), gv = MX ? 1.0f : nv_global_scale(*c.v_amax);
   const QueryRow row = query_row(u, p, head, u.tile * p.rows + 32 * wave + r32, rows_end, sp.t1);
   f16x8 qh[kSteps], ql[SPLIT ? kSteps : 1];
-  float factor;
+  RowScale<MX> factor;                          // c: scores -> base-2 exponents (MX: its exponent but for the keys')
   {
     uint32_t top = 0;
     float v[8];
@@ -133,10 +133,12 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = umax(top, __float_as_uint(v[j]) & 0x7fffffffu);
     }
-    float f, inverse;
+    float f;
+    int inverse;
     row_factors(max_over_halves(__uint_as_float(top)), f, inverse);
-    factor = in_range(fabsf(a.scale) * kLog2e * inverse * gk);
-    if (a.scale < 0) f = -f;
+    if constexpr (MX) factor = a.exponent + inverse - 140;
+    else factor = row_factor_nv(a, inverse, gk);
+    if (a.negative) f = -f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       read(i);
@@ -190,7 +192,9 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     take_tops(round - 1);
     f32x16 s[2];
     scores(k_now, s);
-    const float cf = MX ? in_range(__builtin_amdgcn_ldexpf(factor, k_ref - 140)) : factor;
+    float cf;
+    if constexpr (MX) cf = row_factor(a.mantissa, factor + k_ref);
+    else cf = factor;
     if ((holes & 15u) != 0 || __any(t0 + 63 > row.last || t0 < row.first)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
