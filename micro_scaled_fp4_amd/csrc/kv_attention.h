@@ -41,6 +41,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightBits = 11.0f;            // P is 2^11 at m
 constexpr float kGrowth = 4.0f;                 // a maximum within m + kGrowth leaves m as it is
+// Up to this |m| a score's exponent is c s - m rounded once: m itself, rounded, is off by 2^-3 at most, and P
+// stays below 2^15.2.  Past it the products are rounded as m was and then m is taken off, which is exact for
+// the largest (elsewhere P would pass fp16, or be 0, from |m| = 2^28 on).
+constexpr float kExactSteps = 0x1p22f;
 
 // The larger of v in lanes l and l ^ 32, or l and l ^ 16.
 __device__ __forceinline__ float max_over_halves(float v) {

@@ -265,12 +265,21 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
       m[g] = next_max(was, top * cf);
       const float base = m[g] == -INFINITY ? 0.0f : m[g];
       const float drop = __builtin_amdgcn_exp2f(was - base);
+      float shift = kWeightBits - base;
+      if (__any(fabsf(base) > kExactSteps)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[g][i][e] = s[g][i][e] * cf - base;
+        cf = 1;
+        shift = kWeightBits;
+      }
       float sum = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g][i][e], cf, kWeightBits - base));
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g][i][e], cf, shift));
           sum += w;
           const _Float16 h = (_Float16)w;
           ph[g][i >> 1][4 * (i & 1) + e] = h;

@@ -213,6 +213,15 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     m = next_max(was, max_over_halves(top) * cf);
     const float base = m == -INFINITY ? 0.0f : m;
     const float drop = __builtin_amdgcn_exp2f(was - base);
+    float shift = kWeightBits - base;
+    if (__any(fabsf(base) > kExactSteps)) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[b][e] = s[b][e] * cf - base;
+      cf = 1;
+      shift = kWeightBits;
+    }
     const float keep = MX ? __builtin_amdgcn_ldexpf(drop, v_ref - v_top) : drop;
     if (__any(keep != 1.0f)) {
       l *= drop;
@@ -226,7 +235,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], cf, kWeightBits - base));
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], cf, shift));
         sum += w;
         const _Float16 h = (_Float16)w;
         ph[2 * b + (e >> 3)][e & 7] = h;
