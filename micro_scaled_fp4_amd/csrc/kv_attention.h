@@ -183,8 +183,9 @@ __device__ __forceinline__ void store4(void* out, bool bf16, int64_t i, f32x4 v)
 }
 
 // 1 / l, by which a row's sums of P v are multiplied before the values' own unit is: P is up to 2^15, so the
-// sums times the unit, or the unit / l, may leave float32's range where the result does not.  0 where l is.
-__device__ __forceinline__ float inverse_of(float l) { return l > 0 ? 1.0f / l : 0.0f; }
+// sums times the unit, or the unit / l, may leave float32's range where the result does not.  0 where l is
+// (nothing was seen), NaN where l is.
+__device__ __forceinline__ float inverse_of(float l) { return l == 0 ? 0.0f : 1.0f / l; }
 
 // A part's results in the workspace: for each of its rows m and l, then the outputs [rows][DP] of
 // its positions alone.
@@ -195,9 +196,9 @@ __device__ __forceinline__ float* part_of(const UnitPlan& p, int heads, int head
 // The reference of a row's weights after a step whose largest exponent is `top`.
 __device__ __forceinline__ float next_max(float m, float top) { return top > m + kGrowth ? top : m; }
 
-// lse of a row with running maximum m and sum l.
+// lse of a row with running maximum m and sum l: -inf where it saw nothing, NaN where l is.
 __device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0 ? (m + __builtin_amdgcn_logf(l) - kWeightBits) * kLn2 : -INFINITY;
+  return l == 0 ? -INFINITY : (m + __builtin_amdgcn_logf(l) - kWeightBits) * kLn2;
 }
 
 // Whether the parts of u's tile have room in the workspace (always, unless offsets decrease).
