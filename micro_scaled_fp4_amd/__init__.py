@@ -776,7 +776,9 @@ class KVCache:
     page_size, head_dim / 2], k_scales, v_scales u8 [num_pages, num_heads, page_size,
     head_dim / bs] and, for NVFP4, the given amax of all keys and of all values (a float or a
     one-element tensor; float32[1] on the device afterwards).  page_size is a power of two
-    from 16 on, head_dim a multiple of 32 up to 256.  The tensors are used in place."""
+    from 16 on, head_dim a multiple of 32 up to 256.  The tensors are used in place, and the calls
+    know their addresses: they are changed in place (`cache.k_amax.copy_(a)`), never replaced; a
+    larger cache is a KVCache of its own."""
 
     __slots__ = ("fmt", "num_pages", "num_heads", "page_size", "head_dim", "device", "k_codes", "k_scales",
                  "v_codes", "v_scales", "k_amax", "v_amax", "_struct", "_address")
@@ -812,6 +814,14 @@ class KVCache:
         self._struct = _KVCacheStruct(fmt, heads, dim, page, pages, _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
                                       _ptr(v_scales), _ptr(self.k_amax), _ptr(self.v_amax))
         self._address = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_address"):
+            raise AttributeError(f"{name} of a KVCache cannot be replaced: change it in place, or make another cache")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a KVCache cannot be deleted")
 
     @classmethod
     def empty(cls, fmt: int, num_pages: int, num_heads: int, page_size: int, head_dim: int, k_amax=None,
