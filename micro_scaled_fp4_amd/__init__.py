@@ -872,6 +872,11 @@ def _head_rows(t: torch.Tensor, heads: Optional[int], dim: int, dev, name: str):
     return t, token
 
 
+def _out_type(out_dtype: Optional[torch.dtype], out: torch.Tensor) -> None:
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+
+
 def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
                    lengths: torch.Tensor, pages: torch.Tensor) -> None:
     """Quantizes k and v [T, num_heads, head_dim] bf16/f32 into their positions: rows offsets[b] ..
@@ -890,10 +895,10 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, offsets: to
 
 
 def kv_cache_read(cache: KVCache, offsets: torch.Tensor, lengths: torch.Tensor, pages: torch.Tensor, rows: int,
-                  starts: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16, out=None):
+                  starts: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, out=None):
     """(k, v) [rows, num_heads, head_dim]: row offsets[b] + i holds position starts[b] + i of sequence b
     (without starts: its last rows), zeros outside [0, lengths[b]) and in holes.  Rows past offsets[B] are not
-    written.  out: (k, v) to write into."""
+    written.  out_dtype: bfloat16 unless given; out: (k, v) to write into, of out_dtype if both are given."""
     dev = cache.device
     B, offsets, lengths, pages, wide = _sequences(cache, offsets, lengths, pages)
     if starts is not None:
@@ -901,7 +906,8 @@ def kv_cache_read(cache: KVCache, offsets: torch.Tensor, lengths: torch.Tensor, 
         starts = _typed(starts, torch.int32, (B,), "starts")
     shape = (int(rows), cache.num_heads, cache.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+        out = [torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=dev) for _ in range(2)]
+    _out_type(out_dtype, out[0])
     for t in out:
         if tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev or t.dtype != out[0].dtype:
             raise ValueError(f"out must be two contiguous {shape} tensors of one type on {dev}")
@@ -917,10 +923,10 @@ def kv_cache_attention(cache: KVCache, q: torch.Tensor, offsets: torch.Tensor, l
                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Attention of q [T, num_q_heads, head_dim] bf16/f32 over the cached positions of each row's sequence
     (query head h over key/value head h // (num_q_heads / num_heads)): out [T, num_q_heads, head_dim]
-    (out_dtype: q's unless given) or, with return_lse, (out, lse float32 [T, num_q_heads]).  Row i of n sits at
-    position lengths[b] - n + i and sees the positions up to its own (causal) and after its own minus window
-    (window > 0); 0 and -inf where it sees none.  scale: 1 / sqrt(head_dim) unless given.  Rows past offsets[B]
-    are not written."""
+    (out_dtype: out's or q's unless given) or, with return_lse, (out, lse float32 [T, num_q_heads]).  Row i of n
+    sits at position lengths[b] - n + i and sees the positions up to its own (causal) and after its own minus
+    window (window > 0); 0 and -inf where it sees none.  scale: 1 / sqrt(head_dim) unless given.  Rows past
+    offsets[B] are not written."""
     dev = cache.device
     q, qs = _head_rows(q, None, cache.head_dim, dev, "q")
     T, heads = q.shape[0], q.shape[1]
@@ -931,6 +937,7 @@ def kv_cache_attention(cache: KVCache, q: torch.Tensor, offsets: torch.Tensor, l
         out = torch.empty(T, heads, cache.head_dim, dtype=out_dtype or q.dtype, device=dev)
     elif tuple(out.shape) != tuple(q.shape) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be contiguous {tuple(q.shape)} on {dev}")
+    _out_type(out_dtype, out)
     lse = torch.empty(T, heads, dtype=torch.float32, device=dev) if return_lse else None
     lib = load_library()
     if workspace is None:
