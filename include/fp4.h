@@ -626,8 +626,8 @@ fp4_status kv_cache_read(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
  *   scale     |scale| <= 2^120; window >= 0, and 0 unless causal is set
  *   out       [T, num_q_heads, head_dim] FP4_F32 or FP4_BF16
  *   lse       out float32 [T, num_q_heads], or NULL
- *   workspace >= kv_cache_attention_workspace_bytes bytes, 16-byte aligned; its contents
- *             matter only within the call
+ *   workspace >= kv_cache_attention_workspace_bytes bytes (0 for sizes that the call
+ *             refuses), 16-byte aligned; its contents matter only within the call
  * Scores, softmax and sums are float32: a row with a score (times log2(e)) past float32's
  * range gets NaN in out and lse, as one with a NaN in q does, and scores below it count as
  * not seen.  With bf16 q and out the softmax weights meet the values as fp16 (half a step:

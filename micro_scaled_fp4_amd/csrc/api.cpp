@@ -675,19 +675,25 @@ fp4_status moe_combine_backward(const void* dy, fp4_dtype dyt, const void* rows,
 
 namespace {
 
+bool kv_sizes_ok(const fp4_kv_cache* c, int64_t T, int64_t B) {
+  return c->num_heads >= 1 && c->num_heads <= FP4_KV_MAX_HEADS && c->head_dim >= 32 && c->head_dim <= 256 &&
+         c->head_dim % 32 == 0 && c->page_size >= 16 && c->page_size <= 65536 &&
+         (c->page_size & (c->page_size - 1)) == 0 && c->num_pages >= 0 && c->num_pages < (int64_t)1 << 31 &&
+         T >= 0 && T <= FP4_KV_MAX_ROWS && B >= 0 && B <= FP4_KV_MAX_SEQS;
+}
+
+bool query_heads_ok(const fp4_kv_cache* c, int64_t T, int num_q_heads) {
+  return num_q_heads >= 1 && num_q_heads <= 1 << 16 && num_q_heads % c->num_heads == 0 &&
+         T * num_q_heads <= (int64_t)1 << 30;
+}
+
 // Checks of what the three cache calls share; *none: there is nothing to do.
 fp4_status check_kv(const fp4_kv_cache* c, int64_t T, int64_t B, const int32_t* offsets, const int32_t* lengths,
                     const int32_t* pages, int64_t max_pages, bool* none) {
   *none = false;
   if (c == nullptr) return FP4_ERR_NULL;
   if (c->format != FP4_NVFP4 && c->format != FP4_MXFP4) return FP4_ERR_DTYPE;
-  if (c->num_heads < 1 || c->num_heads > FP4_KV_MAX_HEADS || c->head_dim < 32 || c->head_dim > 256 ||
-      c->head_dim % 32 != 0 || c->page_size < 16 || c->page_size > 65536 ||
-      (c->page_size & (c->page_size - 1)) != 0 || c->num_pages < 0 || c->num_pages >= (int64_t)1 << 31)
-    return FP4_ERR_SHAPE;
-  if (T < 0 || T > FP4_KV_MAX_ROWS || B < 0 || B > FP4_KV_MAX_SEQS || max_pages < 0 ||
-      max_pages > ((int64_t)1 << 30) / c->page_size)
-    return FP4_ERR_SHAPE;
+  if (!kv_sizes_ok(c, T, B) || max_pages < 0 || max_pages > ((int64_t)1 << 30) / c->page_size) return FP4_ERR_SHAPE;
   const bool mx = c->format == FP4_MXFP4;
   if (mx && (c->k_amax != nullptr || c->v_amax != nullptr)) return FP4_ERR_DTYPE;
   *none = T == 0 || B == 0;
@@ -753,9 +759,8 @@ fp4_status kv_cache_read(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
 
 size_t kv_cache_attention_workspace_bytes(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
                                           int num_q_heads) {
-  if (cache == nullptr || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 ||
-      num_q_heads > 1 << 16 || T < 1 || T > FP4_KV_MAX_ROWS || num_seqs < 1 || num_seqs > FP4_KV_MAX_SEQS ||
-      cache->head_dim < 32 || cache->head_dim > 256)
+  if (cache == nullptr || T < 1 || num_seqs < 1 || !kv_sizes_ok(cache, T, num_seqs) ||
+      !query_heads_ok(cache, T, num_q_heads))
     return 0;
   return fp4impl::kv_attention_workspace_bytes(T, num_seqs, num_q_heads, cache->num_heads, cache->head_dim);
 }
@@ -770,8 +775,7 @@ fp4_status kv_cache_attention(const fp4_kv_cache* cache, const void* q, int64_t 
   bool none;
   fp4_status st = check_kv(cache, T, num_seqs, offsets, lengths, pages, max_pages, &none);
   if (st != FP4_OK) return st;
-  if (num_q_heads < 1 || num_q_heads > 1 << 16 || num_q_heads % cache->num_heads != 0 ||
-      T * num_q_heads > (int64_t)1 << 30 || q_stride < 0 || q_stride > (int64_t)1 << 32 || window < 0 ||
+  if (!query_heads_ok(cache, T, num_q_heads) || q_stride < 0 || q_stride > (int64_t)1 << 32 || window < 0 ||
       (window > 0 && !causal) || !(std::fabs(scale) <= 0x1p120f))
     return FP4_ERR_SHAPE;
   if (none) return FP4_OK;
