@@ -816,12 +816,14 @@ class KVCache:
         self._address = ctypes.addressof(self._struct)
 
     def __setattr__(self, name, value):
-        if hasattr(self, "_address"):
+        if name in KVCache.__slots__ and hasattr(self, "_address"):
             raise AttributeError(f"{name} of a KVCache cannot be replaced: change it in place, or make another cache")
         object.__setattr__(self, name, value)
 
     def __delattr__(self, name):
-        raise AttributeError(f"{name} of a KVCache cannot be deleted")
+        if name in KVCache.__slots__:
+            raise AttributeError(f"{name} of a KVCache cannot be deleted")
+        object.__delattr__(self, name)
 
     @classmethod
     def empty(cls, fmt: int, num_pages: int, num_heads: int, page_size: int, head_dim: int, k_amax=None,

@@ -10,14 +10,13 @@ from test_gpu_kv_attention import check
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("power", [18, 21, 23, 25, 26, 29, 60, 110])
+@pytest.mark.parametrize("D,power", [(64, p) for p in (18, 21, 23, 25, 26, 29, 60, 110)] + [(128, 24), (128, 30), (256, 24), (256, 30)])
 @pytest.mark.parametrize("fmt", [ref.NV, ref.MX])
-def test_the_largest_score_takes_all(fmt, power):
+def test_the_largest_score_takes_all(fmt, D, power):
     """Constant keys of 1, 2 and 4 beside one of 8 (negative scores: 2, 4 and 8 beside one of 1): the
     loudest score is ahead by half of itself (negative ones: by itself), more than 2^14, so the other weights are 0 and the output
     is that position's value.  Its weight cancels but for its rounding to fp16 (2^-11; in two parts 2^-20)."""
-    announce(f"kv attention scores of 2^{power} fmt {fmt}")
-    D = 64
+    announce(f"kv attention scores of 2^{power} fmt {fmt} D {D}")
     for seqs, places in (([(300, 1), (70, 1)], (0, 150, 299)), ([(1500, 1)], (0, 1499)), ([(400, 12)], (380,)), ([(200, 130)], (60,)),
                          ([(90, 90)], (0,))):
         for at in places:

@@ -1,4 +1,5 @@
 """A KVCache's fields cannot be replaced: the library reads the addresses that it was made with."""
+import copy
 import ctypes
 import os
 
@@ -28,3 +29,24 @@ def test_fields_are_not_replaced(name):
     with pytest.raises(AttributeError):
         delattr(c, name)
     assert getattr(c, name) is before
+
+
+@pytest.mark.skipif(not os.path.exists(m.LIB_PATH), reason="libfp4.so not built")
+def test_copies_and_subclasses():
+    c = made()
+    other = copy.copy(c)
+    assert all(getattr(other, name) is getattr(c, name) for name in m.KVCache.__slots__)
+    with pytest.raises(AttributeError):
+        other.k_codes = 0
+
+    class Named(m.KVCache):
+        pass
+
+    n = Named.__new__(Named)
+    for name in m.KVCache.__slots__:
+        setattr(n, name, getattr(c, name))
+    n.layer = 3
+    n.layer = 4
+    del n.layer
+    with pytest.raises(AttributeError):
+        n.v_codes = 0
