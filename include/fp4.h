@@ -631,10 +631,14 @@ fp4_status kv_cache_read(const fp4_kv_cache* cache, int64_t T, int64_t num_seqs,
  * Scores, softmax and sums are float32: a row with a score (times log2(e)) past float32's
  * range gets NaN in out and lse, as one with a NaN in q does, and scores below it count as
  * not seen.  With bf16 q and out the softmax weights meet the values as fp16 (half a step:
- * 2^-12 of a weight); float32 operands are split into two fp16 parts.  MXFP4: a key or value
- * below 2^-36 of the largest scale among the 64 positions around it (values: among the
- * positions so far) may count as 0.  The same call gives the same bits every time.  Bytes of
- * positions that no row of the call sees are not looked at.
+ * 2^-12 of a weight); float32 operands are split into two fp16 parts.  Channels of a query
+ * row are held to 2^-38 of its largest.  MXFP4: a key or value below 2^-36 of the largest
+ * scale among the 64 positions around it (values: among the positions so far), whether the
+ * row sees that position or another row of the call, may count as 0.  The same call gives
+ * the same bits every time; a sequence's last bits may differ with the other sequences of
+ * the call, which share the choice of tiles and parts.  Bytes of positions that no row of
+ * the call sees are not looked at; a NaN scale (no quantizer writes one) at a position that
+ * some rows see may reach others.
  * num_q_heads a multiple of num_heads up to 2^16, T * num_q_heads <= 2^30, else
  * FP4_ERR_SHAPE.
  */

@@ -21,8 +21,8 @@ namespace {
 // Joins the parts of four rows of a tile that was cut: the mean of their outputs by their shares of the
 // row's sum.  Wave w finds the shares of row w's parts; then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
 // sums meet in LDS.  The order of the parts is fixed, so the same call gives the same bits.
-// Bound by its launch and two chains of loads for few parts (4 us), by the bytes of many (113 MB of
-// parts read and 17 written in 41 us: 3.2 TB/s); holding all of a part's loads in registers halves the
+// Bound by its launch and two chains of loads for few parts (4.6 us), by the bytes of many (113 MB of
+// parts read and 17 written in 39 us: 3.3 TB/s); holding all of a part's loads in registers halves the
 // waves (5 -> 12 us for 256 tiles of 4 parts).
 template <int DP>
 __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, UnitPlan p, int groups) {
@@ -94,8 +94,9 @@ __global__ void __launch_bounds__(256) k_join_parts(KvCache c, AttendProblem a, 
 
 // Lays more than kLaneSeqs sequences out, for unit_of: one workgroup, each thread a run of them.  Bound by
 // its launch and chains of loads; with it one token each of 65, 128, 256, 512 and 4096 sequences of 1000
-// positions (8 heads x 128) takes 39, 49, 80, 151 and 1027 us, laid out by every wave for itself 34, 48,
-// 88, 208 and 5704.
+// positions (8 heads x 128) takes 39, 50, 85, 154 and 1046 us, laid out by every wave for itself, in an
+// earlier state, 34, 48, 88, 208 and 5704.  (So both cost the same near 128; a lane for each sequence
+// ends at 64.)
 constexpr int kLayOutThreads = 1024, kLayOutWaves = kLayOutThreads / 64;
 __global__ void __launch_bounds__(kLayOutThreads) k_lay_out(KvCache c, UnitPlan p) {
   __shared__ float sums[kLayOutWaves];
@@ -179,7 +180,8 @@ int tile_rows(int64_t T, int64_t seqs, int group, int dp, bool split) {
   return rows <= 16 * seqs || dp == 256 || split ? 16 : 32;
 }
 
-// Workgroups that a compute unit holds, by their registers and LDS (a wave of each on each SIMD).
+// Workgroups that a compute unit holds, by their registers and LDS (a wave of each on each SIMD).  (Tiles of 128
+// rows of 64 channels would fit three times but for MXFP4 in float32; rounds are planned for two.)
 int resident(int rows, int dp, bool split) {
   if (rows == 128) return dp == 256 ? 1 : 2;
   if (rows == 32) return dp == 64 ? 3 : 2;
@@ -193,8 +195,8 @@ UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool s
   p.target = std::max(1, resident(p.rows, dp, split) * fp4impl::num_cus() / heads);
   p.max_slots = (int)(T * p.group / p.rows + seqs);
   // Few rows: parts of 4 steps, one for each wave (one token, 32 / 8 heads x 128, replayed: 1000 positions 11.2
-  // us against 13.4 with parts of 8; 4096 12.2, 13.6; 16384, 64 parts of 4 or 32 of 8, 16.4, 14.6), joining
-  // them for 9 steps' time (32 sequences of 1000, not cut, 18.5 us; cut by a cost of 5 20.1; 1000 positions
+  // us against 13.4 with parts of 8; 4096 12.2, 13.6; 16384, 64 parts of 4 or 32 of 8, 16.4, 14.6; with a
+  // join 0.3 us shorter than now), joining them for 9 steps' time (32 sequences of 1000, not cut, 18.5 us; cut by a cost of 5 20.1; 1000 positions
   // left whole by a cost of 14 15.0).  Where few tiles can be cut evenly one round is enough, and no
   // workgroups wait for nothing; else 2 (1, 2, 3 rounds: 128 sequences of 1000 to 16000 173, 165, 173 us).
   // Tiles of 128 rows: a round's parts are 34 MB to write and read, 14 steps' time (a prompt of 1024 whole
@@ -251,7 +253,7 @@ void launch_dp(const KvCache& c, const AttendProblem& a, const UnitPlan& p, hipS
   if (c.mx) go(std::true_type{});
   else go(std::false_type{});
   if (most_parts(c, p) <= 1) return;
-  // (80 rows of 8 heads over 16 sequences: 6.0 us with 8 workgroups a tile of 32 rows, 7.3 with 4; tiles
+  // (25 rows of 8 heads over each of 16 sequences: 6.0 us with 8 workgroups a tile of 32 rows, 7.3 with 4; tiles
   // of 128 rows are bound by the parts' bytes: 264 of them in 2 parts 20 us with 4, 23 with 16)
   const int groups = p.rows < 128 ? p.rows / 4 : 4;
   k_join_parts<DP><<<fp4impl::grid_of((int64_t)p.max_slots * c.heads * groups), 256, 0, stream>>>(c, a, p, groups);

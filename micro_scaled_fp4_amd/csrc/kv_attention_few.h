@@ -9,12 +9,13 @@
 // loaded while this one is computed.
 //
 // Bound by HBM bytes where contexts are long: 1000000 positions, 8 heads x 128, 4 query heads
-// each: 228 us NVFP4, 216 us MXFP4 with the join of the parts (5.06 and 5.05 TB/s), 64 sequences of
-// 16384: 252 us (4.8 TB/s).  R = 2 is bound by vector instructions, half of them for its two
-// softmaxes: 80 packed rows of 8 heads x 128 over 16 sequences of 5750 positions 36 us (2.7 TB/s).
-// Short contexts pay the chain of a part: 2.6 us until its unit is known, 1.9 the first loads, 2.0 a
-// step, 0.8 the join of the waves (1000 positions: 11 us in all).  Unrolling over two steps
-// needs more registers than two waves a SIMD leave (32 sequences, 51 -> 61 us).
+// each: 227 us NVFP4, 214 us MXFP4 with the join of the parts (5.08 and 5.07 TB/s), 64 sequences of
+// 16384 with 8 query heads each 247 us (4.9 TB/s).  R = 2 is bound by waits: 25 packed rows of 8 heads x 128
+// over 16 sequences of 2500 to 9001 positions 36 us (2.6 TB/s), vector units 39% and matrix units 10%
+// busy; its waves, 1.4 a SIMD on average, wait 40% of their cycles.  Short contexts pay the chain of a part:
+// 2.6 us until its unit is known, 1.9 the first loads, 2.0 a step, 0.8 the join of the waves (1000
+// positions, a step a wave: 9 us).  Unrolling over two steps needs more registers than two waves a SIMD
+// leave (32 sequences, 51 -> 61 us).
 #pragma once
 
 #include "kv_attention.h"
@@ -88,7 +89,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 // Granule (32 bytes: 16 channels) of row t of a [.][DP] fp16 tile in LDS: rows that a transposed
-// read takes together fall on different banks.
+// read takes together fall on different granules.  (Stores do conflict: all lanes of one write the same half of
+// their granules, so half of the banks.  Conflicts are 35% of the LDS cycles here and 40% in the tiles of
+// 128 rows, where waves wait for LDS 7% of their cycles.)
 template <int DP>
 __device__ __forceinline__ int v_granule(int t, int g) { return DP == 64 ? g ^ ((t >> 1) & 3) : g ^ (t & 7); }
 

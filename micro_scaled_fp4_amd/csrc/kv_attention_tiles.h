@@ -6,13 +6,17 @@
 // step.  Codes are loaded two steps ahead.
 //
 // Bound by the matrix and the vector instructions together: of a step at 128 channels a wave
-// issues 32 MFMAs (about 1040 cycles) and 265 vector instructions (about 1300: half for the
+// issues 32 MFMAs (about 1040 cycles) and 270 vector instructions (about 1350: half for the
 // softmax, a quarter for its share of the dequantizing), and the two waves of a SIMD hardly overlap
-// them (the cycles of both add up to 98% of the time).  A causal prompt of 16384, 32 / 8 heads x
-// 128: 2230 us NVFP4 (985 TFLOP/s), 2200 us MXFP4 (1000); 64 channels 693, 256 channels 571 TFLOP/s
-// (sums and q fill 192 registers: one wave a SIMD).  At the same prompt, 64 rows a wave at one wave a
-// SIMD reached 722 TFLOP/s, eight waves over 256 rows 970, the next step's scores beside this
-// step's weights 930, raised wave priorities 2% less.
+// them (matrix units 43%, vector units 57% busy).  Causal prompts of 16384, TFLOP/s:
+//                                    bf16: NVFP4  MXFP4   float32: NVFP4  MXFP4
+//   32 / 8 heads x 64                    808      802          497      477
+//   32 / 8 heads x 128                   957      972          562      591
+//   8 / 4 heads x 256                    561      514          370      347
+// 256 channels: sums and q fill 192 registers, one wave a SIMD; in float32, whose two parts of q and P make
+// twice the MFMAs, 35 to 37 more registers spill.  In an earlier state (985 TFLOP/s at the prompt of
+// 128 channels), 64 rows a wave at one wave a SIMD reached 722, eight waves over 256 rows 970, the next
+// step's scores beside this step's weights 930, raised wave priorities 2% less.
 #pragma once
 
 #include <type_traits>
