@@ -790,7 +790,8 @@ fp4_status kv_cache_attention(const fp4_kv_cache* cache, const void* q, int64_t 
   int exponent;
   const float mantissa = (float)(std::frexp(std::fabs((double)scale), &exponent) * 1.4426950408889634);
   const fp4impl::AttendProblem p{q, q_stride, qt == FP4_BF16, ot == FP4_BF16, num_q_heads, scale < 0, mantissa,
-                                 exponent, causal != 0, (int)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30), out, lse, workspace};
+                                 exponent, causal != 0, (int)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30),
+                                 out, lse, workspace};
   FP4_TRY_LAUNCH(fp4impl::launch_kv_attention(kv_of(cache, T, num_seqs, offsets, lengths, pages, max_pages), p,
                                               stream),
                  "kv_cache_attention");

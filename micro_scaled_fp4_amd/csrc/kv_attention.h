@@ -145,9 +145,9 @@ __device__ __forceinline__ void row_factors(float top, float& f, int& inverse) {
   inverse = e - 141;
 }
 
-// A row's factor c is |scale| log2(e) (mantissa 2^exponent in AttendProblem) x q's factor's inverse x the keys' (NVFP4: their
-// tensor scale; MXFP4: a step's reference).  Products of some of them may leave float32's range where c does
-// not, so it is put together from exponents and rounded once.
+// A row's factor c is |scale| log2(e) (mantissa 2^exponent in AttendProblem) x the inverse of q's factor x
+// the keys' (NVFP4: their tensor scale; MXFP4: a step's reference).  Products of some of them may leave
+// float32's range where c does not, so it is put together from exponents and rounded once.
 
 // What a lane keeps of its row's c: c itself, or (MXFP4, where the keys' reference joins in each step) an exponent.
 template <bool MX>
@@ -193,8 +193,9 @@ __device__ __forceinline__ float* part_of(const UnitPlan& p, int heads, int head
   return p.parts + ((int64_t)part * heads + head) * p.rows * (dp + 2);
 }
 
-// The reference of a row's weights after a step whose largest exponent is `top`.
-__device__ __forceinline__ float next_max(float m, float top) { return top > m + kGrowth ? top : m; }
+// The reference of a row's weights after a step whose largest exponent is `top`.  (The difference: m + kGrowth
+// may round up to `top` where float32's steps are 8.  Where both are -inf it is NaN, and m stays.)
+__device__ __forceinline__ float next_max(float m, float top) { return top - m > kGrowth ? top : m; }
 
 // lse of a row with running maximum m and sum l: -inf where it saw nothing, NaN where l is.
 __device__ __forceinline__ float row_lse(float m, float l) {

@@ -19,8 +19,8 @@ using fp4impl::UnitPlan;
 namespace {
 
 // Joins the parts of four rows of a tile that was cut: the mean of their outputs by their shares of the
-// row's sum.  Wave w finds the shares of row w's parts; then each wave sums every fourth part's four rows, a lane DP / 64 channels, and the waves'
-// sums meet in LDS.  The order of the parts is fixed, so the same call gives the same bits.
+// row's sum.  Wave w finds the shares of row w's parts; then each wave sums every fourth part's four
+// rows, a lane DP / 64 channels, and the waves' sums meet in LDS.  The order of the parts is fixed, so the same call gives the same bits.
 // Bound by its launch and two chains of loads for few parts (4.6 us), by the bytes of many (113 MB of
 // parts read and 17 written in 39 us: 3.3 TB/s); holding all of a part's loads in registers halves the
 // waves (5 -> 12 us for 256 tiles of 4 parts).
@@ -196,8 +196,8 @@ UnitPlan plan_of(int64_t T, int64_t seqs, int q_heads, int heads, int dp, bool s
   p.max_slots = (int)(T * p.group / p.rows + seqs);
   // Few rows: parts of 4 steps, one for each wave (one token, 32 / 8 heads x 128, replayed: 1000 positions 11.2
   // us against 13.4 with parts of 8; 4096 12.2, 13.6; 16384, 64 parts of 4 or 32 of 8, 16.4, 14.6; with a
-  // join 0.3 us shorter than now), joining them for 9 steps' time (32 sequences of 1000, not cut, 18.5 us; cut by a cost of 5 20.1; 1000 positions
-  // left whole by a cost of 14 15.0).  Where few tiles can be cut evenly one round is enough, and no
+  // join 0.3 us shorter than now), joining them for 9 steps' time (32 sequences of 1000, not cut, 18.5 us; cut by a cost
+  // of 5 20.1; 1000 positions left whole by a cost of 14 15.0).  Where few tiles can be cut evenly one round is enough, and no
   // workgroups wait for nothing; else 2 (1, 2, 3 rounds: 128 sequences of 1000 to 16000 173, 165, 173 us).
   // Tiles of 128 rows: a round's parts are 34 MB to write and read, 14 steps' time (a prompt of 1024 whole
   // 37 us, in two parts 54).  Up to 4 rounds level batches like two chunks over 16384 and 32768

@@ -39,3 +39,38 @@ def test_the_largest_score_takes_all(fmt, D, power):
                         want = case.held(store, b, 1)[0][min(at, int(case.lengths[b]) - 1), 0]
                         off = np.abs(got[lo:hi].double().cpu().numpy() - want)
                         assert (off <= near * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("fmt", [ref.NV, ref.MX])
+def test_a_maximum_that_grows_by_a_float32_step(fmt, steps):
+    """Scores (times log2(e)) of 2^26 + 8 and 8 `steps` above it, exact, the float32 step being 8 there: the weights
+    are as 1 to 2^(8 steps), whichever comes first, in the same wave's steps."""
+    announce(f"kv attention maximum grown by {steps} steps of 8 at 2^26, fmt {fmt}")
+    D = 64
+    for seqs in ([(400, 1)], [(400, 12)], [(400, 70)]):
+        for first, second in ((3, 290), (290, 3)):
+            case = ref.Case(fmt, 1, D, 16, seqs, seed=steps)
+            k = case.k[0]
+            k[:] = 0
+            # <q, k> = 2^23 + 1 and 2^23 + 1 + steps, in bits of 1, 2, 4, 8 and 16
+            k[first, 0, [0, 8]] = 1.0
+            k[second, 0, 0] = 1.0
+            k[[first, second], 0, 15] = 1.5     # 6 x the block's scale, which is 1/4 then (q is 0 there)
+            for bit in range(5):
+                k[second, 0, 8 + bit] = float((1 + steps) >> bit & 1)
+            case.k_amax = np.float32(2688.0 / 4)        # NVFP4: a tensor scale of 1/4
+            store = case.full_store()
+            held = case.held(store, 0, 0)[0]
+            assert np.array_equal(held[:, 0], k[:, 0])
+            for dtype in (torch.bfloat16, torch.float32):
+                q = torch.zeros(case.T, 2, D, dtype=dtype, device=DEV)
+                q[:, :, 0] = 2.0 ** 23
+                for bit in range(5):
+                    q[:, :, 8 + bit] = 2.0 ** bit
+                got, _ = check(case, store, q, q.double().cpu().numpy(), scale=float(np.float32(8 * np.log(2.0))))
+                v = case.held(store, 0, 1)[0][:, 0]
+                small = 2.0 ** (-8 * steps)
+                want, size = (v[second] + small * v[first]) / (1 + small), (np.abs(v[second]) + small * np.abs(v[first])) / (1 + small)
+                near = 2.0 ** -11 + 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -19
+                assert (np.abs(got.double().cpu().numpy() - want) <= near * size + 2.0 ** -24 * np.abs(v).max()).all()
